@@ -16,6 +16,11 @@
  *                                   modulation of the new residual
  *   nr_silu_and_mul                 silu(gate) * up
  *   nr_gelu_and_mul                 gelu_tanh(gate) * up
+ *   nr_kv_cache_write               K and V quantised into a paged cache
+ *   nr_qk_norm_rope_cache           nr_qk_norm_rope_ex with K and V going into it
+ *   nr_kv_cache_read                sequences of the cache read back
+ *   nr_group_norm                   group norm, channels last, optional SiLU
+ *   nr_group_norm_backward          its gradient
  *
  * Conventions shared by every entry point
  *   - Pointers are DEVICE pointers (CUDA global memory) owned by the caller; the
@@ -208,6 +213,156 @@ nr_status nr_qk_norm_rope_ex(void* q_out, void* k_out, const void* q, const void
                              int64_t head_dim, int64_t q_tok_stride, int64_t k_tok_stride,
                              float eps, int gemma, const nr_rope_config* rope, nr_dtype dtype,
                              cudaStream_t stream);
+
+/*
+ * A paged K/V cache in 8 or 4 bits.  Place t % block_size of block b holds one
+ * token of every head (one slot, numbered b * block_size + place):
+ *   codes   bytes [blocks, block_size, heads, head_dim]       NR_CACHE_FP8
+ *           bytes [blocks, block_size, heads, head_dim / 2]   NR_CACHE_MXFP4
+ *   scales  f32   [blocks, block_size, heads]                 NR_CACHE_FP8
+ *           bytes [blocks, block_size, heads, head_dim / 32]  NR_CACHE_MXFP4
+ * of K and of V alike.  Inside a block the layout is contiguous; blocks may be
+ * further apart (K and V as halves of one allocation), by the strides below.
+ * With a the largest magnitude of the head row (FP8) or of 32 consecutive
+ * elements (MXFP4), taken as at least 2^-100 and at most the largest f32:
+ *   FP8    scale = a / 448,  code_j = e4m3(x_j * (448 / a)), each quotient and
+ *          the product rounded to f32; the value held is code * scale
+ *   MXFP4  (OCP microscaling, e2m1 elements, e8m0 scales) s the least integer
+ *          with a / 2^s <= 6, scale byte s + 127, code_j = e2m1(x_j / 2^s), the
+ *          even element in the low nibble; the value held is code * 2^s
+ * Codes are rounded to nearest even.  A NaN stays NaN in e4m3 and spoils no
+ * other element; e2m1 has no NaN (it becomes +-6).
+ *   code_block_stride    bytes between blocks of codes: at least block_size *
+ *                        heads * (code bytes of a head), a multiple of 16
+ *   scale_block_stride   bytes between blocks of scales: at least those of one
+ *                        block, a multiple of 4 for NR_CACHE_FP8
+ * Code pointers are 16-byte aligned; scale pointers 4-byte (FP8) or not at all.
+ * blocks, block_size, heads >= 1; heads * head_dim <= 2^24.  head_dim is a
+ * multiple of 16 (FP8) or 32 (MXFP4), at most 512.
+ */
+typedef enum nr_cache_format { NR_CACHE_FP8 = 0, NR_CACHE_MXFP4 = 1 } nr_cache_format;
+
+typedef struct nr_kv_cache {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  int64_t blocks;
+  int64_t block_size;
+  int64_t heads;
+  int64_t head_dim;
+  int64_t code_block_stride;
+  int64_t scale_block_stride;
+  nr_cache_format format;
+} nr_kv_cache;
+
+/*
+ * Quantises the K and V of new tokens into their slots.
+ *
+ * k, v     [tokens, heads, head_dim], dtype `dtype`, heads contiguous in a token;
+ *          k_tok_stride / v_tok_stride elements between tokens, a multiple of 16
+ *          bytes.
+ * slots    [tokens] int64, device memory (8-byte aligned).  A token whose slot
+ *          is outside [0, blocks * block_size) is padding: nothing is written
+ *          for it and its k and v may hold anything.  The slots of one call are
+ *          distinct; a slot given twice holds a mixture of its tokens.
+ * Other slots keep what they held.  tokens * heads < 2^31.
+ * Errors: as nr_rmsnorm.
+ */
+nr_status nr_kv_cache_write(const nr_kv_cache* cache, const void* k, const void* v,
+                            const int64_t* slots, int64_t tokens, int64_t k_tok_stride,
+                            int64_t v_tok_stride, nr_dtype dtype, cudaStream_t stream);
+
+/*
+ * The attention preamble: nr_qk_norm_rope_ex of q into q_out, and of k into the
+ * cache beside the plain v.  K is quantised from its normed and rotated f32
+ * value, with no rounding to `dtype` in between.
+ *
+ * q_out, q    [tokens, hq, head_dim], q_tok_stride apart; q_out may be q.
+ * k, v        [tokens, heads, head_dim] (heads and head_dim of the cache).
+ * slots       as nr_kv_cache_write; q_out is written for padding too.
+ * wq, wk, positions, eps, gemma, rope: as nr_qk_norm_rope_ex.
+ * head_dim    bf16: 64, 128, 256 or 512; f32: 32, 64, 128 or 256.  With
+ *             NR_CACHE_MXFP4 a multiple of 64, and so is rotary_dim for
+ *             rotate-half pairs.
+ * Errors: as nr_rmsnorm; nr_device_status as nr_qk_norm_rope.
+ */
+nr_status nr_qk_norm_rope_cache(const nr_kv_cache* cache, void* q_out, const void* q,
+                                const void* k, const void* v, const void* wq, const void* wk,
+                                nr_dtype w_dtype, const int32_t* positions, const int64_t* slots,
+                                int64_t tokens, int64_t hq, int64_t q_tok_stride,
+                                int64_t k_tok_stride, int64_t v_tok_stride, float eps, int gemma,
+                                const nr_rope_config* rope, nr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Reads sequences back: row cu_seqlens[s] + t of k_out and v_out is token t of
+ * sequence s, the values held rounded to `dtype`.
+ *
+ * k_out, v_out   [rows, heads, head_dim] contiguous, dtype `dtype`.
+ * block_table    [seqs, table_width] int32, device memory: block t / block_size
+ *                of sequence s.  A row whose block is past the table or outside
+ *                [0, blocks) reads as zeros.
+ * cu_seqlens     [seqs + 1] int32, device memory, not decreasing.  Rows before
+ *                cu_seqlens[0], from cu_seqlens[seqs] on, and past `rows` are left
+ *                as they were.
+ * rows >= 0, seqs >= 0, table_width >= 0; rows and seqs < 2^31.
+ * Errors: as nr_rmsnorm.
+ */
+nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
+                           const int32_t* block_table, int64_t table_width,
+                           const int32_t* cu_seqlens, int64_t seqs, int64_t rows, nr_dtype dtype,
+                           cudaStream_t stream);
+
+/*
+ * Group norm over channels-last tensors, with an optional activation.
+ *
+ * x is [samples, space, channels], channels contiguous; group g has channels
+ * [g * cpg, (g + 1) * cpg), cpg = channels / groups.  Per sample and group, over its
+ * space * cpg values (f32 statistics):
+ *     mean, var (biased);  rstd = 1 / sqrt(var + eps)
+ *     out = round(act((x - mean) * rstd * w_c + b_c)),  act the identity or silu
+ *
+ * out, x      dtype `dtype`; out may be x.
+ * mean, rstd  [samples, groups] f32, written (the backward pass reads them).
+ * w, b        [channels], dtype `w_dtype`; both NULL: w = 1, b = 0.
+ * workspace   device memory of at least nr_group_norm_workspace bytes, not
+ *             initialised, its contents lost.  Calls that may run at the same
+ *             time need workspaces of their own.
+ * samples >= 0, space >= 0, groups >= 1 dividing channels; channels a multiple of
+ * 8 (bf16) or 4 (f32).  With no elements nothing is written.
+ * eps finite >= 0.
+ * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
+ */
+typedef enum nr_activation { NR_ACT_NONE = 0, NR_ACT_SILU = 1 } nr_activation;
+
+nr_status nr_group_norm(void* out, float* mean, float* rstd, const void* x, const void* w,
+                        const void* b, nr_dtype w_dtype, int64_t samples, int64_t space,
+                        int64_t channels, int64_t groups, float eps, nr_activation act,
+                        nr_dtype dtype, void* workspace, int64_t workspace_bytes,
+                        cudaStream_t stream);
+
+/*
+ * Gradient of nr_group_norm: with z = xhat w_c + b_c and dz = dy act'(z),
+ *     db_c = sum dz,  dw_c = sum dz xhat   (over samples and space)
+ *     dx = round(rstd (w_c dz - mean_g(w dz) - xhat mean_g(w dz xhat)))
+ * Sums are formed in a fixed order (the same inputs give the same bits).
+ *
+ * dx, dy, x   [samples, space, channels], dtype `dtype`; dx may be dy or x.
+ * dw, db      [channels], dtype `w_dtype`; NULL when w is NULL.
+ * mean, rstd  as nr_group_norm wrote them for x.
+ * Other arguments, the workspace and errors: as nr_group_norm.
+ */
+nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, const void* x,
+                                 const float* mean, const float* rstd, const void* w,
+                                 const void* b, nr_dtype w_dtype, int64_t samples, int64_t space,
+                                 int64_t channels, int64_t groups, nr_activation act,
+                                 nr_dtype dtype, void* workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* Workspace bytes of either direction, into *bytes.  Errors: NR_ERR_NULL and the
+ * size errors of nr_group_norm. */
+nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channels,
+                                  int64_t groups, nr_dtype dtype, int64_t* bytes);
 
 /*
  * LayerNorm (no affine) fused with adaLN modulation.

@@ -19,6 +19,13 @@ or ``__graft_entry__.build()``).
     gelu_and_mul(x, out=None)
     gated_residual_ln_modulate(residual, y, gate, shift, scale, eps=1e-6,
                                rows_per_sample=None, out=None)
+    kv_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, rows=None,
+                  dtype=torch.bfloat16, k_out=None, v_out=None)
+    qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_scale, v_scale,
+                       ..., q_out=None)
+    group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, stats=False)
+    group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=None)
 """
 from __future__ import annotations
 
@@ -71,6 +78,36 @@ lib.nr_silu_and_mul.argtypes = [_vp, _vp, _i64, _i64, _int, _vp]
 lib.nr_silu_and_mul.restype = _int
 lib.nr_gelu_and_mul.argtypes = [_vp, _vp, _i64, _i64, _int, _vp]
 lib.nr_gelu_and_mul.restype = _int
+
+
+class KvCache(ctypes.Structure):
+    """Mirror of nr_kv_cache (include/nr.h)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("blocks", ctypes.c_int64), ("block_size", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("code_block_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64),
+                ("format", ctypes.c_int)]
+
+
+lib.nr_kv_cache_write.argtypes = [ctypes.POINTER(KvCache), _vp, _vp, _vp, _i64, _i64, _i64, _int,
+                                  _vp]
+lib.nr_kv_cache_write.restype = _int
+lib.nr_qk_norm_rope_cache.argtypes = [ctypes.POINTER(KvCache), _vp, _vp, _vp, _vp, _vp, _vp, _int,
+                                      _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _int,
+                                      ctypes.POINTER(RopeConfig), _int, _vp]
+lib.nr_qk_norm_rope_cache.restype = _int
+lib.nr_kv_cache_read.argtypes = [_vp, _vp, ctypes.POINTER(KvCache), _vp, _i64, _vp, _i64, _i64,
+                                 _int, _vp]
+lib.nr_kv_cache_read.restype = _int
+lib.nr_group_norm.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _i64, _f32,
+                              _int, _int, _vp, _i64, _vp]
+lib.nr_group_norm.restype = _int
+lib.nr_group_norm_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64,
+                                       _i64, _i64, _i64, _int, _int, _vp, _i64, _vp]
+lib.nr_group_norm_backward.restype = _int
+lib.nr_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.POINTER(_i64)]
+lib.nr_group_norm_workspace.restype = _int
 lib.nr_device_status.argtypes = [_vp]
 lib.nr_device_status.restype = _int
 lib.nr_test_wait_probe.argtypes = [_i64, _vp]
@@ -84,8 +121,14 @@ lib.nr_version.restype = _int
 
 NR_F32 = 0
 NR_BF16 = 1
+NR_CACHE_FP8 = 0
+NR_CACHE_MXFP4 = 1
+NR_ACT_NONE = 0
+NR_ACT_SILU = 1
 ENTRY_POINTS = ("nr_rmsnorm", "nr_rmsnorm_quant_fp8", "nr_qk_norm_rope", "nr_qk_norm_rope_ex", "nr_ln_modulate",
                 "nr_silu_and_mul", "nr_gelu_and_mul", "nr_gated_residual_ln_modulate",
+                "nr_kv_cache_write", "nr_qk_norm_rope_cache", "nr_kv_cache_read",
+                "nr_group_norm", "nr_group_norm_backward", "nr_group_norm_workspace",
                 "nr_device_status", "nr_test_wait_probe",
                 "nr_status_string", "nr_last_error_message", "nr_version")
 
@@ -291,6 +334,15 @@ def qk_norm_rope_ex(q, k, wq, wk, positions, eps=1e-6, gemma=False, rotary_dim=N
         q_out = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty_strided(k.shape, k.stride(), dtype=k.dtype, device=k.device)
+    cfg = _rope_config(rotary_dim, interleaved, theta, llama3, mrope_sections, mrope_interleaved)
+    _check(lib.nr_qk_norm_rope_ex(_ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
+                                  _dtype_code(wq), _ptr(positions), q.shape[0], q.shape[1],
+                                  k.shape[1], q.shape[2], q.stride(0), k.stride(0), float(eps),
+                                  int(bool(gemma)), ctypes.byref(cfg), _dtype_code(q), _stream(q)))
+    return q_out, k_out
+
+
+def _rope_config(rotary_dim, interleaved, theta, llama3, mrope_sections, mrope_interleaved):
     cfg = RopeConfig()
     cfg.rotary_dim = 0 if rotary_dim is None else int(rotary_dim)
     cfg.interleaved = int(bool(interleaved))
@@ -302,11 +354,318 @@ def qk_norm_rope_ex(q, k, wq, wk, positions, eps=1e-6, gemma=False, rotary_dim=N
     if mrope_sections is not None:
         for i, v in enumerate(mrope_sections):
             cfg.mrope_section[i] = int(v)
-    _check(lib.nr_qk_norm_rope_ex(_ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
-                                  _dtype_code(wq), _ptr(positions), q.shape[0], q.shape[1],
-                                  k.shape[1], q.shape[2], q.stride(0), k.stride(0), float(eps),
-                                  int(bool(gemma)), ctypes.byref(cfg), _dtype_code(q), _stream(q)))
-    return q_out, k_out
+    return cfg
+
+
+# Checked argument layouts of the calls below.  What the checks look at (types,
+# shapes, strides, devices and options, no addresses and no values) is the key,
+# so a layout that passed once costs one look-up; what they found is the entry.
+_checked = {}
+_CHECKED_MOST = 4096
+
+
+def _layout(*ts):
+    return tuple([None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+                  for t in ts])
+
+
+def _remember(key, entry):
+    if key is not None:
+        if len(_checked) >= _CHECKED_MOST:
+            _checked.clear()
+        _checked[key] = entry
+    return entry
+
+
+def _known(*key_and_tensors):
+    """(key, entry or None) of a call; no key for what is not a tensor (the
+    checks then say so)."""
+    name, options, ts = key_and_tensors
+    try:
+        key = (name, options, _layout(*ts))
+        return key, _checked.get(key)
+    except (AttributeError, TypeError, RuntimeError):
+        return None, None
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _launch(device, fn, *args):
+    """fn(*args, the device's current stream) with `device` the current one: the
+    library launches on the current device, and a default stream does not say
+    which device it is of."""
+    if device == torch.cuda.current_device():
+        _check(fn(*args, _raw_stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _raw_stream(device)))
+
+
+def _block_strided(t, name):
+    """The stride between blocks of a cache tensor whose blocks are contiguous."""
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError("%s must be contiguous inside a block" % name)
+        inner *= size
+    if t.shape[0] > 1 and t.stride(0) < inner:
+        raise ValueError("the blocks of %s overlap" % name)
+    return t.stride(0) if t.shape[0] > 1 else inner
+
+
+def _cache_layout(k_cache, v_cache, k_scale, v_scale):
+    """The fields of KvCache behind its pointers, for four tensors: codes [blocks, block_size, heads, width] uint8
+    and scales float32 [blocks, block_size, heads] (fp8, width = head_dim) or
+    uint8 [blocks, block_size, heads, head_dim / 32] (mxfp4, width = head_dim / 2)."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"),
+                    (v_scale, "v_scale")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor" % name)
+    if k_cache.dtype != torch.uint8 or k_cache.dim() != 4:
+        raise TypeError("k_cache must be uint8 codes [blocks, block_size, heads, width]")
+    blocks, page, heads, width = k_cache.shape
+    if k_scale.dtype == torch.float32:
+        fmt, dim, scales = NR_CACHE_FP8, width, (blocks, page, heads)
+    elif k_scale.dtype == torch.uint8:
+        fmt, dim, scales = NR_CACHE_MXFP4, 2 * width, (blocks, page, heads, width // 16)
+    else:
+        raise TypeError("k_scale must be float32 (fp8) or uint8 (mxfp4), got %s" % k_scale.dtype)
+    _expect(v_cache, "v_cache", torch.uint8, k_cache.shape, contiguous=False)
+    _expect(k_scale, "k_scale", k_scale.dtype, scales, contiguous=False)
+    _expect(v_scale, "v_scale", k_scale.dtype, scales, contiguous=False)
+    code = _block_strided(k_cache, "k_cache")
+    scale = _block_strided(k_scale, "k_scale")
+    if _block_strided(v_cache, "v_cache") != code or _block_strided(v_scale, "v_scale") != scale:
+        raise ValueError("the K and V parts of the cache must have the same block strides")
+    return blocks, page, heads, dim, code, scale * k_scale.element_size(), fmt
+
+
+def _kv_cache(layout, k_cache, v_cache, k_scale, v_scale):
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   *layout)
+
+
+def _check_kv(k, v, slots, heads, dim):
+    _heads_3d(k, "k")
+    _heads_3d(v, "v")
+    if v.dtype != k.dtype:
+        raise TypeError("k and v share one dtype")
+    shape = (k.shape[0], heads, dim)
+    for t, name in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must be [tokens, %d, %d] for this cache, got %s"
+                             % (name, heads, dim, tuple(t.shape)))
+    _expect(slots, "slots", torch.int64, (k.shape[0],))
+
+
+def _tok_stride(t):
+    """Elements between tokens (a single token's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale):
+    """Quantises k and v [tokens, heads, head_dim] into the places `slots`
+    (int64, block * block_size + place; outside the cache: padding, skipped) of
+    a paged cache: uint8 codes [blocks, block_size, heads, head_dim] with
+    float32 scales [blocks, block_size, heads] (fp8), or codes of width
+    head_dim / 2 with uint8 scales [blocks, block_size, heads, head_dim / 32]
+    (mxfp4).  k and v may be token-strided, the cache's parts block-strided."""
+    key, known = _known("write", None, (k, v, slots, k_cache, v_cache, k_scale, v_scale))
+    if known is None:
+        layout = _cache_layout(k_cache, v_cache, k_scale, v_scale)
+        _check_kv(k, v, slots, layout[2], layout[3])
+        _cuda(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+        known = _remember(key, (layout, (k.shape[0], _tok_stride(k), _tok_stride(v),
+                                         _dtype_code(k)), k.get_device()))
+    layout, sizes, device = known
+    _launch(device, lib.nr_kv_cache_write, _kv_cache(layout, k_cache, v_cache, k_scale, v_scale),
+            k.data_ptr(), v.data_ptr(), slots.data_ptr(), *sizes)
+
+
+def qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_scale, v_scale,
+                       eps=1e-6, gemma=False, rotary_dim=None, interleaved=False, theta=10000.0,
+                       llama3=None, mrope_sections=None, mrope_interleaved=False, q_out=None):
+    """qk_norm_rope_ex with K (quantised from its f32 value) and V written into
+    the cache as kv_cache_write does.  Returns q_out."""
+    options = (eps, gemma, rotary_dim, interleaved, theta, llama3,
+               None if mrope_sections is None else tuple(mrope_sections), mrope_interleaved)
+    key, known = _known("fused", options, (q, k, v, wq, wk, positions, slots, k_cache, v_cache,
+                                           k_scale, v_scale, q_out))
+    if known is None:
+        layout = _cache_layout(k_cache, v_cache, k_scale, v_scale)
+        _check_kv(k, v, slots, layout[2], layout[3])
+        _check_qk(q, k, wq, wk, q_out, None)
+        _expect(positions, "positions", torch.int32,
+                (3, q.shape[0]) if mrope_sections is not None else (q.shape[0],))
+        _cuda(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_scale, v_scale, q_out)
+        cfg = _rope_config(rotary_dim, interleaved, theta, llama3, mrope_sections,
+                           mrope_interleaved)
+        known = _remember(key, (layout, _dtype_code(wq),
+                                (q.shape[0], q.shape[1], _tok_stride(q), _tok_stride(k),
+                                 _tok_stride(v), float(eps), int(bool(gemma)), cfg,
+                                 _dtype_code(q)), q.get_device()))
+    layout, wcode, sizes, device = known
+    if q_out is None:
+        q_out = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    _launch(device, lib.nr_qk_norm_rope_cache,
+            _kv_cache(layout, k_cache, v_cache, k_scale, v_scale), q_out.data_ptr(), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), wq.data_ptr(), wk.data_ptr(), wcode, positions.data_ptr(),
+            slots.data_ptr(), *sizes)
+    return q_out
+
+
+def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, rows=None,
+                  dtype=torch.bfloat16, k_out=None, v_out=None):
+    """Reads sequences back from the cache: row cu_seqlens[s] + t of k and v
+    [rows, heads, head_dim] is token t of sequence s, found through
+    block_table [seqs, n] int32; cu_seqlens is [seqs + 1] int32.  Give `rows`
+    (at least cu_seqlens[-1], which is not read on the host) or outputs to fill;
+    rows behind the last sequence are left as they were.  Returns (k, v)."""
+    key, known = _known("read", (rows, dtype), (k_cache, v_cache, k_scale, v_scale, block_table,
+                                                cu_seqlens, k_out, v_out))
+    if known is None:
+        layout = _cache_layout(k_cache, v_cache, k_scale, v_scale)
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a [seqs, blocks] tensor")
+        _expect(block_table, "block_table", torch.int32, block_table.shape)
+        _expect(cu_seqlens, "cu_seqlens", torch.int32, (block_table.shape[0] + 1,))
+        for t in (k_out, v_out):
+            if rows is None and isinstance(t, torch.Tensor) and t.dim() == 3:
+                rows, dtype = t.shape[0], t.dtype
+        if rows is None:
+            raise ValueError("kv_cache_read needs rows or outputs [rows, heads, head_dim]")
+        if int(rows) < 0:
+            raise ValueError("rows must be >= 0")
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("dtype must be bfloat16 or float32, got %s" % dtype)
+        shape = (int(rows), layout[2], layout[3])
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None:
+                _expect(t, name, dtype, shape)
+        _cuda(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, k_out, v_out)
+        known = _remember(key, (layout, shape, dtype, k_cache.device, block_table.shape[1],
+                                (block_table.shape[0], shape[0],
+                                 NR_BF16 if dtype == torch.bfloat16 else NR_F32)))
+    layout, shape, dtype, device, width, sizes = known
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=device)
+    _launch(device.index, lib.nr_kv_cache_read, k_out.data_ptr(), v_out.data_ptr(),
+            _kv_cache(layout, k_cache, v_cache, k_scale, v_scale), block_table.data_ptr(), width,
+            cu_seqlens.data_ptr(), *sizes)
+    return k_out, v_out
+
+
+def _activation(name):
+    if name is None or name == "none":
+        return NR_ACT_NONE
+    if name == "silu":
+        return NR_ACT_SILU
+    raise ValueError("activation must be None or 'silu', got %r" % (name,))
+
+
+def _group_norm_workspace(samples, space, channels, groups, code):
+    n = ctypes.c_int64()
+    _check(lib.nr_group_norm_workspace(samples, space, channels, groups, code, ctypes.byref(n)))
+    return n.value
+
+
+def _check_norm(x, w, b):
+    """x [samples, ..., channels] and its affine parameters; (samples, space,
+    channels, dtype code of the parameters)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    if x.dim() < 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [samples, ..., channels] tensor")
+    code = _dtype_code(x)
+    samples, channels = x.shape[0], x.shape[-1]
+    if (w is None) != (b is None):
+        raise ValueError("w and b are given together or not at all")
+    if w is not None:
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("w must be a float32 or bfloat16 tensor")
+        _expect(w, "w", w.dtype, (channels,))
+        _expect(b, "b", w.dtype, (channels,))
+        code = _dtype_code(w)
+    space = 1
+    for n in x.shape[1:-1]:
+        space *= n
+    return samples, space, channels, code
+
+
+def group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, stats=False):
+    """Group norm of x [samples, ..., channels] (channels last, any number of
+    axes between) with w and b [channels] (float32 or bfloat16; both or
+    neither), then `activation` (None or "silu").  Returns out, or (out, mean,
+    rstd) with stats=True: the [samples, groups] float32 statistics that
+    group_norm_backward takes."""
+    key, known = _known("norm", (groups, eps, activation), (x, w, b, out))
+    if known is None:
+        samples, space, channels, wcode = _check_norm(x, w, b)
+        groups = int(groups)
+        if groups < 1 or channels % groups:
+            raise ValueError("%d channels do not divide into %d groups" % (channels, groups))
+        act = _activation(activation)
+        if out is not None:
+            _expect(out, "out", x.dtype, x.shape)
+        _cuda(x, w, b, out)
+        code = _dtype_code(x)
+        known = _remember(key, (wcode, (samples, space, channels, groups, float(eps), act, code),
+                                _group_norm_workspace(samples, space, channels, groups, code),
+                                x.device))
+    wcode, sizes, need, device = known
+    if out is None:
+        out = torch.empty_like(x)
+    samples, groups = sizes[0], sizes[3]
+    # with no elements nothing is written
+    held = torch.empty if sizes[1] else torch.zeros
+    both = held((2, samples, groups), dtype=torch.float32, device=device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    mean = both.data_ptr()
+    _launch(device.index, lib.nr_group_norm, out.data_ptr(), mean, mean + 4 * samples * groups,
+            x.data_ptr(), None if w is None else w.data_ptr(), None if b is None else b.data_ptr(),
+            wcode, *sizes, workspace.data_ptr(), need)
+    return (out, *both.unbind(0)) if stats else out
+
+
+def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=None):
+    """The gradient of group_norm: dy and x [samples, ..., channels], the mean
+    and rstd that it returned, the same w, b and activation.  Returns (dx, dw,
+    db); dw and db have w's dtype (None without w).  dx may be dy or x."""
+    key, known = _known("norm back", activation, (dy, x, mean, rstd, w, b, dx))
+    if known is None:
+        samples, space, channels, wcode = _check_norm(x, w, b)
+        _expect(dy, "dy", x.dtype, x.shape)
+        if not isinstance(mean, torch.Tensor) or mean.dim() != 2:
+            raise ValueError("mean must be a [samples, groups] tensor")
+        groups = mean.shape[1]
+        _expect(mean, "mean", torch.float32, (samples, groups))
+        _expect(rstd, "rstd", torch.float32, (samples, groups))
+        if groups < 1 or channels % groups:
+            raise ValueError("%d channels do not divide into %d groups" % (channels, groups))
+        act = _activation(activation)
+        if dx is not None:
+            _expect(dx, "dx", x.dtype, x.shape)
+        _cuda(x, dy, mean, rstd, w, b, dx)
+        code = _dtype_code(x)
+        known = _remember(key, (wcode, (samples, space, channels, groups, act, code),
+                                _group_norm_workspace(samples, space, channels, groups, code),
+                                x.device))
+    wcode, sizes, need, device = known
+    if dx is None:
+        dx = torch.empty_like(x)
+    dw = db = pw = pb = pdw = pdb = None
+    if w is not None:
+        held = torch.empty_like if sizes[0] and sizes[1] else torch.zeros_like
+        dw, db = held(w), held(b)
+        pw, pb, pdw, pdb = w.data_ptr(), b.data_ptr(), dw.data_ptr(), db.data_ptr()
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _launch(device.index, lib.nr_group_norm_backward, dx.data_ptr(), pdw, pdb, dy.data_ptr(),
+            x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), pw, pb, wcode, *sizes,
+            workspace.data_ptr(), need)
+    return dx, dw, db
 
 
 def ln_modulate(x, shift, scale, eps=1e-6, rows_per_sample=None, out=None):
@@ -389,5 +748,7 @@ def gelu_and_mul(x, out=None):
 
 __all__ = ["rmsnorm", "rmsnorm_quant_fp8", "qk_norm_rope", "qk_norm_rope_ex", "RopeConfig", "ln_modulate",
            "silu_and_mul", "gelu_and_mul", "device_status", "wait_probe",
-           "gated_residual_ln_modulate", "NrError", "lib",
-           "LIB_PATH", "ENTRY_POINTS", "NR_F32", "NR_BF16"]
+           "gated_residual_ln_modulate", "kv_cache_write", "kv_cache_read", "qk_norm_rope_cache",
+           "group_norm", "group_norm_backward", "KvCache", "NrError", "lib",
+           "LIB_PATH", "ENTRY_POINTS", "NR_F32", "NR_BF16", "NR_CACHE_FP8", "NR_CACHE_MXFP4",
+           "NR_ACT_NONE", "NR_ACT_SILU"]

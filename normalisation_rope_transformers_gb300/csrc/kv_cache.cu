@@ -1,0 +1,331 @@
+// Quantised paged K/V cache for sm_103a: writing new tokens, and reading
+// sequences back.
+//
+// Write: a group of L lanes owns one (token, head) row, eight values a lane,
+// so the row's (FP8) or the 32-element group's (MXFP4) largest magnitude is a
+// butterfly over lanes, and the codes leave as one store a lane.  Each input
+// byte is read once and each code written once; HBM (large calls) or latency
+// (decode) bounds it.
+//
+// Read: a block first resolves the slots of a few output rows (a binary search
+// for the sequence, a page-table lookup) into shared memory, then streams
+// their codes, eight a lane, and writes widened rows.
+#include "quant.cuh"
+
+namespace nr {
+namespace {
+
+constexpr int kCacheThreads = 128;
+constexpr int kUnit = 8;  // values a lane handles at a time
+
+template <typename T>
+struct Unit;
+template <>
+struct Unit<__nv_bfloat16> {
+  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float (&f)[kUnit]) {
+    Vec<__nv_bfloat16>::unpack(ld_stream(p), f);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&f)[kUnit]) {
+    st_stream(p, Vec<__nv_bfloat16>::pack(f));
+  }
+};
+template <>
+struct Unit<float> {
+  __device__ __forceinline__ static void load(const float* p, float (&f)[kUnit]) {
+    float a[4], b[4];
+    Vec<float>::unpack(ld_stream(p), a);
+    Vec<float>::unpack(ld_stream(p + 4), b);
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[e] = a[e], f[e + 4] = b[e];
+  }
+  __device__ __forceinline__ static void store(float* p, const float (&f)[kUnit]) {
+    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+    st_stream(p, Vec<float>::pack(a));
+    st_stream(p + 4, Vec<float>::pack(b));
+  }
+};
+
+struct WriteArgs {
+  const void* src[2];   // k, v
+  int64_t stride[2];    // elements between tokens
+  CacheSide side[2];
+  CacheGeom geo;
+  const int64_t* slots;
+  FastDiv heads;
+  uint32_t rows;  // tokens * heads
+  int units;      // head_dim / 8
+};
+
+// L lanes a row, NV units a lane (head_dim <= 8 * L * NV), ROWS rows a lane
+// group in flight.  blockIdx.y: 0 K, 1 V.
+template <typename T, bool FP4, int L, int NV, int ROWS>
+__global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs a) {
+  constexpr int GW = kWarp / L;
+  pdl_enter();
+  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  const int g = lane32 / L, l = lane32 % L;
+  const uint32_t first =
+      (blockIdx.x * (kCacheThreads / kWarp) + warp) * static_cast<uint32_t>(GW * ROWS) + g;
+  const bool is_v = blockIdx.y != 0;
+  const T* src = static_cast<const T*>(is_v ? a.src[1] : a.src[0]);
+  const int64_t stride = is_v ? a.stride[1] : a.stride[0];
+  const CacheSide side = is_v ? a.side[1] : a.side[0];
+  const int dim = a.units * kUnit;
+
+  // every load before any use; a padded token's row is in bounds, and its
+  // values go nowhere
+  float x[ROWS][NV][kUnit];
+  int64_t slot[ROWS];
+  uint32_t head[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; i++) {
+    const uint32_t row = first + i * GW;
+    slot[i] = -1;
+    head[i] = 0;
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int e = 0; e < kUnit; e++) x[i][j][e] = 0.0f;
+    if (row < a.rows) {
+      const uint32_t tok = a.heads.quot(row);
+      head[i] = row - tok * a.heads.div;
+      slot[i] = __ldg(a.slots + tok);
+      const T* p = src + tok * stride + static_cast<int64_t>(head[i]) * dim;
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+        if (l + j * L < a.units) Unit<T>::load(p + (l + j * L) * kUnit, x[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; i++) {
+    float top[NV], row_top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      top[j] = max_abs(x[i][j]);
+      if (FP4) top[j] = group_max<4>(top[j]);
+      row_top = fmaxf(row_top, top[j]);
+    }
+    if (!FP4) row_top = group_max<L>(row_top);
+    // slots outside the cache (padding) are skipped
+    if (slot[i] < 0 || slot[i] >= a.geo.slots) continue;
+    const int64_t block = a.geo.block_of(slot[i]);
+    const int64_t place = slot[i] - block * a.geo.block_size;
+    unsigned char* codes = side.codes + block * a.geo.code_block_stride + place * a.geo.code_row;
+    unsigned char* scales =
+        side.scales + block * a.geo.scale_block_stride + place * a.geo.scale_row;
+    if (!FP4) {
+      const float am = clamp_scale(row_top), inv = fp8_inverse(am);
+      codes += static_cast<int64_t>(head[i]) * dim;
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+        if (l + j * L < a.units) {
+          uint32_t c[2];
+          fp8_codes(x[i][j], inv, c);
+          st_stream8(codes + (l + j * L) * kUnit, make_uint2(c[0], c[1]));
+        }
+      if (l == 0) reinterpret_cast<float*>(scales)[head[i]] = fp8_scale(am);
+    } else {
+      codes += static_cast<int64_t>(head[i]) * (dim / 2);
+      scales += static_cast<int64_t>(head[i]) * (dim / 32);
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+        if (l + j * L < a.units) {
+          const int u = l + j * L;
+          const uint32_t byte = mx_scale_byte(clamp_scale(top[j]));
+          st_stream4(codes + u * (kUnit / 2), fp4_codes(x[i][j], mx_inverse(byte)));
+          if (u % 4 == 0) scales[u / 4] = static_cast<unsigned char>(byte);
+        }
+    }
+  }
+}
+
+template <typename T, bool FP4, int L, int NV>
+cudaError_t write_l(const WriteArgs& a, cudaStream_t s) {
+  constexpr int GW = kWarp / L;
+  constexpr int kWarps = kCacheThreads / kWarp;
+  // Large calls keep several rows a lane in flight; small ones spread out.
+  constexpr int ROWS = NV * static_cast<int>(sizeof(T)) >= 8 ? 2 : 4;
+  if (a.rows >= 152u * 8 * kWarps * GW * ROWS) {
+    const unsigned blocks = (a.rows + kWarps * GW * ROWS - 1) / (kWarps * GW * ROWS);
+    return launch_pdl(kv_write_kernel<T, FP4, L, NV, ROWS>, dim3(blocks, 2), dim3(kCacheThreads),
+                      0, s, a);
+  }
+  const unsigned blocks = (a.rows + kWarps * GW - 1) / (kWarps * GW);
+  return launch_pdl(kv_write_kernel<T, FP4, L, NV, 1>, dim3(blocks, 2), dim3(kCacheThreads), 0, s,
+                    a);
+}
+
+template <typename T, bool FP4>
+cudaError_t write_t(const WriteArgs& a, cudaStream_t s) {
+  if (a.units <= 2) return write_l<T, FP4, FP4 ? 4 : 2, 1>(a, s);
+  if (a.units <= 4) return write_l<T, FP4, 4, 1>(a, s);
+  if (a.units <= 8) return write_l<T, FP4, 8, 1>(a, s);
+  if (a.units <= 16) return write_l<T, FP4, 16, 1>(a, s);
+  if (a.units <= 32) return write_l<T, FP4, 32, 1>(a, s);
+  return write_l<T, FP4, 32, 2>(a, s);
+}
+
+// ---------------------------------------------------------------------------
+// Read
+// ---------------------------------------------------------------------------
+constexpr int kReadThreads = 256;
+constexpr int kReadMaxRows = 64;  // output rows a block resolves
+
+struct ReadArgs {
+  void* out[2];
+  CacheSide side[2];
+  CacheGeom geo;
+  const int32_t* table;  // [seqs, width]
+  const int32_t* cu;     // [seqs + 1]
+  int64_t width;
+  int64_t blocks;
+  int seqs;
+  int64_t rows;      // rows of the outputs
+  int block_rows;    // output rows of a thread block
+  FastDiv row_units; // heads * head_dim / 8
+  FastDiv head_units;
+};
+
+// The slot of output row r: -1 for a row of no sequence (left as it is), -2
+// for one whose page is missing (read as zeros).
+__device__ __forceinline__ int64_t slot_of(const ReadArgs& a, int64_t r) {
+  if (r >= a.rows || r < a.cu[0] || r >= a.cu[a.seqs]) return -1;
+  int lo = 0, hi = a.seqs;  // cu[lo] <= r < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.cu[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  const int64_t t = r - a.cu[lo];
+  const int64_t page = a.geo.block_of(t);
+  if (page >= a.width) return -2;
+  const int64_t block = a.table[lo * a.width + page];
+  if (block < 0 || block >= a.blocks) return -2;
+  return block * a.geo.block_size + (t - page * a.geo.block_size);
+}
+
+template <typename T, bool FP4>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
+  __shared__ int64_t code_at[kReadMaxRows];  // byte offsets, or -1 / -2
+  __shared__ int64_t scale_at[kReadMaxRows];
+  pdl_enter();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.block_rows;
+  if (threadIdx.x < a.block_rows) {
+    const int64_t slot = slot_of(a, row0 + threadIdx.x);
+    int64_t c = slot, s = slot;
+    if (slot >= 0) {
+      const int64_t block = a.geo.block_of(slot);
+      const int64_t place = slot - block * a.geo.block_size;
+      c = block * a.geo.code_block_stride + place * a.geo.code_row;
+      s = block * a.geo.scale_block_stride + place * a.geo.scale_row;
+    }
+    code_at[threadIdx.x] = c;
+    scale_at[threadIdx.x] = s;
+  }
+  __syncthreads();
+  const bool is_v = blockIdx.y != 0;
+  T* out = static_cast<T*>(is_v ? a.out[1] : a.out[0]) +
+           row0 * static_cast<int64_t>(a.row_units.div) * kUnit;
+  const CacheSide side = is_v ? a.side[1] : a.side[0];
+  const uint32_t n = static_cast<uint32_t>(a.block_rows) * a.row_units.div;
+  constexpr int U = 4;
+  for (uint32_t base = threadIdx.x; base < n; base += U * kReadThreads) {
+    uint2 codes[U];
+    float scale[U];
+    int64_t where[U];
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      const uint32_t i = base + j * kReadThreads;
+      where[j] = -1;
+      codes[j] = make_uint2(0u, 0u);
+      scale[j] = 0.0f;
+      if (i >= n) continue;
+      const uint32_t r = a.row_units.quot(i), u = i - r * a.row_units.div;
+      where[j] = code_at[r];
+      if (where[j] < 0) continue;
+      if (FP4) {
+        codes[j].x = __ldg(reinterpret_cast<const uint32_t*>(side.codes + where[j]) + u);
+        const uint32_t byte = __ldg(side.scales + scale_at[r] + u / 4);
+        // 2^(byte - 127); bytes 0 and 255 (2^-127, NaN) as the format has them
+        scale[j] = byte == 0 ? 0x1p-127f : __uint_as_float(byte == 255 ? 0x7FC00000u : byte << 23);
+      } else {
+        codes[j] = __ldg(reinterpret_cast<const uint2*>(side.codes + where[j]) + u);
+        scale[j] = __ldg(reinterpret_cast<const float*>(side.scales + scale_at[r]) +
+                         a.head_units.quot(u));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < U; j++) {
+      if (where[j] == -1) continue;
+      float f[kUnit];
+#pragma unroll
+      for (int h = 0; h < kUnit / 2; h++) {
+        float2 v;
+        if (FP4) {
+          const __half2_raw p = __nv_cvt_fp4x2_to_halfraw2(
+              static_cast<__nv_fp4x2_storage_t>(codes[j].x >> (8 * h)), __NV_E2M1);
+          v = __half22float2(__half2(p));
+        } else {
+          const uint32_t w = h < 2 ? codes[j].x : codes[j].y;
+          const __half2_raw p = __nv_cvt_fp8x2_to_halfraw2(
+              static_cast<__nv_fp8x2_storage_t>(w >> (16 * (h % 2))), __NV_E4M3);
+          v = __half22float2(__half2(p));
+        }
+        f[2 * h] = v.x * scale[j];
+        f[2 * h + 1] = v.y * scale[j];
+      }
+      Unit<T>::store(out + static_cast<int64_t>(base + j * kReadThreads) * kUnit, f);
+    }
+  }
+}
+
+template <typename T, bool FP4>
+cudaError_t read_t(ReadArgs& a, cudaStream_t s) {
+  // About eight units a thread, so that resolving a slot is shared by many.
+  int64_t rows = 8 * kReadThreads / static_cast<int64_t>(a.row_units.div);
+  rows = rows < 1 ? 1 : rows > kReadMaxRows ? kReadMaxRows : rows;
+  a.block_rows = static_cast<int>(rows);
+  const unsigned blocks = static_cast<unsigned>((a.rows + rows - 1) / rows);
+  return launch_pdl(kv_read_kernel<T, FP4>, dim3(blocks, 2), dim3(kReadThreads), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvCacheArgs& c, const void* k, const void* v,
+                            const int64_t* slots, int64_t tokens, int64_t k_stride,
+                            int64_t v_stride, int is_bf16, cudaStream_t stream) {
+  WriteArgs a{{k, v},
+              {k_stride, v_stride},
+              {{c.k_codes, c.k_scales}, {c.v_codes, c.v_scales}},
+              cache_geometry(c),
+              slots,
+              FastDiv(static_cast<uint32_t>(c.heads)),
+              static_cast<uint32_t>(tokens * c.heads),
+              static_cast<int>(c.head_dim / kUnit)};
+  if (is_bf16)
+    return c.fp4 ? write_t<__nv_bfloat16, true>(a, stream)
+                 : write_t<__nv_bfloat16, false>(a, stream);
+  return c.fp4 ? write_t<float, true>(a, stream) : write_t<float, false>(a, stream);
+}
+
+cudaError_t launch_kv_read(const KvCacheArgs& c, void* k_out, void* v_out, const int32_t* table,
+                           int64_t width, const int32_t* cu, int64_t seqs, int64_t rows,
+                           int is_bf16, cudaStream_t stream) {
+  ReadArgs a{{k_out, v_out},
+             {{c.k_codes, c.k_scales}, {c.v_codes, c.v_scales}},
+             cache_geometry(c),
+             table,
+             cu,
+             width,
+             c.blocks,
+             static_cast<int>(seqs),
+             rows,
+             0,
+             FastDiv(static_cast<uint32_t>(c.heads * c.head_dim / kUnit)),
+             FastDiv(static_cast<uint32_t>(c.head_dim / kUnit))};
+  if (is_bf16)
+    return c.fp4 ? read_t<__nv_bfloat16, true>(a, stream) : read_t<__nv_bfloat16, false>(a, stream);
+  return c.fp4 ? read_t<float, true>(a, stream) : read_t<float, false>(a, stream);
+}
+
+}  // namespace nr

@@ -213,25 +213,11 @@ unsigned char mrope_row(int64_t i, const nr_rope_config& c) {
   return i < sec[0] + sec[1] ? 1 : 2;
 }
 
-nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void* q, const void* k,
-                            const void* wq, const void* wk, nr_dtype w_dtype,
-                            const int32_t* positions, int64_t tokens, int64_t hq, int64_t hk,
-                            int64_t head_dim, int64_t q_tok_stride, int64_t k_tok_stride,
-                            float eps, int gemma, const nr_rope_config& rope, nr_dtype dtype,
-                            cudaStream_t stream) {
-  if (!valid_dtype(dtype) || !valid_dtype(w_dtype))
-    return fail(NR_ERR_DTYPE, "%s: unknown dtype (%d, weights %d)", fn, (int)dtype, (int)w_dtype);
-  if (tokens < 0 || hq < 1 || hk < 0 || head_dim <= 0)
-    return fail(NR_ERR_SHAPE, "%s: need tokens >= 0, hq >= 1, hk >= 0, head_dim > 0", fn);
-  if (head_dim % 2 != 0) return fail(NR_ERR_SHAPE, "%s: head_dim must be even", fn);
-  const int vec = vec_elems(dtype);
-  const int64_t lanes = head_dim / (2 * vec);
-  if (head_dim % (2 * vec) != 0 || lanes > 32 || (lanes & (lanes - 1)) != 0)
-    return fail(NR_ERR_UNSUPPORTED,
-                "%s: head_dim %lld not supported for this dtype (bf16: 16..512, f32: 8..256, "
-                "powers of two)",
-                fn, (long long)head_dim);
-  const int64_t rot = rope.rotary_dim == 0 ? head_dim : rope.rotary_dim;
+// The rotary configuration and eps for a head of head_dim elements in vectors
+// of `vec`; the rotary dimension and whether M-RoPE is on.
+nr_status check_rope(const char* fn, const nr_rope_config& rope, int64_t head_dim, int vec,
+                     float eps, int64_t* rot_out, bool* mrope_out) {
+  const int64_t rot = *rot_out = rope.rotary_dim == 0 ? head_dim : rope.rotary_dim;
   if (rot <= 0 || rot > head_dim || rot % 2 != 0)
     return fail(NR_ERR_SHAPE, "%s: rotary_dim %lld must be even and in (0, head_dim]", fn,
                 (long long)rot);
@@ -252,10 +238,55 @@ nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void
          isfinite(rope.llama3_original_max_position))))
     return fail(NR_ERR_VALUE, "%s: Llama-3 factors must be positive and finite, high >= low", fn);
   const int32_t* sec = rope.mrope_section;
-  const bool mrope = sec[0] != 0 || sec[1] != 0 || sec[2] != 0;
+  const bool mrope = *mrope_out = sec[0] != 0 || sec[1] != 0 || sec[2] != 0;
   if (sec[0] < 0 || sec[1] < 0 || sec[2] < 0 ||
       (mrope && static_cast<int64_t>(sec[0]) + sec[1] + sec[2] != rot / 2))
     return fail(NR_ERR_SHAPE, "%s: M-RoPE sections must be >= 0 and sum to rotary_dim / 2", fn);
+  return NR_OK;
+}
+
+void fill_turns(const nr_rope_config& rope, int64_t rot, bool mrope, nr::RopeTurns* out) {
+  // turn_i = frac(freq_i / 2pi) * 2^64, freq_i = theta^(-2i/rot) (Llama-3
+  // rescaled when asked), in double.  Positions are integers, so
+  // pos * freq_i mod 2pi = pos * (freq_i mod 2pi) mod 2pi.
+  nr::RopeTurns& turns = *out;
+  for (int64_t i = 0; i < nr::kMaxHalfDim; i++) {
+    turns.turn[i] = 0;
+    turns.axis[i] = 0;
+  }
+  for (int64_t i = 0; i < rot / 2; i++) {
+    const double freq = llama3_rescale(
+        pow(rope.theta, -2.0 * static_cast<double>(i) / static_cast<double>(rot)), rope);
+    const double turns_per_step = freq / (2.0 * M_PI);
+    const double frac = turns_per_step - floor(turns_per_step);
+    const double scaled = ldexp(frac, 64);
+    turns.turn[i] =
+        scaled >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(scaled);
+    turns.axis[i] = mrope ? mrope_row(i, rope) : 0;
+  }
+}
+
+nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void* q, const void* k,
+                            const void* wq, const void* wk, nr_dtype w_dtype,
+                            const int32_t* positions, int64_t tokens, int64_t hq, int64_t hk,
+                            int64_t head_dim, int64_t q_tok_stride, int64_t k_tok_stride,
+                            float eps, int gemma, const nr_rope_config& rope, nr_dtype dtype,
+                            cudaStream_t stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(w_dtype))
+    return fail(NR_ERR_DTYPE, "%s: unknown dtype (%d, weights %d)", fn, (int)dtype, (int)w_dtype);
+  if (tokens < 0 || hq < 1 || hk < 0 || head_dim <= 0)
+    return fail(NR_ERR_SHAPE, "%s: need tokens >= 0, hq >= 1, hk >= 0, head_dim > 0", fn);
+  if (head_dim % 2 != 0) return fail(NR_ERR_SHAPE, "%s: head_dim must be even", fn);
+  const int vec = vec_elems(dtype);
+  const int64_t lanes = head_dim / (2 * vec);
+  if (head_dim % (2 * vec) != 0 || lanes > 32 || (lanes & (lanes - 1)) != 0)
+    return fail(NR_ERR_UNSUPPORTED,
+                "%s: head_dim %lld not supported for this dtype (bf16: 16..512, f32: 8..256, "
+                "powers of two)",
+                fn, (long long)head_dim);
+  int64_t rot = 0;
+  bool mrope = false;
+  if (const nr_status s = check_rope(fn, rope, head_dim, vec, eps, &rot, &mrope)) return s;
   if (gemma != 0 && gemma != 1) return fail(NR_ERR_VALUE, "%s: gemma must be 0 or 1", fn);
   if (q_tok_stride < hq * head_dim || (hk > 0 && k_tok_stride < hk * head_dim))
     return fail(NR_ERR_SHAPE, "%s: token stride smaller than heads * head_dim", fn);
@@ -293,24 +324,8 @@ nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void
       overlap(rko, rwk) || overlap(rko, rpos))
     return fail(NR_ERR_ALIAS, "%s: k_out overlaps an input", fn);
 
-  // turn_i = frac(freq_i / 2pi) * 2^64, freq_i = theta^(-2i/rot) (Llama-3
-  // rescaled when asked), in double.  Positions are integers, so
-  // pos * freq_i mod 2pi = pos * (freq_i mod 2pi) mod 2pi.
   nr::RopeTurns turns;
-  for (int64_t i = 0; i < nr::kMaxHalfDim; i++) {
-    turns.turn[i] = 0;
-    turns.axis[i] = 0;
-  }
-  for (int64_t i = 0; i < rot / 2; i++) {
-    const double freq = llama3_rescale(
-        pow(rope.theta, -2.0 * static_cast<double>(i) / static_cast<double>(rot)), rope);
-    const double turns_per_step = freq / (2.0 * M_PI);
-    const double frac = turns_per_step - floor(turns_per_step);
-    const double scaled = ldexp(frac, 64);
-    turns.turn[i] =
-        scaled >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(scaled);
-    turns.axis[i] = mrope ? mrope_row(i, rope) : 0;
-  }
+  fill_turns(rope, rot, mrope, &turns);
   return from_cuda(nr::launch_qk_norm_rope(q_out, k_out, q, k, wq, wk, w_dtype == NR_BF16,
                                            positions, tokens, hq, hk, head_dim, q_tok_stride,
                                            k_tok_stride, eps, turns, gemma, rot, rope.interleaved,
@@ -444,6 +459,389 @@ nr_status act_and_mul(const char* fn, int gelu, void* out, const void* x, int64_
 
 }  // namespace
 
+namespace {
+
+// The cache's sizes, strides and pointers (`need_pointers` false: a call that
+// touches nothing).  On success `args` is what the launchers take.
+nr_status check_cache(const char* fn, const nr_kv_cache* c, bool need_pointers,
+                      nr::KvCacheArgs* args) {
+  if (c == nullptr) return fail(NR_ERR_NULL, "%s: the cache is NULL", fn);
+  if (c->format != NR_CACHE_FP8 && c->format != NR_CACHE_MXFP4)
+    return fail(NR_ERR_DTYPE, "%s: unknown cache format %d", fn, (int)c->format);
+  const bool fp4 = c->format == NR_CACHE_MXFP4;
+  if (c->blocks < 1 || c->block_size < 1 || c->heads < 1 || c->head_dim < 1)
+    return fail(NR_ERR_SHAPE, "%s: blocks, block_size, heads and head_dim must be >= 1", fn);
+  if (c->head_dim > 512 || c->head_dim % (fp4 ? 32 : 16) != 0)
+    return fail(NR_ERR_UNSUPPORTED, "%s: head_dim %lld must be a multiple of %d, at most 512", fn,
+                (long long)c->head_dim, fp4 ? 32 : 16);
+  if (c->heads > (int64_t(1) << 24) / c->head_dim || c->blocks > INT32_MAX ||
+      c->block_size > INT32_MAX)
+    return fail(NR_ERR_SHAPE, "%s: heads, blocks or block_size too large", fn);
+  const int64_t code_bytes = c->block_size * c->heads * (fp4 ? c->head_dim / 2 : c->head_dim);
+  const int64_t scale_bytes = c->block_size * c->heads * (fp4 ? c->head_dim / 32 : 4);
+  if (c->code_block_stride < code_bytes || c->scale_block_stride < scale_bytes)
+    return fail(NR_ERR_SHAPE, "%s: a block stride is smaller than a block", fn);
+  if (c->code_block_stride > INT64_MAX / 2 / c->blocks ||
+      c->scale_block_stride > INT64_MAX / 2 / c->blocks)
+    return fail(NR_ERR_SHAPE, "%s: a block stride is too large", fn);
+  if (c->code_block_stride % 16 != 0 || (!fp4 && c->scale_block_stride % 4 != 0))
+    return fail(NR_ERR_ALIGN, "%s: block strides must be multiples of 16 (codes) and 4 (f32 scales)",
+                fn);
+  if (need_pointers) {
+    if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+      return fail(NR_ERR_NULL, "%s: the cache's pointers must be non-NULL", fn);
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) ||
+        (!fp4 && ((reinterpret_cast<uintptr_t>(c->k_scales) |
+                   reinterpret_cast<uintptr_t>(c->v_scales)) & 3u)))
+      return fail(NR_ERR_ALIGN, "%s: codes must be 16-byte aligned, f32 scales 4-byte", fn);
+  }
+  *args = nr::KvCacheArgs{static_cast<unsigned char*>(c->k_codes),
+                          static_cast<unsigned char*>(c->v_codes),
+                          static_cast<unsigned char*>(c->k_scales),
+                          static_cast<unsigned char*>(c->v_scales),
+                          c->blocks,
+                          c->block_size,
+                          c->heads,
+                          c->head_dim,
+                          c->code_block_stride,
+                          c->scale_block_stride,
+                          fp4};
+  return NR_OK;
+}
+
+// The cache's four parts: K codes, V codes, K scales, V scales.
+struct CacheRegions {
+  Region part[4];
+  explicit CacheRegions(const nr_kv_cache& c) {
+    const bool fp4 = c.format == NR_CACHE_MXFP4;
+    const int64_t codes = c.block_size * c.heads * (fp4 ? c.head_dim / 2 : c.head_dim);
+    const int64_t scales = c.block_size * c.heads * (fp4 ? c.head_dim / 32 : 4);
+    auto region = [&](const void* p, int64_t stride, int64_t span) {
+      return Region{reinterpret_cast<uintptr_t>(p), stride, span, c.blocks};
+    };
+    part[0] = region(c.k_codes, c.code_block_stride, codes);
+    part[1] = region(c.v_codes, c.code_block_stride, codes);
+    part[2] = region(c.k_scales, c.scale_block_stride, scales);
+    part[3] = region(c.v_scales, c.scale_block_stride, scales);
+  }
+  bool overlaps(const Region& r) const {
+    for (const Region& p : part)
+      if (overlap(p, r)) return true;
+    return false;
+  }
+  bool overlaps_itself() const {
+    for (int i = 0; i < 4; i++)
+      for (int j = 0; j < i; j++)
+        if (overlap(part[i], part[j])) return true;
+    return false;
+  }
+};
+
+bool misaligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+nr_status nr_kv_cache_write(const nr_kv_cache* cache, const void* k, const void* v,
+                            const int64_t* slots, int64_t tokens, int64_t k_tok_stride,
+                            int64_t v_tok_stride, nr_dtype dtype, cudaStream_t stream) {
+  CallRange range("nr_kv_cache_write");
+  const char* fn = "nr_kv_cache_write";
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (tokens < 0) return fail(NR_ERR_SHAPE, "%s: tokens = %lld < 0", fn, (long long)tokens);
+  nr::KvCacheArgs args;
+  if (const nr_status s = check_cache(fn, cache, tokens > 0, &args)) return s;
+  const int64_t row = cache->heads * cache->head_dim;
+  if (k_tok_stride < row || v_tok_stride < row)
+    return fail(NR_ERR_SHAPE, "%s: token stride smaller than heads * head_dim", fn);
+  if (tokens > INT32_MAX / cache->heads)
+    return fail(NR_ERR_SHAPE, "%s: tokens * heads too large", fn);
+  if (tokens == 0) return ok();
+  if (!k || !v || !slots) return fail(NR_ERR_NULL, "%s: k, v and slots must be non-NULL", fn);
+  const int es = elem_size(dtype);
+  if ((k_tok_stride * es) % 16 != 0 || (v_tok_stride * es) % 16 != 0)
+    return fail(NR_ERR_ALIGN, "%s: token strides must be multiples of 16 bytes", fn);
+  if (!aligned16(k) || !aligned16(v) || misaligned(slots, 8))
+    return fail(NR_ERR_ALIGN, "%s: k and v must be 16-byte aligned, slots 8-byte", fn);
+  const CacheRegions held(*cache);
+  if (held.overlaps_itself())
+    return fail(NR_ERR_ALIAS, "%s: parts of the cache overlap", fn);
+  if (held.overlaps(Region{reinterpret_cast<uintptr_t>(k), k_tok_stride * es, row * es, tokens}) ||
+      held.overlaps(Region{reinterpret_cast<uintptr_t>(v), v_tok_stride * es, row * es, tokens}) ||
+      held.overlaps(dense(slots, tokens * 8)))
+    return fail(NR_ERR_ALIAS, "%s: the cache overlaps an input", fn);
+  return from_cuda(nr::launch_kv_write(args, k, v, slots, tokens, k_tok_stride, v_tok_stride,
+                                       dtype == NR_BF16, stream),
+                   "nr_kv_cache_write launch");
+}
+
+nr_status nr_qk_norm_rope_cache(const nr_kv_cache* cache, void* q_out, const void* q,
+                                const void* k, const void* v, const void* wq, const void* wk,
+                                nr_dtype w_dtype, const int32_t* positions, const int64_t* slots,
+                                int64_t tokens, int64_t hq, int64_t q_tok_stride,
+                                int64_t k_tok_stride, int64_t v_tok_stride, float eps, int gemma,
+                                const nr_rope_config* rope, nr_dtype dtype, cudaStream_t stream) {
+  CallRange range("nr_qk_norm_rope_cache");
+  const char* fn = "nr_qk_norm_rope_cache";
+  if (!valid_dtype(dtype) || !valid_dtype(w_dtype))
+    return fail(NR_ERR_DTYPE, "%s: unknown dtype (%d, weights %d)", fn, (int)dtype, (int)w_dtype);
+  if (rope == nullptr) return fail(NR_ERR_NULL, "%s: rope config is NULL", fn);
+  if (tokens < 0 || hq < 1) return fail(NR_ERR_SHAPE, "%s: need tokens >= 0 and hq >= 1", fn);
+  nr::KvCacheArgs args;
+  if (const nr_status s = check_cache(fn, cache, tokens > 0, &args)) return s;
+  const int vec = vec_elems(dtype);
+  const int64_t dim = cache->head_dim, lanes = dim / (2 * vec);
+  if (dim % (2 * vec) != 0 || lanes < 4 || lanes > 32 || (lanes & (lanes - 1)) != 0)
+    return fail(NR_ERR_UNSUPPORTED,
+                "%s: head_dim %lld not supported for this dtype (bf16: 64..512, f32: 32..256, "
+                "powers of two)",
+                fn, (long long)dim);
+  int64_t rot = 0;
+  bool mrope = false;
+  if (const nr_status s = check_rope(fn, *rope, dim, vec, eps, &rot, &mrope)) return s;
+  if (args.fp4 && (dim % 64 != 0 || (!rope->interleaved && rot % 64 != 0)))
+    return fail(NR_ERR_UNSUPPORTED,
+                "%s: MXFP4 needs head_dim %lld and (rotate-half) rotary_dim %lld in multiples of 64",
+                fn, (long long)dim, (long long)rot);
+  if (gemma != 0 && gemma != 1) return fail(NR_ERR_VALUE, "%s: gemma must be 0 or 1", fn);
+  const int64_t hk = cache->heads;
+  if (q_tok_stride < hq * dim || k_tok_stride < hk * dim || v_tok_stride < hk * dim)
+    return fail(NR_ERR_SHAPE, "%s: token stride smaller than heads * head_dim", fn);
+  if (tokens > INT32_MAX || hq + 2 * hk > 65536)
+    return fail(NR_ERR_SHAPE, "%s: tokens or head count too large", fn);
+  if (tokens == 0) return ok();
+  if (!q_out || !q || !k || !v || !wq || !wk || !positions || !slots)
+    return fail(NR_ERR_NULL, "%s: every pointer must be non-NULL", fn);
+  const int es = elem_size(dtype);
+  if ((q_tok_stride * es) % 16 != 0 || (k_tok_stride * es) % 16 != 0 ||
+      (v_tok_stride * es) % 16 != 0)
+    return fail(NR_ERR_ALIGN, "%s: token strides must be multiples of 16 bytes", fn);
+  if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(wq) ||
+      !aligned16(wk) || misaligned(positions, 4) || misaligned(slots, 8))
+    return fail(NR_ERR_ALIGN,
+                "%s: q/k/v/weights must be 16-byte aligned, positions 4-byte, slots 8-byte", fn);
+  const int ws = elem_size(w_dtype);
+  const Region rqo{reinterpret_cast<uintptr_t>(q_out), q_tok_stride * es, hq * dim * es, tokens};
+  const Region rq{reinterpret_cast<uintptr_t>(q), q_tok_stride * es, hq * dim * es, tokens};
+  const Region ins[] = {
+      Region{reinterpret_cast<uintptr_t>(k), k_tok_stride * es, hk * dim * es, tokens},
+      Region{reinterpret_cast<uintptr_t>(v), v_tok_stride * es, hk * dim * es, tokens},
+      dense(wq, dim * ws), dense(wk, dim * ws), dense(positions, (mrope ? 3 : 1) * tokens * 4),
+      dense(slots, tokens * 8)};
+  const CacheRegions held(*cache);
+  if (held.overlaps_itself()) return fail(NR_ERR_ALIAS, "%s: parts of the cache overlap", fn);
+  if ((q_out != q && overlap(rqo, rq)) || held.overlaps(rqo) || held.overlaps(rq))
+    return fail(NR_ERR_ALIAS, "%s: q_out overlaps q or the cache", fn);
+  for (const Region& in : ins)
+    if (overlap(rqo, in) || held.overlaps(in))
+      return fail(NR_ERR_ALIAS, "%s: q_out or the cache overlaps an input", fn);
+  nr::RopeTurns turns;
+  fill_turns(*rope, rot, mrope, &turns);
+  return from_cuda(nr::launch_qk_norm_rope_cache(args, q_out, q, k, v, wq, wk, w_dtype == NR_BF16,
+                                                 positions, slots, tokens, hq, q_tok_stride,
+                                                 k_tok_stride, v_tok_stride, eps, turns, gemma,
+                                                 rot, rope->interleaved, mrope ? 1 : 0,
+                                                 dtype == NR_BF16, stream),
+                   "nr_qk_norm_rope_cache launch");
+}
+
+nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
+                           const int32_t* block_table, int64_t table_width,
+                           const int32_t* cu_seqlens, int64_t seqs, int64_t rows, nr_dtype dtype,
+                           cudaStream_t stream) {
+  CallRange range("nr_kv_cache_read");
+  const char* fn = "nr_kv_cache_read";
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (rows < 0 || seqs < 0 || table_width < 0)
+    return fail(NR_ERR_SHAPE, "%s: need rows, seqs and table_width >= 0", fn);
+  if (rows > INT32_MAX || seqs >= INT32_MAX || table_width > INT32_MAX)
+    return fail(NR_ERR_SHAPE, "%s: rows, seqs or table_width too large", fn);
+  const bool empty = rows == 0 || seqs == 0;
+  nr::KvCacheArgs args;
+  if (const nr_status s = check_cache(fn, cache, !empty, &args)) return s;
+  if (empty) return ok();
+  if (!k_out || !v_out || !cu_seqlens || (!block_table && table_width > 0))
+    return fail(NR_ERR_NULL, "%s: k_out, v_out, block_table and cu_seqlens must be non-NULL", fn);
+  if (!aligned16(k_out) || !aligned16(v_out) || misaligned(block_table, 4) ||
+      misaligned(cu_seqlens, 4))
+    return fail(NR_ERR_ALIGN, "%s: outputs must be 16-byte aligned, the tables 4-byte", fn);
+  const int64_t bytes = rows * cache->heads * cache->head_dim * elem_size(dtype);
+  const Region rk = dense(k_out, bytes), rv = dense(v_out, bytes);
+  const Region table = dense(block_table, seqs * table_width * 4);
+  const Region cu = dense(cu_seqlens, (seqs + 1) * 4);
+  const CacheRegions held(*cache);
+  if (overlap(rk, rv) || held.overlaps(rk) || held.overlaps(rv) || overlap(rk, table) ||
+      overlap(rv, table) || overlap(rk, cu) || overlap(rv, cu))
+    return fail(NR_ERR_ALIAS, "%s: an output overlaps the other, the cache or a table", fn);
+  return from_cuda(nr::launch_kv_read(args, k_out, v_out, block_table, table_width, cu_seqlens,
+                                      seqs, rows, dtype == NR_BF16, stream),
+                   "nr_kv_cache_read launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+nr_status check_group_norm_sizes(const char* fn, int64_t samples, int64_t space, int64_t channels,
+                                 int64_t groups, nr_dtype dtype) {
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (samples < 0 || space < 0 || channels <= 0 || groups <= 0)
+    return fail(NR_ERR_SHAPE, "%s: need samples, space >= 0 and channels, groups > 0", fn);
+  if (channels % groups != 0)
+    return fail(NR_ERR_SHAPE, "%s: %lld channels do not divide into %lld groups", fn,
+                (long long)channels, (long long)groups);
+  const int vec = vec_elems(dtype);
+  if (channels % vec != 0)
+    return fail(NR_ERR_UNSUPPORTED, "%s: channels = %lld is not a multiple of %d", fn,
+                (long long)channels, vec);
+  if (channels > (1 << 20) || samples > INT32_MAX || space > INT64_MAX / 16 / channels ||
+      (samples > 0 && space * channels > INT64_MAX / 16 / samples))
+    return fail(NR_ERR_SHAPE, "%s: samples, space or channels too large", fn);
+  if (samples > 0 && space > 0 &&
+      nr::group_norm_blocks(samples, space, channels, groups, dtype == NR_BF16) > INT32_MAX)
+    return fail(NR_ERR_SHAPE, "%s: too many samples for one launch", fn);
+  return NR_OK;
+}
+
+// What both directions share.
+nr_status check_group_norm(const char* fn, const nr::GroupNormArgs& a, nr_dtype w_dtype,
+                           nr_activation act, nr_dtype dtype, int64_t workspace_bytes) {
+  if (!valid_dtype(w_dtype))
+    return fail(NR_ERR_DTYPE, "%s: unknown weight dtype %d", fn, (int)w_dtype);
+  if (act != NR_ACT_NONE && act != NR_ACT_SILU)
+    return fail(NR_ERR_VALUE, "%s: unknown activation %d", fn, (int)act);
+  if (a.samples == 0 || a.space == 0) return NR_OK;
+  if (!a.out || !a.x || !a.mean || !a.rstd || !a.workspace)
+    return fail(NR_ERR_NULL, "%s: the tensors, mean, rstd and workspace must be non-NULL", fn);
+  if ((a.w == nullptr) != (a.b == nullptr))
+    return fail(NR_ERR_NULL, "%s: w and b are given together or not at all", fn);
+  if (!aligned16(a.out) || !aligned16(a.x) || !aligned16(a.w) || !aligned16(a.b) ||
+      !aligned16(a.workspace) || misaligned(a.mean, 4) || misaligned(a.rstd, 4))
+    return fail(NR_ERR_ALIGN, "%s: pointers must be 16-byte aligned (mean and rstd 4-byte)", fn);
+  const int64_t need = nr::group_norm_workspace(a.samples, a.space, a.channels, a.groups,
+                                                dtype == NR_BF16);
+  if (workspace_bytes < need)
+    return fail(NR_ERR_SHAPE, "%s: the workspace has %lld bytes, %lld are needed", fn,
+                (long long)workspace_bytes, (long long)need);
+  return NR_OK;
+}
+
+bool any_overlap(const Region* all, int n, const Region& one) {
+  for (int i = 0; i < n; i++)
+    if (overlap(all[i], one)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channels,
+                                  int64_t groups, nr_dtype dtype, int64_t* bytes) {
+  const char* fn = "nr_group_norm_workspace";
+  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+    return s;
+  if (bytes == nullptr) return fail(NR_ERR_NULL, "%s: bytes must be non-NULL", fn);
+  *bytes = samples == 0 || space == 0
+               ? 0
+               : nr::group_norm_workspace(samples, space, channels, groups, dtype == NR_BF16);
+  return ok();
+}
+
+nr_status nr_group_norm(void* out, float* mean, float* rstd, const void* x, const void* w,
+                        const void* b, nr_dtype w_dtype, int64_t samples, int64_t space,
+                        int64_t channels, int64_t groups, float eps, nr_activation act,
+                        nr_dtype dtype, void* workspace, int64_t workspace_bytes,
+                        cudaStream_t stream) {
+  CallRange range("nr_group_norm");
+  const char* fn = "nr_group_norm";
+  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+    return s;
+  if (!eps_ok(eps)) return fail(NR_ERR_VALUE, "%s: eps must be finite and >= 0", fn);
+  nr::GroupNormArgs a = {};
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.x = x;
+  a.w = w;
+  a.b = b;
+  a.w_is_bf16 = w_dtype == NR_BF16;
+  a.samples = samples;
+  a.space = space;
+  a.channels = channels;
+  a.groups = groups;
+  a.eps = eps;
+  a.silu = act == NR_ACT_SILU;
+  a.workspace = workspace;
+  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, dtype, workspace_bytes)) return s;
+  if (samples == 0 || space == 0) return ok();
+  const int64_t bytes = samples * space * channels * elem_size(dtype);
+  const int64_t wb = channels * elem_size(w_dtype), stats = samples * groups * 4;
+  const Region ro = dense(out, bytes), rx = dense(x, bytes);
+  const Region rm = dense(mean, stats), rr = dense(rstd, stats);
+  const Region ws = dense(workspace, workspace_bytes);
+  const Region ins[] = {rx, dense(w, w ? wb : 0), dense(b, b ? wb : 0)};
+  if ((out != x && overlap(ro, rx)) || any_overlap(ins + 1, 2, ro) || any_overlap(ins, 3, rm) ||
+      any_overlap(ins, 3, rr) || any_overlap(ins, 3, ws) || overlap(ro, rm) || overlap(ro, rr) ||
+      overlap(ro, ws) || overlap(rm, rr) || overlap(rm, ws) || overlap(rr, ws))
+    return fail(NR_ERR_ALIAS, "%s: an output or the workspace overlaps another tensor", fn);
+  return from_cuda(nr::launch_group_norm(a, dtype == NR_BF16, stream), "nr_group_norm launch");
+}
+
+nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, const void* x,
+                                 const float* mean, const float* rstd, const void* w,
+                                 const void* b, nr_dtype w_dtype, int64_t samples, int64_t space,
+                                 int64_t channels, int64_t groups, nr_activation act,
+                                 nr_dtype dtype, void* workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream) {
+  CallRange range("nr_group_norm_backward");
+  const char* fn = "nr_group_norm_backward";
+  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+    return s;
+  nr::GroupNormArgs a = {};
+  a.out = dx;
+  a.dw = dw;
+  a.db = db;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dy = dy;
+  a.x = x;
+  a.w = w;
+  a.b = b;
+  a.w_is_bf16 = w_dtype == NR_BF16;
+  a.samples = samples;
+  a.space = space;
+  a.channels = channels;
+  a.groups = groups;
+  a.silu = act == NR_ACT_SILU;
+  a.workspace = workspace;
+  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, dtype, workspace_bytes)) return s;
+  if (samples == 0 || space == 0) return ok();
+  if (!dy) return fail(NR_ERR_NULL, "%s: dy must be non-NULL", fn);
+  if ((dw != nullptr) != (w != nullptr) || (db != nullptr) != (w != nullptr))
+    return fail(NR_ERR_NULL, "%s: dw and db are given exactly when w and b are", fn);
+  if (!aligned16(dy) || !aligned16(dw) || !aligned16(db))
+    return fail(NR_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
+  const int64_t bytes = samples * space * channels * elem_size(dtype);
+  const int64_t wb = channels * elem_size(w_dtype), stats = samples * groups * 4;
+  const Region ro = dense(dx, bytes), rw = dense(dw, dw ? wb : 0), rb = dense(db, db ? wb : 0);
+  const Region ws = dense(workspace, workspace_bytes);
+  const Region ins[] = {dense(dy, bytes),        dense(x, bytes),          dense(mean, stats),
+                        dense(rstd, stats),      dense(w, w ? wb : 0),     dense(b, b ? wb : 0)};
+  if ((dx != dy && overlap(ro, ins[0])) || (dx != x && overlap(ro, ins[1])) ||
+      any_overlap(ins + 2, 4, ro) || any_overlap(ins, 6, rw) || any_overlap(ins, 6, rb) ||
+      any_overlap(ins, 6, ws) || overlap(ro, rw) || overlap(ro, rb) || overlap(ro, ws) ||
+      overlap(rw, rb) || overlap(rw, ws) || overlap(rb, ws))
+    return fail(NR_ERR_ALIAS, "%s: an output or the workspace overlaps another tensor", fn);
+  return from_cuda(nr::launch_group_norm_backward(a, dtype == NR_BF16, stream),
+                   "nr_group_norm_backward launch");
+}
+
+}  // extern "C"
+
 extern "C" {
 
 nr_status nr_device_status(cudaStream_t stream) {
@@ -454,6 +852,9 @@ nr_status nr_device_status(cudaStream_t stream) {
   if (bits & nr::kStatusBitQkBulkWait)
     return fail(NR_ERR_TIMEOUT, "nr_device_status: a bounded wait for a bulk copy ran out in the "
                                 "Q/K norm + RoPE kernel (status bits 0x%x)", bits);
+  if (bits & nr::kStatusBitCacheBulkWait)
+    return fail(NR_ERR_TIMEOUT, "nr_device_status: a bounded wait for a bulk copy ran out in the "
+                                "Q/K norm + RoPE + cache kernel (status bits 0x%x)", bits);
   if (bits != 0)
     return fail(NR_ERR_TIMEOUT, "nr_device_status: the wait probe's wait ran out (status bits "
                                 "0x%x)", bits);

@@ -133,9 +133,66 @@ cudaError_t launch_qk_norm_rope(void* q_out, void* k_out, const void* q, const v
                                 float eps, const RopeTurns& turns, int gemma, int64_t rotary_dim,
                                 int interleaved, int mrope, int is_bf16, cudaStream_t stream);
 
+// A quantised paged cache (nr_kv_cache), its fields checked.
+struct KvCacheArgs {
+  unsigned char* k_codes;
+  unsigned char* v_codes;
+  unsigned char* k_scales;
+  unsigned char* v_scales;
+  int64_t blocks, block_size, heads, head_dim;
+  int64_t code_block_stride, scale_block_stride;  // bytes
+  bool fp4;
+};
+
+cudaError_t launch_kv_write(const KvCacheArgs& cache, const void* k, const void* v,
+                            const int64_t* slots, int64_t tokens, int64_t k_stride,
+                            int64_t v_stride, int is_bf16, cudaStream_t stream);
+
+cudaError_t launch_kv_read(const KvCacheArgs& cache, void* k_out, void* v_out,
+                           const int32_t* table, int64_t width, const int32_t* cu, int64_t seqs,
+                           int64_t rows, int is_bf16, cudaStream_t stream);
+
+cudaError_t launch_qk_norm_rope_cache(const KvCacheArgs& cache, void* q_out, const void* q,
+                                      const void* k, const void* v, const void* wq,
+                                      const void* wk, int w_is_bf16, const int32_t* positions,
+                                      const int64_t* slots, int64_t tokens, int64_t hq,
+                                      int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                      float eps, const RopeTurns& turns, int gemma,
+                                      int64_t rotary_dim, int interleaved, int mrope, int is_bf16,
+                                      cudaStream_t stream);
+
+// Group norm, forward (out, mean, rstd written) and backward (out is dx; mean
+// and rstd are read).  w and b are both NULL or both given.
+struct GroupNormArgs {
+  void* out;
+  void* dw;
+  void* db;
+  float* mean;
+  float* rstd;
+  const void* dy;
+  const void* x;
+  const void* w;
+  const void* b;
+  int w_is_bf16;
+  int64_t samples, space, channels, groups;
+  float eps;
+  int silu;
+  void* workspace;
+};
+
+// Bytes that either direction needs, and blocks of its largest launch.
+int64_t group_norm_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups,
+                             int is_bf16);
+int64_t group_norm_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups,
+                          int is_bf16);
+cudaError_t launch_group_norm(const GroupNormArgs& args, int is_bf16, cudaStream_t stream);
+cudaError_t launch_group_norm_backward(const GroupNormArgs& args, int is_bf16,
+                                       cudaStream_t stream);
+
 // Device status word: bits set by kernels whose bounded waits ran out.
 constexpr unsigned kStatusBitQkBulkWait = 1u;
 constexpr unsigned kStatusBitProbeWait = 2u;
+constexpr unsigned kStatusBitCacheBulkWait = 4u;
 
 // Device address of the current device's status word (status.cu), looked up
 // once per device.  Kernels that bound a wait take it as an argument.
