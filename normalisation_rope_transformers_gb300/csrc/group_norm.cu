@@ -25,8 +25,11 @@ namespace nr {
 namespace {
 
 constexpr int kGnThreads = 256;
-// Blocks that the geometry aims at: four of 256 threads on each of 152 SMs.
-constexpr int64_t kGnBlocks = 152 * 4;
+// Blocks that the geometry aims at: as many as the kernels' registers let
+// reside on 152 SMs, so that a pass is one wave.
+constexpr int kGnPerSm = 3, kGnGradPerSm = 2;
+// Rows that a thread loads before it works on them (backward: of each tensor).
+constexpr int kGnRows = 8, kGnGradRows = 4;
 
 // Columns and rows of one launch; the same for every pass of a call.
 struct GnGeom {
@@ -40,7 +43,8 @@ struct GnGeom {
   int chunks;
 };
 
-GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups, int vec) {
+GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups, int vec,
+                   int per_sm) {
   GnGeom g;
   g.space = space;
   g.channels = static_cast<int>(channels);
@@ -52,7 +56,7 @@ GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t gro
   g.lanes = kGnThreads / g.tile_cols;
   // at least four rows a thread, so that its loads overlap
   const int64_t most = (space + 4 * g.lanes - 1) / (4 * g.lanes);
-  int64_t want = kGnBlocks / (samples * g.tiles);
+  int64_t want = 152 * per_sm / (samples * g.tiles);
   want = want < 1 ? 1 : want > most ? most : want;
   g.rows = (space + want - 1) / want;
   g.chunks = static_cast<int>((space + g.rows - 1) / g.rows);
@@ -93,15 +97,18 @@ __device__ __forceinline__ void gn_params(const void* p, int is_bf16, int channe
   }
 }
 
-// sigmoid(z) from t = e^-|z| in (0, 1], which never overflows; the hardware
-// exponential and reciprocal (about 1e-6) where the result is rounded to bf16.
+// sigmoid(z).  Where the result is rounded to bf16: the hardware exponential
+// and reciprocal (each about 2^-22), two instructions of the special unit a
+// value; below z = -88 the exponential is infinite and the sigmoid zero, off by
+// less than 2^-126.  For f32 from t = e^-|z|, which never overflows.
 template <typename T>
 __device__ __forceinline__ float gn_sigmoid(float z);
 template <>
 __device__ __forceinline__ float gn_sigmoid<__nv_bfloat16>(float z) {
-  const float t = exp2f(-fabsf(z) * 1.4426950408889634f);
-  const float r = __fdividef(1.0f, 1.0f + t);
-  return z >= 0.0f ? r : t * r;
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
 }
 template <>
 __device__ __forceinline__ float gn_sigmoid<float>(float z) {
@@ -120,7 +127,7 @@ __device__ __forceinline__ float gn_sigmoid<float>(float z) {
 // part (group, tile) is at place group + tile, which no other part has, as the
 // groups of a tile are never below those of the tile before.
 template <typename T>
-__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(float2* __restrict__ parts,
+__global__ void __launch_bounds__(kGnThreads, kGnPerSm) gn_stats_kernel(float2* __restrict__ parts,
                                                               const T* __restrict__ x,
                                                               const GnGeom g) {
   constexpr int N = Vec<T>::N;
@@ -129,31 +136,34 @@ __global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(float2* __restrict
   const GnPlace at(g, blockIdx.x, N);
   const int width = g.tile_cols * N;
   if (at.active && at.lane < g.lanes) {
-    const uint4* p = reinterpret_cast<const uint4*>(x) + (at.sample * g.space) * g.cols + at.col;
     float first[N], s1[N], s2[N];
 #pragma unroll
     for (int e = 0; e < N; e++) first[e] = s1[e] = s2[e] = 0.0f;
-    int64_t r = at.row0 + at.lane;
-    if (r < at.row1) Vec<T>::unpack(ld_stream(p + r * g.cols), first);
-    int64_t count = 0;
-    auto add = [&](const uint4& v) {
-      float f[N];
-      Vec<T>::unpack(v, f);
+    const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
+    const uint4* p = reinterpret_cast<const uint4*>(x) +
+                     (at.sample * g.space + at.row0 + at.lane) * g.cols + at.col;
+    const int rows = static_cast<int>(at.row1 - at.row0);
+    int count = 0;
+    for (int r = at.lane; r < rows; r += kGnRows * g.lanes) {
+      uint4 v[kGnRows];
 #pragma unroll
-      for (int e = 0; e < N; e++) {
-        const float d = f[e] - first[e];
-        s1[e] += d;
-        s2[e] = fmaf(d, d, s2[e]);
-      }
-    };
-    for (; r + 3 * g.lanes < at.row1; r += 4 * g.lanes, count += 4) {
-      uint4 v[4];
+      for (int u = 0; u < kGnRows; u++, p += step)
+        if (r + u * g.lanes < rows) v[u] = ld_stream(p);
+      if (count == 0) Vec<T>::unpack(v[0], first);
 #pragma unroll
-      for (int u = 0; u < 4; u++) v[u] = ld_stream(p + (r + u * g.lanes) * g.cols);
+      for (int u = 0; u < kGnRows; u++)
+        if (r + u * g.lanes < rows) {
+          float f[N];
+          Vec<T>::unpack(v[u], f);
 #pragma unroll
-      for (int u = 0; u < 4; u++) add(v[u]);
+          for (int e = 0; e < N; e++) {
+            const float d = f[e] - first[e];
+            s1[e] += d;
+            s2[e] = fmaf(d, d, s2[e]);
+          }
+          count++;
+        }
     }
-    for (; r < at.row1; r += g.lanes, count++) add(ld_stream(p + r * g.cols));
     const float inv = count > 0 ? 1.0f / static_cast<float>(count) : 0.0f;
     float2* o = sm + at.lane * width + (at.channel - at.tile * width);
 #pragma unroll
@@ -245,7 +255,7 @@ struct GnParams {
 };
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(T* __restrict__ out,
+__global__ void __launch_bounds__(kGnThreads, kGnPerSm) gn_apply_kernel(T* __restrict__ out,
                                                               const T* __restrict__ x,
                                                               const float* __restrict__ mean,
                                                               const float* __restrict__ rstd,
@@ -263,28 +273,29 @@ __global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(T* __restrict__ ou
     mu[e] = mean[i];
     a[e] *= rstd[i];
   }
-  const int64_t base = at.sample * g.space * g.cols + at.col;
+  const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
+  const int rows = static_cast<int>(at.row1 - at.row0);
+  const int64_t base = (at.sample * g.space + at.row1 - 1 - at.lane) * g.cols + at.col;
   const uint4* p = reinterpret_cast<const uint4*>(x) + base;
   uint4* o = reinterpret_cast<uint4*>(out) + base;
-  auto write = [&](int64_t r, const uint4& v) {
-    float f[N];
-    Vec<T>::unpack(v, f);
+  for (int r = at.lane; r < rows; r += kGnRows * g.lanes) {
+    uint4 v[kGnRows];
 #pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float z = fmaf(f[e] - mu[e], a[e], b[e]);
-      f[e] = SILU ? z * gn_sigmoid<T>(z) : z;
-    }
-    st_stream(o + r * g.cols, Vec<T>::pack(f));
-  };
-  int64_t r = at.row1 - 1 - at.lane;
-  for (; r - 3 * g.lanes >= at.row0; r -= 4 * g.lanes) {
-    uint4 v[4];
+    for (int u = 0; u < kGnRows; u++, p -= step)
+      if (r + u * g.lanes < rows) v[u] = ld_stream(p);
 #pragma unroll
-    for (int u = 0; u < 4; u++) v[u] = ld_coherent(p + (r - u * g.lanes) * g.cols);
+    for (int u = 0; u < kGnRows; u++, o -= step)
+      if (r + u * g.lanes < rows) {
+        float f[N];
+        Vec<T>::unpack(v[u], f);
 #pragma unroll
-    for (int u = 0; u < 4; u++) write(r - u * g.lanes, v[u]);
+        for (int e = 0; e < N; e++) {
+          const float z = fmaf(f[e] - mu[e], a[e], b[e]);
+          f[e] = SILU ? z * gn_sigmoid<T>(z) : z;
+        }
+        st_stream(o, Vec<T>::pack(f));
+      }
   }
-  for (; r >= at.row0; r -= g.lanes) write(r, ld_coherent(p + r * g.cols));
 }
 
 // ---------------------------------------------------------------------------
@@ -308,7 +319,7 @@ struct GnGradIn {
 
 // Per channel and chunk: sum dz and sum dz * (x - mean).
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_grad_stats_kernel(float2* __restrict__ parts,
+__global__ void __launch_bounds__(kGnThreads, kGnGradPerSm) gn_grad_stats_kernel(float2* __restrict__ parts,
                                                                    const GnGradIn in,
                                                                    const GnGeom g) {
   constexpr int N = Vec<T>::N;
@@ -327,33 +338,34 @@ __global__ void __launch_bounds__(kGnThreads) gn_grad_stats_kernel(float2* __res
       a[e] *= in.rstd[i];
       s1[e] = s2[e] = 0.0f;
     }
-    const int64_t base = at.sample * g.space * g.cols + at.col;
+    const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
+    const int rows = static_cast<int>(at.row1 - at.row0);
+    const int64_t base = (at.sample * g.space + at.row0 + at.lane) * g.cols + at.col;
     const uint4* px = static_cast<const uint4*>(in.x) + base;
     const uint4* pd = static_cast<const uint4*>(in.dy) + base;
-    auto add = [&](const uint4& vx, const uint4& vd) {
-      float f[N], d[N];
-      Vec<T>::unpack(vx, f);
-      Vec<T>::unpack(vd, d);
+    for (int r = at.lane; r < rows; r += kGnGradRows * g.lanes) {
+      uint4 vx[kGnGradRows], vd[kGnGradRows];
 #pragma unroll
-      for (int e = 0; e < N; e++) {
-        const float c = f[e] - mu[e];
-        const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
-        s1[e] += dz;
-        s2[e] = fmaf(dz, c, s2[e]);
-      }
-    };
-    int64_t r = at.row0 + at.lane;
-    for (; r + g.lanes < at.row1; r += 2 * g.lanes) {
-      uint4 vx[2], vd[2];
+      for (int u = 0; u < kGnGradRows; u++, px += step, pd += step)
+        if (r + u * g.lanes < rows) {
+          vx[u] = ld_stream(px);
+          vd[u] = ld_stream(pd);
+        }
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
-        vx[u] = ld_stream(px + (r + u * g.lanes) * g.cols);
-        vd[u] = ld_stream(pd + (r + u * g.lanes) * g.cols);
-      }
+      for (int u = 0; u < kGnGradRows; u++)
+        if (r + u * g.lanes < rows) {
+          float f[N], d[N];
+          Vec<T>::unpack(vx[u], f);
+          Vec<T>::unpack(vd[u], d);
 #pragma unroll
-      for (int u = 0; u < 2; u++) add(vx[u], vd[u]);
+          for (int e = 0; e < N; e++) {
+            const float c = f[e] - mu[e];
+            const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
+            s1[e] += dz;
+            s2[e] = fmaf(dz, c, s2[e]);
+          }
+        }
     }
-    if (r < at.row1) add(ld_stream(px + r * g.cols), ld_stream(pd + r * g.cols));
     float2* o = sm + at.lane * width + (at.channel - at.tile * width);
 #pragma unroll
     for (int e = 0; e < N; e++) o[e] = make_float2(s1[e], s2[e]);
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(32 * kGnSumLanes) gn_grad_join_kernel(
 }
 
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads) gn_grad_apply_kernel(
+__global__ void __launch_bounds__(kGnThreads, kGnGradPerSm) gn_grad_apply_kernel(
     T* __restrict__ dx, void* __restrict__ dw, void* __restrict__ db,
     const float2* __restrict__ sums, const GnGradIn in, const GnGeom g, int samples) {
   constexpr int N = Vec<T>::N;
@@ -467,34 +479,35 @@ __global__ void __launch_bounds__(kGnThreads) gn_grad_apply_kernel(
     k1[e] = rs * grp_mean[grp - g0].x;
     k2[e] = rs * rs * grp_mean[grp - g0].y;
   }
-  const int64_t base = at.sample * g.space * g.cols + at.col;
+  const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
+  const int rows = static_cast<int>(at.row1 - at.row0);
+  const int64_t base = (at.sample * g.space + at.row1 - 1 - at.lane) * g.cols + at.col;
   const uint4* px = static_cast<const uint4*>(in.x) + base;
   const uint4* pd = static_cast<const uint4*>(in.dy) + base;
   uint4* o = reinterpret_cast<uint4*>(dx) + base;
-  auto write = [&](int64_t r, const uint4& vx, const uint4& vd) {
-    float f[N], d[N];
-    Vec<T>::unpack(vx, f);
-    Vec<T>::unpack(vd, d);
+  for (int r = at.lane; r < rows; r += kGnGradRows * g.lanes) {
+    uint4 vx[kGnGradRows], vd[kGnGradRows];
 #pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float c = f[e] - mu[e];
-      const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
-      f[e] = fmaf(a[e], dz, -fmaf(c, k2[e], k1[e]));
-    }
-    st_stream(o + r * g.cols, Vec<T>::pack(f));
-  };
-  int64_t r = at.row1 - 1 - at.lane;
-  for (; r - g.lanes >= at.row0; r -= 2 * g.lanes) {
-    uint4 vx[2], vd[2];
+    for (int u = 0; u < kGnGradRows; u++, px -= step, pd -= step)
+      if (r + u * g.lanes < rows) {
+        vx[u] = ld_stream(px);
+        vd[u] = ld_stream(pd);
+      }
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-      vx[u] = ld_coherent(px + (r - u * g.lanes) * g.cols);
-      vd[u] = ld_coherent(pd + (r - u * g.lanes) * g.cols);
-    }
+    for (int u = 0; u < kGnGradRows; u++, o -= step)
+      if (r + u * g.lanes < rows) {
+        float f[N], d[N];
+        Vec<T>::unpack(vx[u], f);
+        Vec<T>::unpack(vd[u], d);
 #pragma unroll
-    for (int u = 0; u < 2; u++) write(r - u * g.lanes, vx[u], vd[u]);
+        for (int e = 0; e < N; e++) {
+          const float c = f[e] - mu[e];
+          const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
+          f[e] = fmaf(a[e], dz, -fmaf(c, k2[e], k1[e]));
+        }
+        st_stream(o, Vec<T>::pack(f));
+      }
   }
-  if (r >= at.row0) write(r, ld_coherent(px + r * g.cols), ld_coherent(pd + r * g.cols));
 }
 
 // Threads of a block: its columns and lanes, in whole warps (the warps of the
@@ -509,7 +522,7 @@ unsigned gn_grid(const GnGeom& g, int64_t samples) {
 
 template <typename T>
 cudaError_t gn_forward(const GroupNormArgs& a, cudaStream_t s) {
-  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N);
+  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N, kGnPerSm);
   const GnParams prm{a.w, a.b, a.w_is_bf16};
   float2* parts = static_cast<float2*>(a.workspace);
   const T* x = static_cast<const T*>(a.x);
@@ -528,7 +541,7 @@ cudaError_t gn_forward(const GroupNormArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t gn_backward(const GroupNormArgs& a, cudaStream_t s) {
-  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N);
+  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N, kGnGradPerSm);
   const GnGradIn in{a.dy, a.x, a.mean, a.rstd, GnParams{a.w, a.b, a.w_is_bf16}};
   float2* parts = static_cast<float2*>(a.workspace);
   float2* sums = parts + a.samples * g.chunks * a.channels;
@@ -553,15 +566,17 @@ cudaError_t gn_backward(const GroupNormArgs& a, cudaStream_t s) {
 
 int64_t group_norm_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                              int is_bf16) {
-  const GnGeom g = gn_geometry(samples, space, channels, groups, is_bf16 ? 8 : 4);
-  const int64_t forward = samples * g.chunks * (groups + g.tiles);
-  const int64_t backward = samples * (g.chunks + 1) * channels;
+  const int vec = is_bf16 ? 8 : 4;
+  const GnGeom f = gn_geometry(samples, space, channels, groups, vec, kGnPerSm);
+  const GnGeom b = gn_geometry(samples, space, channels, groups, vec, kGnGradPerSm);
+  const int64_t forward = samples * f.chunks * (groups + f.tiles);
+  const int64_t backward = samples * (b.chunks + 1) * channels;
   return static_cast<int64_t>(sizeof(float2)) * (forward > backward ? forward : backward);
 }
 
 int64_t group_norm_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                           int is_bf16) {
-  const GnGeom g = gn_geometry(samples, space, channels, groups, is_bf16 ? 8 : 4);
+  const GnGeom g = gn_geometry(samples, space, channels, groups, is_bf16 ? 8 : 4, kGnPerSm);
   const int64_t blocks = g.chunks * static_cast<int64_t>(g.tiles);
   const int64_t joins = groups > (channels + 31) / 32 ? groups : (channels + 31) / 32;
   return samples * (blocks > joins ? blocks : joins);

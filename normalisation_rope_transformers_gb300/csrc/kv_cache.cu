@@ -1,9 +1,9 @@
 // Quantised paged K/V cache for sm_103a: writing new tokens, and reading
 // sequences back.
 //
-// Write: a group of L lanes owns one (token, head) row, eight values a lane,
-// so the row's (FP8) or the 32-element group's (MXFP4) largest magnitude is a
-// butterfly over lanes, and the codes leave as one store a lane.  Each input
+// Write: a group of L lanes owns one (token, head) row, each lane units of
+// eight values, so the row's (FP8) or the 32-element group's (MXFP4) largest
+// magnitude is a butterfly over lanes.  Each input
 // byte is read once and each code written once; HBM (large calls) or latency
 // (decode) bounds it.
 //
@@ -22,22 +22,12 @@ template <typename T>
 struct Unit;
 template <>
 struct Unit<__nv_bfloat16> {
-  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float (&f)[kUnit]) {
-    Vec<__nv_bfloat16>::unpack(ld_stream(p), f);
-  }
   __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&f)[kUnit]) {
     st_stream(p, Vec<__nv_bfloat16>::pack(f));
   }
 };
 template <>
 struct Unit<float> {
-  __device__ __forceinline__ static void load(const float* p, float (&f)[kUnit]) {
-    float a[4], b[4];
-    Vec<float>::unpack(ld_stream(p), a);
-    Vec<float>::unpack(ld_stream(p + 4), b);
-#pragma unroll
-    for (int e = 0; e < 4; e++) f[e] = a[e], f[e + 4] = b[e];
-  }
   __device__ __forceinline__ static void store(float* p, const float (&f)[kUnit]) {
     const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
     st_stream(p, Vec<float>::pack(a));
@@ -56,113 +46,146 @@ struct WriteArgs {
   int units;      // head_dim / 8
 };
 
-// L lanes a row, NV units a lane (head_dim <= 8 * L * NV), ROWS rows a lane
-// group in flight.  blockIdx.y: 0 K, 1 V.
-template <typename T, bool FP4, int L, int NV, int ROWS>
+// Raw words of a unit (8 values), the largest magnitude among them, and the
+// values themselves.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = ld_stream(p); }
+  // Of the packed pairs, sign bits cleared: two values an instruction.
+  __device__ __forceinline__ float top() const {
+    const uint32_t m = max2(max2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                            max2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  __device__ __forceinline__ void get(float (&f)[kUnit]) const {
+    Vec<__nv_bfloat16>::unpack(v, f);
+  }
+  // The larger of each pair of halves; a NaN counts as nothing.
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
+template <>
+struct Raw<float> {
+  uint4 v, w;
+  __device__ __forceinline__ void zero() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const float* p) {
+    v = ld_stream(p);
+    w = ld_stream(p + 4);
+  }
+  __device__ __forceinline__ float top() const {
+    float f[kUnit];
+    get(f);
+    return max_abs(f);
+  }
+  __device__ __forceinline__ void get(float (&f)[kUnit]) const {
+    float a[4], b[4];
+    Vec<float>::unpack(v, a);
+    Vec<float>::unpack(w, b);
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[e] = a[e], f[e + 4] = b[e];
+  }
+};
+
+// L lanes a row, NV units a lane (head_dim <= 8 * L * NV); lane l has units l,
+// l + L, ...  blockIdx.y: 0 K, 1 V.  Few lanes and several units a lane: what a
+// row costs once (its slot, its scale's division, the butterfly) is shared by
+// more values.  At [16381, 8, 128] bf16 -> fp8: 16 lanes with one unit 33 us.
+template <typename T, bool FP4, int L, int NV>
 __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs a) {
   constexpr int GW = kWarp / L;
   pdl_enter();
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
-  const int g = lane32 / L, l = lane32 % L;
-  const uint32_t first =
-      (blockIdx.x * (kCacheThreads / kWarp) + warp) * static_cast<uint32_t>(GW * ROWS) + g;
+  const int l = lane32 % L;
+  const uint32_t row =
+      (blockIdx.x * (kCacheThreads / kWarp) + warp) * static_cast<uint32_t>(GW) + lane32 / L;
   const bool is_v = blockIdx.y != 0;
-  const T* src = static_cast<const T*>(is_v ? a.src[1] : a.src[0]);
-  const int64_t stride = is_v ? a.stride[1] : a.stride[0];
   const CacheSide side = is_v ? a.side[1] : a.side[0];
   const int dim = a.units * kUnit;
 
-  // every load before any use; a padded token's row is in bounds, and its
-  // values go nowhere
-  float x[ROWS][NV][kUnit];
-  int64_t slot[ROWS];
-  uint32_t head[ROWS];
+  // Every load before any use; a padded token's row is in bounds, and its
+  // values go nowhere.
+  Raw<T> x[NV];
+  int64_t slot = -1;
+  uint32_t head = 0;
 #pragma unroll
-  for (int i = 0; i < ROWS; i++) {
-    const uint32_t row = first + i * GW;
-    slot[i] = -1;
-    head[i] = 0;
+  for (int j = 0; j < NV; j++) x[j].zero();
+  if (row < a.rows) {
+    const uint32_t tok = a.heads.quot(row);
+    head = row - tok * a.heads.div;
+    slot = __ldg(a.slots + tok);
+    const T* p = static_cast<const T*>(is_v ? a.src[1] : a.src[0]) +
+                 tok * (is_v ? a.stride[1] : a.stride[0]) + head * dim;
 #pragma unroll
     for (int j = 0; j < NV; j++)
-#pragma unroll
-      for (int e = 0; e < kUnit; e++) x[i][j][e] = 0.0f;
-    if (row < a.rows) {
-      const uint32_t tok = a.heads.quot(row);
-      head[i] = row - tok * a.heads.div;
-      slot[i] = __ldg(a.slots + tok);
-      const T* p = src + tok * stride + static_cast<int64_t>(head[i]) * dim;
-#pragma unroll
-      for (int j = 0; j < NV; j++)
-        if (l + j * L < a.units) Unit<T>::load(p + (l + j * L) * kUnit, x[i][j]);
-    }
+      if (l + j * L < a.units) x[j].load(p + (l + j * L) * kUnit);
   }
+  float top[NV], row_top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < ROWS; i++) {
-    float top[NV], row_top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; j++) {
-      top[j] = max_abs(x[i][j]);
-      if (FP4) top[j] = group_max<4>(top[j]);
+  for (int j = 0; j < NV; j++) {
+    top[j] = x[j].top();
+    if (FP4)
+      top[j] = group_max<4>(top[j]);  // units 4i .. 4i + 3: one 32-element group
+    else
       row_top = fmaxf(row_top, top[j]);
-    }
-    if (!FP4) row_top = group_max<L>(row_top);
-    // slots outside the cache (padding) are skipped
-    if (slot[i] < 0 || slot[i] >= a.geo.slots) continue;
-    const int64_t block = a.geo.block_of(slot[i]);
-    const int64_t place = slot[i] - block * a.geo.block_size;
-    unsigned char* codes = side.codes + block * a.geo.code_block_stride + place * a.geo.code_row;
-    unsigned char* scales =
-        side.scales + block * a.geo.scale_block_stride + place * a.geo.scale_row;
-    if (!FP4) {
-      const float am = clamp_scale(row_top), inv = fp8_inverse(am);
-      codes += static_cast<int64_t>(head[i]) * dim;
+  }
+  if (!FP4) row_top = group_max<L>(row_top);
+  // slots outside the cache (padding) are skipped
+  if (slot < 0 || slot >= a.geo.slots) return;
+  const int64_t block = a.geo.block_of(slot);
+  const int64_t place = slot - block * a.geo.block_size;
+  unsigned char* codes = side.codes + block * a.geo.code_block_stride + place * a.geo.code_row;
+  unsigned char* scales = side.scales + block * a.geo.scale_block_stride + place * a.geo.scale_row;
+  float f[kUnit];
+  if (!FP4) {
+    const float am = clamp_scale(row_top), inv = fp8_inverse(am);
+    codes += head * dim;
 #pragma unroll
-      for (int j = 0; j < NV; j++)
-        if (l + j * L < a.units) {
-          uint32_t c[2];
-          fp8_codes(x[i][j], inv, c);
-          st_stream8(codes + (l + j * L) * kUnit, make_uint2(c[0], c[1]));
-        }
-      if (l == 0) reinterpret_cast<float*>(scales)[head[i]] = fp8_scale(am);
-    } else {
-      codes += static_cast<int64_t>(head[i]) * (dim / 2);
-      scales += static_cast<int64_t>(head[i]) * (dim / 32);
+    for (int j = 0; j < NV; j++)
+      if (l + j * L < a.units) {
+        uint32_t c[2];
+        x[j].get(f);
+        fp8_codes(f, inv, c);
+        st_stream8(codes + (l + j * L) * kUnit, make_uint2(c[0], c[1]));
+      }
+    if (l == 0) reinterpret_cast<float*>(scales)[head] = fp8_scale(am);
+  } else {
+    codes += head * (dim / 2);
+    scales += head * (dim / 32);
 #pragma unroll
-      for (int j = 0; j < NV; j++)
-        if (l + j * L < a.units) {
-          const int u = l + j * L;
-          const uint32_t byte = mx_scale_byte(clamp_scale(top[j]));
-          st_stream4(codes + u * (kUnit / 2), fp4_codes(x[i][j], mx_inverse(byte)));
-          if (u % 4 == 0) scales[u / 4] = static_cast<unsigned char>(byte);
-        }
-    }
+    for (int j = 0; j < NV; j++)
+      if (l + j * L < a.units) {
+        const int u = l + j * L;
+        const uint32_t byte = mx_scale_byte(clamp_scale(top[j]));
+        x[j].get(f);
+        st_stream4(codes + u * (kUnit / 2), fp4_codes(f, mx_inverse(byte)));
+        if (u % 4 == 0) scales[u / 4] = static_cast<unsigned char>(byte);
+      }
   }
 }
 
 template <typename T, bool FP4, int L, int NV>
 cudaError_t write_l(const WriteArgs& a, cudaStream_t s) {
-  constexpr int GW = kWarp / L;
-  constexpr int kWarps = kCacheThreads / kWarp;
-  // Large calls keep several rows a lane in flight; small ones spread out.
-  constexpr int ROWS = NV * static_cast<int>(sizeof(T)) >= 8 ? 2 : 4;
-  if (a.rows >= 152u * 8 * kWarps * GW * ROWS) {
-    const unsigned blocks = (a.rows + kWarps * GW * ROWS - 1) / (kWarps * GW * ROWS);
-    return launch_pdl(kv_write_kernel<T, FP4, L, NV, ROWS>, dim3(blocks, 2), dim3(kCacheThreads),
-                      0, s, a);
-  }
-  const unsigned blocks = (a.rows + kWarps * GW - 1) / (kWarps * GW);
-  return launch_pdl(kv_write_kernel<T, FP4, L, NV, 1>, dim3(blocks, 2), dim3(kCacheThreads), 0, s,
-                    a);
+  constexpr unsigned rows = kCacheThreads / L;
+  return launch_pdl(kv_write_kernel<T, FP4, L, NV>, dim3((a.rows + rows - 1) / rows, 2),
+                    dim3(kCacheThreads), 0, s, a);
 }
 
 template <typename T, bool FP4>
 cudaError_t write_t(const WriteArgs& a, cudaStream_t s) {
-  if (a.units <= 2) return write_l<T, FP4, FP4 ? 4 : 2, 1>(a, s);
   if (a.units <= 4) return write_l<T, FP4, 4, 1>(a, s);
-  if (a.units <= 8) return write_l<T, FP4, 8, 1>(a, s);
-  if (a.units <= 16) return write_l<T, FP4, 16, 1>(a, s);
-  if (a.units <= 32) return write_l<T, FP4, 32, 1>(a, s);
-  return write_l<T, FP4, 32, 2>(a, s);
+  if (a.units <= 8) return write_l<T, FP4, 4, 2>(a, s);
+  if (a.units <= 12) return write_l<T, FP4, 4, 3>(a, s);
+  if (a.units <= 16) return write_l<T, FP4, 4, 4>(a, s);
+  if (a.units <= 24) return write_l<T, FP4, 8, 3>(a, s);
+  if (a.units <= 32) return write_l<T, FP4, 8, 4>(a, s);
+  return write_l<T, FP4, 16, 4>(a, s);
 }
 
 // ---------------------------------------------------------------------------

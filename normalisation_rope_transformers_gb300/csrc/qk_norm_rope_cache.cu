@@ -29,7 +29,10 @@ namespace {
 constexpr int kFusedThreads = 128;
 constexpr int kFusedWarps = kFusedThreads / kWarp;
 constexpr int kStages = 3;
-constexpr int kItemBytes = 8192;
+// Bytes of an item: calls of many tokens take whole tokens where they fit (one
+// barrier and one angle table for more rows), small calls spread their rows.
+constexpr int kItemBytesMany = 20 * 1024;
+constexpr int kItemBytesFew = 8 * 1024;
 constexpr long long kFusedWaitLimit = 1LL << 31;  // SM cycles, about one second
 
 struct FusedArgs {
@@ -396,7 +399,7 @@ cudaError_t fused_resident(Kernel kernel, size_t smem, std::atomic<uint64_t>* ca
   int sms = 0, per_sm = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kFusedThreads, smem);
   if (e != cudaSuccess) return e;
@@ -410,8 +413,15 @@ template <typename T, typename WT, int L, bool FP4, bool GEN>
 cudaError_t fused_launch(FusedArgs& a, const RopeTurns& turns, cudaStream_t s) {
   constexpr int row_bytes = FusedSmem<T, L>::D * static_cast<int>(sizeof(T));
   const int rows = a.hq + 2 * a.hk;
-  a.items = static_cast<int>((static_cast<int64_t>(rows) * row_bytes + kItemBytes - 1) / kItemBytes);
+  const int item_bytes = a.tokens * rows * row_bytes >= 152 * 4 * 2 * int64_t(kItemBytesMany)
+                             ? kItemBytesMany
+                             : kItemBytesFew;
+  a.items = static_cast<int>((static_cast<int64_t>(rows) * row_bytes + item_bytes - 1) / item_bytes);
   a.chunk = (rows + a.items - 1) / a.items;
+  // whole passes of the four warps, where that does not outgrow the stage
+  constexpr int pass_rows = kFusedWarps * (kWarp / L);
+  const int even = (a.chunk + pass_rows - 1) / pass_rows * pass_rows;
+  if (a.items > 1 && even * row_bytes <= item_bytes) a.chunk = even;
   a.items = (rows + a.chunk - 1) / a.chunk;
   a.stage_bytes = (static_cast<unsigned>(a.chunk * row_bytes) + 127u) & ~127u;
   const size_t smem = FusedSmem<T, L>::bytes(a.stage_bytes);

@@ -43,7 +43,15 @@ __device__ __forceinline__ float clamp_scale(float a) {
   return fminf(fmaxf(a, kScaleFloor), kScaleCeil);
 }
 
-__device__ __forceinline__ float fp8_scale(float a) { return __fdiv_rn(a, 448.0f); }
+// a / 448 correctly rounded, without a division: q = a * RN(1/448) corrected by
+// its remainder a - 448 q, which is exact.  (The outcome depends on a's 2^23
+// significands alone while nothing underflows; compared with the division for
+// every one of them.)
+__device__ __forceinline__ float fp8_scale(float a) {
+  constexpr float r = 1.0f / 448.0f;
+  const float q = a * r;
+  return fmaf(fmaf(-448.0f, q, a), r, q);
+}
 __device__ __forceinline__ float fp8_inverse(float a) { return __fdiv_rn(448.0f, a); }
 
 // e4m3 codes of N values times `inv`, four to a word.
