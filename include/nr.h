@@ -329,7 +329,7 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
  *             initialised, its contents lost.  Calls that may run at the same
  *             time need workspaces of their own.
  * samples >= 0, space >= 0, groups >= 1 dividing channels; channels a multiple of
- * 8 (bf16) or 4 (f32).  With no elements nothing is written.
+ * 8 (bf16) or 4 (f32), at most 65536.  With no elements nothing is written.
  * eps finite >= 0.
  * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
  */
@@ -446,8 +446,8 @@ nr_status nr_gelu_and_mul(void* out, const void* x, int64_t rows, int64_t inter,
 
 /*
  * Device-side failure report.  Kernels that wait on hardware events (the
- * bulk-copy path of nr_qk_norm_rope waits for its copies on shared-memory
- * barriers) bound every wait (about one second of SM clock); a wait that runs
+ * bulk-copy paths of nr_qk_norm_rope and nr_qk_norm_rope_cache wait for their
+ * copies on shared-memory barriers) bound every wait (about one second of SM clock); a wait that runs
  * out sets a bit in a status word the library keeps on each device, the
  * kernel lets its copies in flight finish and returns, and the outputs of
  * that call are not valid.  nr_device_status works on the device that owns

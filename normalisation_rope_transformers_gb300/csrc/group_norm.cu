@@ -8,77 +8,174 @@
 //     db_c = sum_n S1,  dw_c = sum_n S2,
 //     dx = rstd * (w_c dz - mean_g(w dz) - xhat * mean_g(w dz xhat))
 //
-// A group's values are strided by `channels`, so its statistics need the whole
-// sample: the tensor is read twice (statistics, then the output) and written
-// once, and HBM bounds every pass.  A block owns a range of rows (a chunk) and
-// a tile of vector columns; each thread keeps one 128-bit column of N channels
-// and walks down the rows, so all reads are whole rows, each value belongs to
-// a fixed channel register, and any channels / groups works (a vector may span
-// several groups).  Blocks write partial results, a small kernel joins them in
-// a fixed order (no atomics: the same inputs give the same bits), and the
-// output pass walks each chunk from its end, so that what the statistics pass
-// read last is still in L2.
+// A group's values are strided by `channels` and its statistics need the whole
+// sample, so every value is used twice, far apart: a statistics kernel and an
+// output kernel, both bound by HBM.  The output kernel takes the rows in the
+// opposite order, so that what was read last still comes from L2.  One block
+// fills an SM; each thread copies its vectors many rows ahead into a ring of
+// its own in shared memory (cp.async), which keeps about 150 KB an SM in flight
+// without registers or barriers.
+//
+// Any channels / groups works: a thread keeps one 128-bit column of N channels
+// and walks down the rows, sums stay per channel until the block's end, and a
+// vector may span several groups.  Every sum has a fixed order (no atomics):
+// the same inputs give the same bits.
+//
+// Tried and slower for [1, 1048576, 128] bf16: one cooperative kernel with a
+// barrier between the passes and 170 KB an SM of rows kept on chip (178 us
+// against 134 us for plain loads in two kernels and a joining one).
+#include <atomic>
+
 #include "nr_common.cuh"
 #include "nr_internal.h"
 
 namespace nr {
 namespace {
 
-constexpr int kGnThreads = 256;
-// Blocks that the geometry aims at: as many as the kernels' registers let
-// reside on 152 SMs, so that a pass is one wave.
-constexpr int kGnPerSm = 3, kGnGradPerSm = 2;
-// Rows that a thread loads before it works on them (backward: of each tensor).
-constexpr int kGnRows = 8, kGnGradRows = 4;
+constexpr int kGnSms = 152;
 
-// Columns and rows of one launch; the same for every pass of a call.
+// A direction's block: threads, rows of a lane in a step, steps in the ring.
+template <typename T, bool BACK>
+struct GnBlock {
+  static constexpr int N = Vec<T>::N;
+  static constexpr int kThreads = 512;
+  static constexpr int kTensors = BACK ? 2 : 1;  // read side by side
+  static constexpr int kRows = BACK ? 2 : 4;
+  static constexpr int kRing = BACK ? 2 : 3;
+  static constexpr int kStepBytes = kThreads * kRows * kTensors * static_cast<int>(sizeof(uint4));
+  static constexpr int kScratch = kThreads * N * static_cast<int>(sizeof(float2));
+  static constexpr int kMostSmem = kRing * kStepBytes > kScratch ? kRing * kStepBytes : kScratch;
+};
+
+// How a call is laid out.  Block (sample, chunk, tile) has the tile's columns of
+// every chunks-th step of step_rows rows of its sample, so that at any time the
+// blocks read one window of the tensor.
 struct GnGeom {
-  int64_t space;
-  int64_t rows;  // rows of a chunk (the last one may be shorter)
+  int64_t samples, space;
+  int64_t steps;  // steps of a sample (the last one may be short)
   int channels, groups, cpg;
   int cols;       // 128-bit vectors of a row
   int tile_cols;  // vector columns of a block
   int tiles;
-  int lanes;  // rows that a block reads at once
+  int lanes;      // rows that a block reads side by side
+  int step_rows;  // lanes * rows of a lane in a step
+  int unroll;     // rows of a lane in a step
   int chunks;
+  // Closed forms of what a chunk has: steps / chunks steps and one more below
+  // steps % chunks; the chunk with the last step misses `missing` rows of it.
+  int chunk_steps, more_steps, last_chunk, missing;
+
+  __device__ __forceinline__ int steps_of(int chunk) const {
+    return chunk_steps + (chunk < more_steps ? 1 : 0);
+  }
+  __device__ __forceinline__ int64_t rows_of(int chunk) const {
+    return static_cast<int64_t>(steps_of(chunk)) * step_rows - (chunk == last_chunk ? missing : 0);
+  }
 };
 
-GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups, int vec,
-                   int per_sm) {
+// What a block costs besides its rows (launch, joining its lanes, parameters),
+// as rows of a thread: about 2 us.
+constexpr int64_t kGnBlockCost = 16;
+
+template <typename T, bool BACK>
+GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups) {
+  using B = GnBlock<T, BACK>;
   GnGeom g;
+  g.samples = samples;
   g.space = space;
   g.channels = static_cast<int>(channels);
   g.groups = static_cast<int>(groups);
   g.cpg = static_cast<int>(channels / groups);
-  g.cols = static_cast<int>(channels / vec);
-  g.tiles = (g.cols + kGnThreads - 1) / kGnThreads;
+  g.cols = static_cast<int>(channels / B::N);
+  g.tiles = (g.cols + B::kThreads - 1) / B::kThreads;
   g.tile_cols = (g.cols + g.tiles - 1) / g.tiles;
-  g.lanes = kGnThreads / g.tile_cols;
-  // at least four rows a thread, so that its loads overlap
-  const int64_t most = (space + 4 * g.lanes - 1) / (4 * g.lanes);
-  int64_t want = 152 * per_sm / (samples * g.tiles);
-  want = want < 1 ? 1 : want > most ? most : want;
-  g.rows = (space + want - 1) / want;
-  g.chunks = static_cast<int>((space + g.rows - 1) / g.rows);
+  g.lanes = B::kThreads / g.tile_cols;
+  // Chunks a sample: as many as one to four waves of blocks hold, whichever
+  // takes the least time.
+  const int64_t sets = (space + g.lanes - 1) / g.lanes;  // of `lanes` rows
+  const int64_t columns = samples * g.tiles;
+  int64_t best = 1, best_cost = INT64_MAX;
+  for (int64_t w = 1; w <= 4; w++) {
+    int64_t c = kGnSms * w / columns;
+    c = c < 1 ? 1 : c > sets ? sets : c;
+    const int64_t waves = (columns * c + kGnSms - 1) / kGnSms;
+    const int64_t cost = waves * ((sets + c - 1) / c + kGnBlockCost);
+    if (cost < best_cost) best = c, best_cost = cost;
+  }
+  // even steps: as many rows of a lane as share a chunk's rows out best
+  const int64_t per = (sets + best - 1) / best;
+  const int64_t turns = (per + B::kRows - 1) / B::kRows;
+  g.unroll = static_cast<int>((per + turns - 1) / turns);
+  g.step_rows = g.lanes * g.unroll;
+  g.steps = (space + g.step_rows - 1) / g.step_rows;
+  g.chunks = static_cast<int>(best < g.steps ? best : g.steps);
+  g.chunk_steps = static_cast<int>(g.steps / g.chunks);
+  g.more_steps = static_cast<int>(g.steps % g.chunks);
+  g.last_chunk = static_cast<int>((g.steps - 1) % g.chunks);
+  g.missing = static_cast<int>(g.steps * g.step_rows - space);
   return g;
 }
 
-// Where a block stands: sample, chunk, and this thread's column and row lane.
-struct GnPlace {
-  int64_t sample, row0, row1;  // rows of the chunk
-  int chunk, tile, col, lane, channel;
-  bool active;
-  __device__ __forceinline__ GnPlace(const GnGeom& g, unsigned block, int vec) {
-    tile = static_cast<int>(block % g.tiles);
-    const unsigned rest = block / g.tiles;
-    chunk = static_cast<int>(rest % g.chunks);
-    sample = rest / g.chunks;
-    row0 = chunk * g.rows;
-    row1 = min(row0 + g.rows, g.space);
-    lane = threadIdx.x / g.tile_cols;
-    col = tile * g.tile_cols + static_cast<int>(threadIdx.x) % g.tile_cols;
-    active = col < g.cols;
-    channel = col * vec;
+// Global scratch: partial results of the blocks.  A group that lies in two tiles
+// has a part in each; part (group, tile) is in row group + tile, which no other
+// part has, as the groups of a tile are never below those of the tile before.
+// The chunks of a part are side by side, so that joining them reads whole
+// sectors (every block of the output kernel does: [chunks][groups + tiles] cost
+// 4 us more with 304 chunks).
+struct GnScratch {
+  float2* parts;  // [samples][groups + tiles][chunks]
+  float2* sums;   // backward: [samples][chunks][channels]
+};
+
+template <typename T, bool BACK>
+int64_t gn_scratch_bytes(const GnGeom& g) {
+  const int64_t row = g.groups + g.tiles + (BACK ? g.channels : 0);
+  return g.samples * g.chunks * row * static_cast<int64_t>(sizeof(float2));
+}
+
+// Two f32 values side by side; one instruction works on both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A 128-bit vector as pairs of values.
+template <typename T>
+struct Pairs {
+  static constexpr int N = Vec<T>::N / 2;
+  __device__ __forceinline__ static void unpack(const uint4& v, F2 (&p)[N]) {
+    float f[Vec<T>::N];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < N; i++) p[i] = f2(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ static uint4 pack(const F2 (&p)[N]) {
+    float f[Vec<T>::N];
+#pragma unroll
+    for (int i = 0; i < N; i++) split(p[i], f[2 * i], f[2 * i + 1]);
+    return Vec<T>::pack(f);
   }
 };
 
@@ -102,149 +199,148 @@ __device__ __forceinline__ void gn_params(const void* p, int is_bf16, int channe
 // value; below z = -88 the exponential is infinite and the sigmoid zero, off by
 // less than 2^-126.  For f32 from t = e^-|z|, which never overflows.
 template <typename T>
-__device__ __forceinline__ float gn_sigmoid(float z);
+__device__ __forceinline__ F2 gn_sigmoid2(F2 z);
 template <>
-__device__ __forceinline__ float gn_sigmoid<__nv_bfloat16>(float z) {
-  float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-  return s;
+__device__ __forceinline__ F2 gn_sigmoid2<float>(F2 z) {
+  float x[2];
+  split(z, x[0], x[1]);
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const float t = expf(-fabsf(x[i]));
+    x[i] = x[i] >= 0.0f ? 1.0f / (1.0f + t) : t / (1.0f + t);
+  }
+  return f2(x[0], x[1]);
 }
 template <>
-__device__ __forceinline__ float gn_sigmoid<float>(float z) {
-  const float t = expf(-fabsf(z));
-  return z >= 0.0f ? 1.0f / (1.0f + t) : t / (1.0f + t);
+__device__ __forceinline__ F2 gn_sigmoid2<__nv_bfloat16>(F2 z) {
+  float lo, hi;
+  split(mul2(z, f2(-1.4426950408889634f, -1.4426950408889634f)), lo, hi);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+  split(add2(f2(lo, hi), f2(1.0f, 1.0f)), lo, hi);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
+  return f2(lo, hi);
 }
 
-// ---------------------------------------------------------------------------
-// Forward
-// ---------------------------------------------------------------------------
-// Mean and sum of squared deviations (M2) of each group's part in this block.
-// A thread sums each channel's values minus the first of them that it sees, so
-// a channel far from zero cancels nothing and one outlier spoils no other
-// thread's sums; parts are joined by their means and counts (the update of
-// Chan, Golub and LeVeque).  A group that lies in two tiles has a part in each:
-// part (group, tile) is at place group + tile, which no other part has, as the
-// groups of a tile are never below those of the tile before.
-template <typename T>
-__global__ void __launch_bounds__(kGnThreads, kGnPerSm) gn_stats_kernel(float2* __restrict__ parts,
-                                                              const T* __restrict__ x,
-                                                              const GnGeom g) {
-  constexpr int N = Vec<T>::N;
-  __shared__ float2 sm[kGnThreads * N];  // [lane][channel of the tile]: mean, M2
-  pdl_enter();
-  const GnPlace at(g, blockIdx.x, N);
-  const int width = g.tile_cols * N;
-  if (at.active && at.lane < g.lanes) {
-    float first[N], s1[N], s2[N];
+template <int P>
+__device__ __forceinline__ void to_pairs(const float (&v)[2 * P], F2 (&p)[P]) {
 #pragma unroll
-    for (int e = 0; e < N; e++) first[e] = s1[e] = s2[e] = 0.0f;
-    const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
-    const uint4* p = reinterpret_cast<const uint4*>(x) +
-                     (at.sample * g.space + at.row0 + at.lane) * g.cols + at.col;
-    const int rows = static_cast<int>(at.row1 - at.row0);
-    int count = 0;
-    for (int r = at.lane; r < rows; r += kGnRows * g.lanes) {
-      uint4 v[kGnRows];
-#pragma unroll
-      for (int u = 0; u < kGnRows; u++, p += step)
-        if (r + u * g.lanes < rows) v[u] = ld_stream(p);
-      if (count == 0) Vec<T>::unpack(v[0], first);
-#pragma unroll
-      for (int u = 0; u < kGnRows; u++)
-        if (r + u * g.lanes < rows) {
-          float f[N];
-          Vec<T>::unpack(v[u], f);
-#pragma unroll
-          for (int e = 0; e < N; e++) {
-            const float d = f[e] - first[e];
-            s1[e] += d;
-            s2[e] = fmaf(d, d, s2[e]);
-          }
-          count++;
-        }
-    }
-    const float inv = count > 0 ? 1.0f / static_cast<float>(count) : 0.0f;
-    float2* o = sm + at.lane * width + (at.channel - at.tile * width);
-#pragma unroll
-    for (int e = 0; e < N; e++)
-      o[e] = make_float2(fmaf(s1[e], inv, first[e]), fmaf(-s1[e] * inv, s1[e], s2[e]));
-  }
-  __syncthreads();
-  // one warp a group: the lanes' parts of its channels that are in this tile
-  const int c0 = at.tile * width, c1 = min(c0 + width, g.channels);
-  const int g0 = c0 / g.cpg, g1 = (c1 - 1) / g.cpg;
-  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
-  const int warps = (blockDim.x + kWarp - 1) / kWarp;
-  const int span = static_cast<int>(at.row1 - at.row0);
-  for (int grp = g0 + warp; grp <= g1; grp += warps) {
-    const int a = max(c0, grp * g.cpg), b = min(c1, (grp + 1) * g.cpg);
-    const int n = (b - a) * g.lanes;
-    // rows of lane i: those i, i + lanes, ... of the chunk
-    auto rows_of = [&](int i) { return i < span ? (span - 1 - i) / g.lanes + 1 : 0; };
-    float s = 0.0f;
-    for (int i = lane32; i < n; i += kWarp) {
-      const int l = i / (b - a);
-      s = fmaf(static_cast<float>(rows_of(l)), sm[l * width + a - c0 + i - l * (b - a)].x, s);
-    }
-    const float total = static_cast<float>(span) * static_cast<float>(b - a);
-    const float mean = __fdiv_rn(group_sum<kWarp>(s), total);
-    float m2 = 0.0f;
-    for (int i = lane32; i < n; i += kWarp) {
-      const int l = i / (b - a);
-      const float2 v = sm[l * width + a - c0 + i - l * (b - a)];
-      const float d = v.x - mean, k = static_cast<float>(rows_of(l));
-      if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
-    }
-    m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0)
-      parts[(at.sample * g.chunks + at.chunk) * (g.groups + g.tiles) + grp + at.tile] =
-          make_float2(mean, m2);
-  }
+  for (int i = 0; i < P; i++) p[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
-constexpr int kGnJoinThreads = 128;
+// Where a block and a thread stand.
+struct GnPlace {
+  int64_t sample;
+  int chunk, tile;
+  int lane, col, channel;  // of this thread
+  int c0, c1;              // the tile's channels
+  int g0, g1;              // the groups that they belong to
+  bool active;
+  template <typename B>
+  __device__ __forceinline__ static GnPlace of(const GnGeom& g, unsigned block) {
+    GnPlace p;
+    p.tile = static_cast<int>(block % g.tiles);
+    const unsigned rest = block / g.tiles;
+    p.chunk = static_cast<int>(rest % g.chunks);
+    p.sample = rest / g.chunks;
+    p.lane = static_cast<int>(threadIdx.x) / g.tile_cols;
+    p.col = p.tile * g.tile_cols + static_cast<int>(threadIdx.x) % g.tile_cols;
+    p.active = p.col < g.cols && p.lane < g.lanes;
+    p.channel = p.col * B::N;
+    p.c0 = p.tile * g.tile_cols * B::N;
+    p.c1 = min(p.c0 + g.tile_cols * B::N, g.channels);
+    p.g0 = p.c0 / g.cpg;
+    p.g1 = (p.c1 - 1) / g.cpg;
+    return p;
+  }
+};
 
-// One block a (sample, group): joins its parts into mean and rstd.
-__global__ void __launch_bounds__(kGnJoinThreads) gn_join_kernel(float* __restrict__ mean_out,
-                                                                 float* __restrict__ rstd_out,
-                                                                 const float2* __restrict__ parts,
-                                                                 const GnGeom g, int width,
-                                                                 float eps) {
-  __shared__ float scratch[2][kGnJoinThreads / kWarp];
-  pdl_enter();
-  const int64_t sample = blockIdx.x / g.groups;
-  const int grp = static_cast<int>(blockIdx.x % g.groups);
-  const int ca = grp * g.cpg, cb = ca + g.cpg;  // the group's channels
-  const int t0 = ca / width, t1 = (cb - 1) / width;
-  const int per = t1 - t0 + 1;
-  const int n = g.chunks * per;
-  const float2* p = parts + sample * g.chunks * (g.groups + g.tiles) + grp;
-  auto part = [&](int i, float& count) {
-    const int chunk = i / per, tile = t0 + i % per;
-    const int64_t rows = min(g.rows, g.space - chunk * g.rows);
-    count = static_cast<float>(rows) *
-            static_cast<float>(min(cb, (tile + 1) * width) - max(ca, tile * width));
-    return p[static_cast<int64_t>(chunk) * (g.groups + g.tiles) + tile];
+// Rows of the lanes of a block: `base` each, and one more below `more`.
+struct GnLaneRows {
+  int base, more;
+  __device__ __forceinline__ GnLaneRows(const GnGeom& g, int chunk) {
+    base = g.steps_of(chunk) * g.unroll;
+    more = 0;
+    if (chunk == g.last_chunk && g.missing > 0) {
+      const int rest = g.step_rows - g.missing;  // rows of the short step
+      base += rest / g.lanes - g.unroll;
+      more = rest % g.lanes;
+    }
+  }
+  // Rows of lanes [l0, l1).
+  __device__ __forceinline__ int of(int l0, int l1) const {
+    return (l1 - l0) * base + max(0, min(more, l1) - l0);
+  }
+};
+
+// Walks this thread's rows of a chunk, from the first step to the last or
+// (REVERSE) back, copying kRing steps ahead: visit(offset, n, v) gets the n rows
+// of a step, one vector of each tensor, `offset` in vectors from the tensors'
+// start to the first of them.
+template <typename B, bool REVERSE, typename Visit>
+__device__ __forceinline__ void gn_walk(const GnGeom& g, const GnPlace& at,
+                                        const void* const (&src)[B::kTensors], unsigned char* smem,
+                                        Visit visit) {
+  constexpr int R = B::kRows, K = B::kTensors, RING = B::kRing;
+  const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
+  const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
+  const int steps = g.steps_of(at.chunk);
+  const int whole = steps - (at.chunk == g.last_chunk && g.missing > 0 ? 1 : 0);
+  const int short_rows = GnLaneRows(g, at.chunk).of(at.lane, at.lane + 1) - whole * g.unroll;
+  const unsigned ring = smem_addr(smem) + threadIdx.x * sizeof(uint4);
+  // Vectors from the tensors' start to step i of this walk, and its rows here.
+  const int64_t step_vecs = static_cast<int64_t>(g.step_rows) * g.cols;
+  auto offset = [&](int i) {
+    const int64_t j = REVERSE ? steps - 1 - i : i;
+    return base + (at.chunk + j * g.chunks) * step_vecs;
   };
-  float s = 0.0f, count;
-  for (int i = threadIdx.x; i < n; i += kGnJoinThreads) {
-    const float2 v = part(i, count);
-    s = fmaf(count, v.x, s);
+  auto rows_in = [&](int i) {
+    return (REVERSE ? steps - 1 - i : i) < whole ? g.unroll : short_rows;
+  };
+  auto issue = [&](int i, int place) {
+    if (i < steps) {
+      const int64_t off = offset(i);
+      const int n = rows_in(i);
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+        const uint4* p = static_cast<const uint4*>(src[k]) + off;
+        unsigned dst = ring + (place * R * K + k) * B::kThreads * 16;
+#pragma unroll
+        for (int u = 0; u < R; u++, p += row_step, dst += K * B::kThreads * 16)
+          if (u < n) cp_async16(dst, p);
+      }
+    }
+    cp_async_commit();  // possibly empty: one group a step
+  };
+  for (int i = 0; i < RING; i++) issue(i, i);
+  int place = 0;
+  for (int i = 0; i < steps; i++) {
+    cp_async_wait<RING - 1>();
+    const int n = rows_in(i);
+    uint4 v[R][K];
+    const unsigned char* slot = smem + threadIdx.x * sizeof(uint4) +
+                                static_cast<size_t>(place) * R * K * B::kThreads * 16;
+#pragma unroll
+    for (int u = 0; u < R; u++)
+      if (u < n)
+#pragma unroll
+        for (int k = 0; k < K; k++) v[u][k] = lds128(slot + (u * K + k) * B::kThreads * 16);
+    visit(offset(i), n, v);
+    issue(i + RING, place);  // the slot's values have been used
+    place = place + 1 == RING ? 0 : place + 1;
   }
-  const float total = static_cast<float>(g.space) * static_cast<float>(g.cpg);
-  const float mean = __fdiv_rn(block_sum(s, scratch[0]), total);
-  float m2 = 0.0f;
-  for (int i = threadIdx.x; i < n; i += kGnJoinThreads) {
-    const float2 v = part(i, count);
-    const float d = v.x - mean;
-    m2 += fmaf(count * d, d, v.y);
-  }
-  m2 = block_sum(m2, scratch[1]);
-  m2 = m2 < 0.0f ? 0.0f : m2;  // a part's rounding may leave a constant group just below zero
-  if (threadIdx.x == 0) {
-    mean_out[blockIdx.x] = mean;
-    rstd_out[blockIdx.x] = 1.0f / sqrtf(__fdiv_rn(m2, total) + eps);
+  cp_async_wait<0>();
+}
+
+// The group of each of N consecutive channels, by one division.
+template <int N>
+__device__ __forceinline__ void gn_groups_of(int channel, int cpg, int (&grp)[N]) {
+  int at = channel / cpg, place = channel - at * cpg;
+#pragma unroll
+  for (int e = 0; e < N; e++) {
+    grp[e] = at;
+    if (++place == cpg) place = 0, at++;
   }
 }
 
@@ -254,48 +350,252 @@ struct GnParams {
   int is_bf16;
 };
 
-template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads, kGnPerSm) gn_apply_kernel(T* __restrict__ out,
-                                                              const T* __restrict__ x,
-                                                              const float* __restrict__ mean,
-                                                              const float* __restrict__ rstd,
-                                                              const GnParams prm, const GnGeom g) {
-  constexpr int N = Vec<T>::N;
+struct GnArgs {
+  void* out;
+  const void* x;
+  const void* dy;
+  float* mean;
+  float* rstd;
+  GnParams prm;
+  void* dw;
+  void* db;
+  float eps;
+  GnScratch scratch;
+};
+
+// How the lanes of a channel are joined: `subs` threads a channel, `per` lanes each.
+struct GnSubs {
+  int per, subs;
+  __device__ __forceinline__ GnSubs(const GnGeom& g, int width, int threads) {
+    const int most = width < threads ? threads / width : 1;
+    per = (g.lanes + most - 1) / most;
+    subs = (g.lanes + per - 1) / per;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+// Statistics are means and sums of squared deviations (M2).  A thread sums each
+// channel's values minus the first of them that it sees, so a channel far from
+// zero cancels nothing and one outlier spoils no other thread's sums; parts are
+// joined by their means and counts (the update of Chan, Golub and LeVeque).
+template <typename T>
+__global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
+    gn_stats_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, false>;
+  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2* sm = reinterpret_cast<float2*>(smem);  // after the walk: [lane][channel] mean, M2
   pdl_enter();
-  const GnPlace at(g, gridDim.x - 1 - blockIdx.x, N);
-  if (!at.active || at.lane >= g.lanes) return;
-  float mu[N], a[N], b[N];
-  gn_params<N>(prm.w, prm.is_bf16, at.channel, 1.0f, a);
-  gn_params<N>(prm.b, prm.is_bf16, at.channel, 0.0f, b);
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  const int width = g.tile_cols * N;
+  const GnLaneRows rows(g, at.chunk);
+  F2 minus[P], s1[P], s2[P];  // minus the first value of each channel
 #pragma unroll
-  for (int e = 0; e < N; e++) {
-    const int64_t i = at.sample * g.groups + (at.channel + e) / g.cpg;
-    mu[e] = mean[i];
-    a[e] *= rstd[i];
-  }
-  const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
-  const int rows = static_cast<int>(at.row1 - at.row0);
-  const int64_t base = (at.sample * g.space + at.row1 - 1 - at.lane) * g.cols + at.col;
-  const uint4* p = reinterpret_cast<const uint4*>(x) + base;
-  uint4* o = reinterpret_cast<uint4*>(out) + base;
-  for (int r = at.lane; r < rows; r += kGnRows * g.lanes) {
-    uint4 v[kGnRows];
+  for (int i = 0; i < P; i++) minus[i] = s1[i] = s2[i] = f2(0.0f, 0.0f);
+  if (at.active) {
+    const void* const src[1] = {a.x};
+    bool begun = false;
+    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][1]) {
+      if (!begun && n > 0) {
+        Pairs<T>::unpack(v[0][0], minus);
 #pragma unroll
-    for (int u = 0; u < kGnRows; u++, p -= step)
-      if (r + u * g.lanes < rows) v[u] = ld_stream(p);
-#pragma unroll
-    for (int u = 0; u < kGnRows; u++, o -= step)
-      if (r + u * g.lanes < rows) {
-        float f[N];
-        Vec<T>::unpack(v[u], f);
-#pragma unroll
-        for (int e = 0; e < N; e++) {
-          const float z = fmaf(f[e] - mu[e], a[e], b[e]);
-          f[e] = SILU ? z * gn_sigmoid<T>(z) : z;
-        }
-        st_stream(o, Vec<T>::pack(f));
+        for (int i = 0; i < P; i++) minus[i] = mul2(minus[i], f2(-1.0f, -1.0f));
+        begun = true;
       }
+#pragma unroll
+      for (int u = 0; u < R; u++)
+        if (u < n) {
+          F2 f[P];
+          Pairs<T>::unpack(v[u][0], f);
+#pragma unroll
+          for (int i = 0; i < P; i++) {
+            const F2 d = add2(f[i], minus[i]);
+            s1[i] = add2(s1[i], d);
+            s2[i] = fma2(d, d, s2[i]);
+          }
+        }
+    });
   }
+  __syncthreads();  // the rings are done with
+  if (at.active) {
+    const float count = static_cast<float>(rows.of(at.lane, at.lane + 1));
+    const float inv = count > 0.0f ? 1.0f / count : 0.0f;
+    float2* o = sm + at.lane * width + (at.channel - at.c0);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      float m0, m1, a0, a1, b0, b1;
+      split(minus[i], m0, m1);
+      split(s1[i], a0, a1);
+      split(s2[i], b0, b1);
+      o[2 * i] = make_float2(fmaf(a0, inv, -m0), fmaf(-a0 * inv, a0, b0));
+      o[2 * i + 1] = make_float2(fmaf(a1, inv, -m1), fmaf(-a1 * inv, a1, b1));
+    }
+  }
+  __syncthreads();
+  // Lanes of a channel: sub s joins lanes s * per ... and leaves the result in
+  // the first of them.
+  const GnSubs sub(g, width, B::kThreads);
+  const int tile_channels = at.c1 - at.c0;
+  for (int i = threadIdx.x; i < sub.subs * tile_channels; i += B::kThreads) {
+    const int s = i / tile_channels, c = i - s * tile_channels;
+    const int l0 = s * sub.per, l1 = min(l0 + sub.per, g.lanes);
+    float2* col = sm + c;
+    float sum = 0.0f;
+    for (int l = l0; l < l1; l++)
+      sum = fmaf(static_cast<float>(rows.of(l, l + 1)), col[l * width].x, sum);
+    const int count = rows.of(l0, l1);
+    const float mean = count > 0 ? __fdiv_rn(sum, static_cast<float>(count)) : 0.0f;
+    float m2 = 0.0f;
+    for (int l = l0; l < l1; l++) {
+      const float2 v = col[l * width];
+      const float d = v.x - mean, k = static_cast<float>(rows.of(l, l + 1));
+      if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
+    }
+    col[l0 * width] = make_float2(mean, m2);
+  }
+  __syncthreads();
+  // The group's channels in this tile: one warp a group.
+  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
+    const int ca = max(at.c0, grp * g.cpg), cn = min(at.c1, (grp + 1) * g.cpg) - ca;
+    // element i: sub i / cn, channel i % cn; a lane's elements are 32 apart
+    const int ds = kWarp / cn, dc = kWarp % cn;
+    auto each = [&](auto use) {
+      int s = lane32 / cn, c = lane32 % cn;
+      while (s < sub.subs) {
+        const int l0 = s * sub.per;
+        const float k = static_cast<float>(rows.of(l0, min(l0 + sub.per, g.lanes)));
+        use(k, sm[l0 * width + ca - at.c0 + c]);
+        s += ds;
+        c += dc;
+        if (c >= cn) c -= cn, s++;
+      }
+    };
+    float sum = 0.0f, m2 = 0.0f;
+    each([&](float k, const float2& v) { sum = fmaf(k, v.x, sum); });
+    const float total = static_cast<float>(g.rows_of(at.chunk)) * static_cast<float>(cn);
+    const float mean = __fdiv_rn(group_sum<kWarp>(sum), total);
+    each([&](float k, const float2& v) {
+      const float d = v.x - mean;
+      if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
+    });
+    m2 = group_sum<kWarp>(m2);
+    if (lane32 == 0)
+      a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
+          make_float2(mean, m2);
+  }
+}
+
+// Joins the parts of one group of the sample into mean and rstd (a warp's work).
+__device__ __forceinline__ float2 gn_join(const GnArgs& a, const GnGeom& g, int64_t sample, int grp,
+                                          int width) {
+  const int lane32 = threadIdx.x % kWarp;
+  const int ca = grp * g.cpg, cb = ca + g.cpg;
+  const int t0 = ca / width, tn = (cb - 1) / width - t0 + 1;
+  const int n = g.chunks * tn;
+  // the rows of a group's tiles follow one another
+  const float2* parts = a.scratch.parts +
+                        (sample * (g.groups + g.tiles) + grp + t0) * static_cast<int64_t>(g.chunks);
+  auto part = [&](int i, float& count) {
+    const int t = tn == 1 ? 0 : i / g.chunks, chunk = i - t * g.chunks, tile = t0 + t;
+    count = static_cast<float>(g.rows_of(chunk)) *
+            static_cast<float>(min(cb, (tile + 1) * width) - max(ca, tile * width));
+    return __ldg(parts + i);
+  };
+  // a lane's first parts stay in registers for the second sum
+  constexpr int kHeld = 5;
+  float2 held[kHeld];
+  float counts[kHeld], sum = 0.0f, count;
+#pragma unroll
+  for (int j = 0; j < kHeld; j++) {
+    counts[j] = 0.0f;
+    held[j] = make_float2(0.0f, 0.0f);
+    if (lane32 + j * kWarp < n) held[j] = part(lane32 + j * kWarp, counts[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kHeld; j++) sum = fmaf(counts[j], held[j].x, sum);
+  for (int i = lane32 + kHeld * kWarp; i < n; i += kWarp) {
+    const float2 v = part(i, count);
+    sum = fmaf(count, v.x, sum);
+  }
+  const float total = static_cast<float>(g.space) * static_cast<float>(g.cpg);
+  const float mean = __fdiv_rn(group_sum<kWarp>(sum), total);
+  float m2 = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kHeld; j++) {
+    const float d = held[j].x - mean;
+    if (counts[j] > 0.0f) m2 += fmaf(counts[j] * d, d, held[j].y);
+  }
+  for (int i = lane32 + kHeld * kWarp; i < n; i += kWarp) {
+    const float2 v = part(i, count);
+    const float d = v.x - mean;
+    m2 += fmaf(count * d, d, v.y);
+  }
+  m2 = group_sum<kWarp>(m2);
+  m2 = m2 < 0.0f ? 0.0f : m2;  // rounding may leave a constant group just below zero
+  return make_float2(mean, 1.0f / sqrtf(__fdiv_rn(m2, total) + a.eps));
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
+    gn_apply_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, false>;
+  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: mean, rstd of the groups
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
+  const int width = g.tile_cols * N;
+  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
+    const float2 v = gn_join(a, g, at.sample, grp, width);
+    if (lane32 == 0) {
+      sm[grp - at.g0] = v;
+      if (at.chunk == 0 && grp * g.cpg >= at.c0) {  // one block of the sample writes a group's
+        a.mean[at.sample * g.groups + grp] = v.x;
+        a.rstd[at.sample * g.groups + grp] = v.y;
+      }
+    }
+  }
+  __syncthreads();
+  F2 mu[P], sc[P], sh[P];  // minus the mean, rstd * w, b
+  if (at.active) {
+    float fm[N], fa[N], fb[N];
+    gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
+    gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
+    int grp[N];
+    gn_groups_of<N>(at.channel, g.cpg, grp);
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+      const float2 v = sm[grp[e] - at.g0];
+      fm[e] = -v.x;
+      fa[e] *= v.y;
+    }
+    to_pairs<P>(fm, mu);
+    to_pairs<P>(fa, sc);
+    to_pairs<P>(fb, sh);
+  }
+  __syncthreads();  // the rings take the place of sm
+  if (!at.active) return;
+  const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
+  const void* const src[1] = {a.x};
+  gn_walk<B, true>(g, at, src, smem, [&](int64_t off, int n, const uint4 (&v)[R][1]) {
+    uint4* o = static_cast<uint4*>(a.out) + off;
+#pragma unroll
+    for (int u = 0; u < R; u++, o += row_step)
+      if (u < n) {
+        F2 f[P];
+        Pairs<T>::unpack(v[u][0], f);
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          f[i] = fma2(add2(f[i], mu[i]), sc[i], sh[i]);
+          if (SILU) f[i] = mul2(f[i], gn_sigmoid2<T>(f[i]));
+        }
+        st_stream(o, Pairs<T>::pack(f));
+      }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -303,291 +603,313 @@ __global__ void __launch_bounds__(kGnThreads, kGnPerSm) gn_apply_kernel(T* __res
 // ---------------------------------------------------------------------------
 // dz = dy * act'(z); silu'(z) = s (1 + z (1 - s)) with s = sigmoid(z).
 template <typename T, bool SILU>
-__device__ __forceinline__ float gn_dz(float dy, float z) {
+__device__ __forceinline__ F2 gn_dz(F2 dy, F2 z) {
   if (!SILU) return dy;
-  const float s = gn_sigmoid<T>(z);
-  return dy * (s * fmaf(z, 1.0f - s, 1.0f));
+  const F2 one = f2(1.0f, 1.0f);
+  const F2 s = gn_sigmoid2<T>(z);
+  const F2 rest = fma2(s, f2(-1.0f, -1.0f), one);
+  return mul2(dy, mul2(s, fma2(z, rest, one)));
 }
 
-struct GnGradIn {
-  const void* dy;
-  const void* x;
-  const float* mean;
-  const float* rstd;
-  GnParams prm;
-};
+// This thread's channels: minus the mean, rstd * w, b.
+template <int N, int P>
+__device__ __forceinline__ void gn_grad_params(const GnArgs& a, const GnGeom& g, const GnPlace& at,
+                                               F2 (&mu)[P], F2 (&sc)[P], F2 (&sh)[P]) {
+  float fm[N], fa[N], fb[N];
+  gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
+  gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
+  int grp[N];
+  gn_groups_of<N>(at.channel, g.cpg, grp);
+#pragma unroll
+  for (int e = 0; e < N; e++) {
+    const int64_t i = at.sample * g.groups + grp[e];
+    fm[e] = -a.mean[i];
+    fa[e] *= a.rstd[i];
+  }
+  to_pairs<P>(fm, mu);
+  to_pairs<P>(fa, sc);
+  to_pairs<P>(fb, sh);
+}
 
-// Per channel and chunk: sum dz and sum dz * (x - mean).
+// Sums of a chunk: S1 and S2 per channel, and weighted by w per group.
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads, kGnGradPerSm) gn_grad_stats_kernel(float2* __restrict__ parts,
-                                                                   const GnGradIn in,
-                                                                   const GnGeom g) {
-  constexpr int N = Vec<T>::N;
-  __shared__ float2 sm[kGnThreads * N];
+__global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
+    gn_grad_stats_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, true>;
+  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2* sm = reinterpret_cast<float2*>(smem);  // after the walk: [lane][channel of the tile]
   pdl_enter();
-  const GnPlace at(g, blockIdx.x, N);
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
   const int width = g.tile_cols * N;
-  if (at.active && at.lane < g.lanes) {
-    float mu[N], a[N], b[N], s1[N], s2[N];
-    gn_params<N>(in.prm.w, in.prm.is_bf16, at.channel, 1.0f, a);
-    gn_params<N>(in.prm.b, in.prm.is_bf16, at.channel, 0.0f, b);
+  F2 s1[P], s2[P];  // sums of dz and of dz (x - mean)
 #pragma unroll
-    for (int e = 0; e < N; e++) {
-      const int64_t i = at.sample * g.groups + (at.channel + e) / g.cpg;
-      mu[e] = in.mean[i];
-      a[e] *= in.rstd[i];
-      s1[e] = s2[e] = 0.0f;
-    }
-    const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
-    const int rows = static_cast<int>(at.row1 - at.row0);
-    const int64_t base = (at.sample * g.space + at.row0 + at.lane) * g.cols + at.col;
-    const uint4* px = static_cast<const uint4*>(in.x) + base;
-    const uint4* pd = static_cast<const uint4*>(in.dy) + base;
-    for (int r = at.lane; r < rows; r += kGnGradRows * g.lanes) {
-      uint4 vx[kGnGradRows], vd[kGnGradRows];
+  for (int i = 0; i < P; i++) s1[i] = s2[i] = f2(0.0f, 0.0f);
+  if (at.active) {
+    F2 mu[P], sc[P], sh[P];
+    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
+    const void* const src[2] = {a.x, a.dy};
+    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][2]) {
 #pragma unroll
-      for (int u = 0; u < kGnGradRows; u++, px += step, pd += step)
-        if (r + u * g.lanes < rows) {
-          vx[u] = ld_stream(px);
-          vd[u] = ld_stream(pd);
-        }
+      for (int u = 0; u < R; u++)
+        if (u < n) {
+          F2 f[P], d[P];
+          Pairs<T>::unpack(v[u][0], f);
+          Pairs<T>::unpack(v[u][1], d);
 #pragma unroll
-      for (int u = 0; u < kGnGradRows; u++)
-        if (r + u * g.lanes < rows) {
-          float f[N], d[N];
-          Vec<T>::unpack(vx[u], f);
-          Vec<T>::unpack(vd[u], d);
-#pragma unroll
-          for (int e = 0; e < N; e++) {
-            const float c = f[e] - mu[e];
-            const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
-            s1[e] += dz;
-            s2[e] = fmaf(dz, c, s2[e]);
+          for (int i = 0; i < P; i++) {
+            const F2 c = add2(f[i], mu[i]);
+            const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
+            s1[i] = add2(s1[i], dz);
+            s2[i] = fma2(dz, c, s2[i]);
           }
         }
-    }
-    float2* o = sm + at.lane * width + (at.channel - at.tile * width);
+    });
+  }
+  __syncthreads();  // the rings are done with
+  if (at.active) {
+    float2* o = sm + at.lane * width + (at.channel - at.c0);
 #pragma unroll
-    for (int e = 0; e < N; e++) o[e] = make_float2(s1[e], s2[e]);
+    for (int i = 0; i < P; i++) {
+      float a0, a1, b0, b1;
+      split(s1[i], a0, a1);
+      split(s2[i], b0, b1);
+      o[2 * i] = make_float2(a0, b0);
+      o[2 * i + 1] = make_float2(a1, b1);
+    }
   }
   __syncthreads();
-  const int c0 = at.tile * width, c1 = min(c0 + width, g.channels);
-  for (int c = threadIdx.x; c < c1 - c0; c += blockDim.x) {
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int l = 0; l < g.lanes; l++) {
-      const float2 v = sm[l * width + c];
-      s.x += v.x;
-      s.y += v.y;
+  // The lanes of a channel, in two steps.
+  const GnSubs sub(g, width, B::kThreads);
+  const int tile_channels = at.c1 - at.c0;
+  for (int i = threadIdx.x; i < sub.subs * tile_channels; i += B::kThreads) {
+    const int s = i / tile_channels, c = i - s * tile_channels;
+    const int l0 = s * sub.per, l1 = min(l0 + sub.per, g.lanes);
+    float2 v = sm[l0 * width + c];
+    for (int l = l0 + 1; l < l1; l++) {
+      v.x += sm[l * width + c].x;
+      v.y += sm[l * width + c].y;
     }
-    parts[(at.sample * g.chunks + at.chunk) * g.channels + c0 + c] = s;
+    sm[l0 * width + c] = v;
   }
-}
-
-constexpr int kGnSumLanes = 32;  // chunk lanes of the joining block (x 32 channels)
-
-// Sums the chunks of 32 channels of one sample: S1 and S2 (with xhat) per channel.
-__global__ void __launch_bounds__(32 * kGnSumLanes) gn_grad_join_kernel(
-    float2* __restrict__ sums, const float2* __restrict__ parts, const float* __restrict__ rstd,
-    const GnGeom g) {
-  __shared__ float2 sm[kGnSumLanes][32 + 1];
-  pdl_enter();
-  const int blocks = (g.channels + 31) / 32;
-  const int64_t sample = blockIdx.x / blocks;
-  const int c = static_cast<int>(blockIdx.x % blocks) * 32 + threadIdx.x % 32;
-  const int lane = threadIdx.x / 32;
-  float2 s = make_float2(0.0f, 0.0f);
-  if (c < g.channels)
-    for (int k = lane; k < g.chunks; k += kGnSumLanes) {
-      const float2 v = parts[(sample * g.chunks + k) * g.channels + c];
-      s.x += v.x;
-      s.y += v.y;
-    }
-  sm[lane][threadIdx.x % 32] = s;
   __syncthreads();
-  // warp `lane` joins channel `lane` of the block
-  float2 v = sm[threadIdx.x % 32][lane];
-  v.x = group_sum<32>(v.x);
-  v.y = group_sum<32>(v.y);
-  const int mine = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
-  if (threadIdx.x % 32 == 0 && mine < g.channels)
-    sums[sample * g.channels + mine] =
-        make_float2(v.x, v.y * rstd[sample * g.groups + mine / g.cpg]);
-}
-
-template <typename T, bool SILU>
-__global__ void __launch_bounds__(kGnThreads, kGnGradPerSm) gn_grad_apply_kernel(
-    T* __restrict__ dx, void* __restrict__ dw, void* __restrict__ db,
-    const float2* __restrict__ sums, const GnGradIn in, const GnGeom g, int samples) {
-  constexpr int N = Vec<T>::N;
-  // mean_g(w dz) and mean_g(w dz xhat) of the groups that this tile touches
-  extern __shared__ float2 grp_mean[];
-  pdl_enter();
-  const GnPlace at(g, gridDim.x - 1 - blockIdx.x, N);
-  const int width = g.tile_cols * N;
-  const int c0 = at.tile * width, c1 = min(c0 + width, g.channels);
-  const int g0 = c0 / g.cpg, g1 = (c1 - 1) / g.cpg;
+  const int64_t block = at.sample * g.chunks + at.chunk;
+  for (int c = threadIdx.x; c < tile_channels; c += B::kThreads) {
+    float2 v = sm[c];
+    for (int s = 1; s < sub.subs; s++) {
+      v.x += sm[s * sub.per * width + c].x;
+      v.y += sm[s * sub.per * width + c].y;
+    }
+    v.y *= a.rstd[at.sample * g.groups + (at.c0 + c) / g.cpg];
+    if (a.dw != nullptr) a.scratch.sums[block * g.channels + at.c0 + c] = v;
+    float w[1];
+    gn_params<1>(a.prm.w, a.prm.is_bf16, at.c0 + c, 1.0f, w);
+    sm[c] = make_float2(w[0] * v.x, w[0] * v.y);
+  }
+  __syncthreads();
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
-  const int warps = (blockDim.x + kWarp - 1) / kWarp;
-  const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
-  auto weight = [&](int c) {
-    float v[1];
-    gn_params<1>(in.prm.w, in.prm.is_bf16, c, 1.0f, v);
-    return v[0];
-  };
-  for (int grp = g0 + warp; grp <= g1; grp += warps) {
+  for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
+    const int ca = max(at.c0, grp * g.cpg), cb = min(at.c1, (grp + 1) * g.cpg);
     float m1 = 0.0f, m2 = 0.0f;
-    for (int i = lane32; i < g.cpg; i += kWarp) {
-      const int c = grp * g.cpg + i;
-      const float2 v = sums[at.sample * g.channels + c];
-      const float w = weight(c);
-      m1 = fmaf(w, v.x, m1);
-      m2 = fmaf(w, v.y, m2);
+    for (int c = ca + lane32; c < cb; c += kWarp) {
+      m1 += sm[c - at.c0].x;
+      m2 += sm[c - at.c0].y;
     }
     m1 = group_sum<kWarp>(m1);
     m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0) grp_mean[grp - g0] = make_float2(m1 * inv, m2 * inv);
+    if (lane32 == 0)
+      a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
+          make_float2(m1, m2);
   }
-  // the first chunk's blocks of sample 0 also write their channels' dw and db
-  if (at.sample == 0 && at.chunk == 0 && dw != nullptr)
-    for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) {
-      float2 s = make_float2(0.0f, 0.0f);
-      for (int n = 0; n < samples; n++) {
-        const float2 v = sums[static_cast<int64_t>(n) * g.channels + c];
-        s.x += v.x;
-        s.y += v.y;
+}
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
+    gn_grad_apply_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, true>;
+  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  constexpr int kWarps = B::kThreads / kWarp;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: the groups' means
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
+  const int width = g.tile_cols * N;
+  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
+  for (int grp = at.g0 + warp; grp <= at.g1; grp += kWarps) {
+    const int t0 = grp * g.cpg / width, tn = ((grp + 1) * g.cpg - 1) / width - t0 + 1;
+    float m1 = 0.0f, m2 = 0.0f;
+    const float2* parts = a.scratch.parts + (at.sample * (g.groups + g.tiles) + grp + t0) *
+                                                static_cast<int64_t>(g.chunks);
+    for (int i = lane32; i < g.chunks * tn; i += kWarp) {
+      const float2 v = __ldg(parts + i);
+      m1 += v.x;
+      m2 += v.y;
+    }
+    m1 = group_sum<kWarp>(m1);
+    m2 = group_sum<kWarp>(m2);
+    if (lane32 == 0) sm[grp - at.g0] = make_float2(m1 * inv, m2 * inv);
+  }
+  // dw and db: the blocks share the channels, one warp each.
+  if (a.dw != nullptr)
+    for (int64_t c = blockIdx.x + static_cast<int64_t>(gridDim.x) * warp; c < g.channels;
+         c += static_cast<int64_t>(gridDim.x) * kWarps) {
+      float t1 = 0.0f, t2 = 0.0f;
+      for (int64_t i = lane32; i < g.samples * g.chunks; i += kWarp) {
+        const float2 v = __ldg(a.scratch.sums + i * g.channels + c);
+        t1 += v.x;
+        t2 += v.y;
       }
-      if (in.prm.is_bf16) {
-        static_cast<__nv_bfloat16*>(db)[c] = __float2bfloat16_rn(s.x);
-        static_cast<__nv_bfloat16*>(dw)[c] = __float2bfloat16_rn(s.y);
-      } else {
-        static_cast<float*>(db)[c] = s.x;
-        static_cast<float*>(dw)[c] = s.y;
+      t1 = group_sum<kWarp>(t1);
+      t2 = group_sum<kWarp>(t2);
+      if (lane32 == 0) {
+        if (a.prm.is_bf16) {
+          static_cast<__nv_bfloat16*>(a.db)[c] = __float2bfloat16_rn(t1);
+          static_cast<__nv_bfloat16*>(a.dw)[c] = __float2bfloat16_rn(t2);
+        } else {
+          static_cast<float*>(a.db)[c] = t1;
+          static_cast<float*>(a.dw)[c] = t2;
+        }
       }
     }
   __syncthreads();
-  if (!at.active || at.lane >= g.lanes) return;
-  // dx = a dz - k1 - (x - mean) k2 with a = rstd w, k1 = rstd m1, k2 = rstd^2 m2
-  float mu[N], a[N], b[N], k1[N], k2[N];
-  gn_params<N>(in.prm.w, in.prm.is_bf16, at.channel, 1.0f, a);
-  gn_params<N>(in.prm.b, in.prm.is_bf16, at.channel, 0.0f, b);
+  // dx = a dz - k1 - (x - mean) k2: a = rstd w, k1 = rstd m1, k2 = rstd^2 m2
+  F2 mu[P], sc[P], sh[P], k1[P], k2[P];  // k1 and k2 negated
+  if (at.active) {
+    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
+    float f1[N], f3[N];
+    int grp[N];
+    gn_groups_of<N>(at.channel, g.cpg, grp);
 #pragma unroll
-  for (int e = 0; e < N; e++) {
-    const int grp = (at.channel + e) / g.cpg;
-    const float rs = in.rstd[at.sample * g.groups + grp];
-    mu[e] = in.mean[at.sample * g.groups + grp];
-    a[e] *= rs;
-    k1[e] = rs * grp_mean[grp - g0].x;
-    k2[e] = rs * rs * grp_mean[grp - g0].y;
+    for (int e = 0; e < N; e++) {
+      const float rs = a.rstd[at.sample * g.groups + grp[e]];
+      f1[e] = -rs * sm[grp[e] - at.g0].x;
+      f3[e] = -rs * rs * sm[grp[e] - at.g0].y;
+    }
+    to_pairs<P>(f1, k1);
+    to_pairs<P>(f3, k2);
   }
-  const int64_t step = static_cast<int64_t>(g.lanes) * g.cols;
-  const int rows = static_cast<int>(at.row1 - at.row0);
-  const int64_t base = (at.sample * g.space + at.row1 - 1 - at.lane) * g.cols + at.col;
-  const uint4* px = static_cast<const uint4*>(in.x) + base;
-  const uint4* pd = static_cast<const uint4*>(in.dy) + base;
-  uint4* o = reinterpret_cast<uint4*>(dx) + base;
-  for (int r = at.lane; r < rows; r += kGnGradRows * g.lanes) {
-    uint4 vx[kGnGradRows], vd[kGnGradRows];
+  __syncthreads();  // the rings take the place of sm
+  if (!at.active) return;
+  const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
+  const void* const src[2] = {a.x, a.dy};
+  gn_walk<B, true>(g, at, src, smem, [&](int64_t off, int n, const uint4 (&v)[R][2]) {
+    uint4* o = static_cast<uint4*>(a.out) + off;
 #pragma unroll
-    for (int u = 0; u < kGnGradRows; u++, px -= step, pd -= step)
-      if (r + u * g.lanes < rows) {
-        vx[u] = ld_stream(px);
-        vd[u] = ld_stream(pd);
-      }
+    for (int u = 0; u < R; u++, o += row_step)
+      if (u < n) {
+        F2 f[P], d[P];
+        Pairs<T>::unpack(v[u][0], f);
+        Pairs<T>::unpack(v[u][1], d);
 #pragma unroll
-    for (int u = 0; u < kGnGradRows; u++, o -= step)
-      if (r + u * g.lanes < rows) {
-        float f[N], d[N];
-        Vec<T>::unpack(vx[u], f);
-        Vec<T>::unpack(vd[u], d);
-#pragma unroll
-        for (int e = 0; e < N; e++) {
-          const float c = f[e] - mu[e];
-          const float dz = gn_dz<T, SILU>(d[e], fmaf(c, a[e], b[e]));
-          f[e] = fmaf(a[e], dz, -fmaf(c, k2[e], k1[e]));
+        for (int i = 0; i < P; i++) {
+          const F2 c = add2(f[i], mu[i]);
+          const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
+          f[i] = fma2(sc[i], dz, fma2(c, k2[i], k1[i]));
         }
-        st_stream(o, Vec<T>::pack(f));
+        st_stream(o, Pairs<T>::pack(f));
       }
+  });
+}
+
+// Raises the shared-memory limit of two kernels, once a device.
+template <typename K1, typename K2>
+cudaError_t gn_raise(K1 k1, K2 k2, int bytes, std::atomic<int>* done) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (done[device].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[device].store(1, std::memory_order_release);
+  return e;
+}
+
+template <typename T, bool BACK, bool SILU>
+cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
+  using B = GnBlock<T, BACK>;
+  void (*stats)(const GnArgs, const GnGeom);
+  void (*apply)(const GnArgs, const GnGeom);
+  if constexpr (BACK) {
+    stats = gn_grad_stats_kernel<T, SILU>;
+    apply = gn_grad_apply_kernel<T, SILU>;
+  } else {
+    stats = gn_stats_kernel<T>;
+    apply = gn_apply_kernel<T, SILU>;
   }
+  static std::atomic<int> done[64];
+  cudaError_t e = gn_raise(stats, apply, B::kMostSmem, done);
+  if (e != cudaSuccess) return e;
+  const GnGeom g = gn_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups);
+  GnArgs a;
+  a.out = in.out;
+  a.x = in.x;
+  a.dy = in.dy;
+  a.mean = in.mean;
+  a.rstd = in.rstd;
+  a.prm = GnParams{in.w, in.b, in.w_is_bf16};
+  a.dw = in.dw;
+  a.db = in.db;
+  a.eps = in.eps;
+  a.scratch.parts = static_cast<float2*>(in.workspace);
+  a.scratch.sums = a.scratch.parts + g.samples * g.chunks * (g.groups + g.tiles);
+  // the ring's used part, or what joining needs
+  const int64_t turns = (g.steps + g.chunks - 1) / g.chunks;
+  const int ring = B::kStepBytes * static_cast<int>(turns < B::kRing ? turns : B::kRing);
+  const size_t smem = ring > B::kScratch ? ring : B::kScratch;
+  const dim3 grid(static_cast<unsigned>(g.samples * g.chunks * g.tiles));
+  e = launch_pdl(stats, grid, dim3(B::kThreads), smem, s, a, g);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(apply, grid, dim3(B::kThreads), smem, s, a, g);
 }
 
-// Threads of a block: its columns and lanes, in whole warps (the warps of the
-// reductions shuffle with every lane).
-unsigned gn_threads(const GnGeom& g) {
-  return static_cast<unsigned>((g.tile_cols * g.lanes + kWarp - 1) / kWarp * kWarp);
-}
-
-unsigned gn_grid(const GnGeom& g, int64_t samples) {
-  return static_cast<unsigned>(samples * g.chunks * g.tiles);
+template <typename T, bool BACK>
+cudaError_t gn_launch_act(const GroupNormArgs& in, cudaStream_t s) {
+  return in.silu ? gn_launch<T, BACK, true>(in, s) : gn_launch<T, BACK, false>(in, s);
 }
 
 template <typename T>
-cudaError_t gn_forward(const GroupNormArgs& a, cudaStream_t s) {
-  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N, kGnPerSm);
-  const GnParams prm{a.w, a.b, a.w_is_bf16};
-  float2* parts = static_cast<float2*>(a.workspace);
-  const T* x = static_cast<const T*>(a.x);
-  const unsigned grid = gn_grid(g, a.samples);
-  const unsigned threads = gn_threads(g);
-  cudaError_t e = launch_pdl(gn_stats_kernel<T>, dim3(grid), dim3(threads), 0, s, parts, x, g);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(gn_join_kernel, dim3(static_cast<unsigned>(a.samples * a.groups)),
-                 dim3(kGnJoinThreads), 0, s, a.mean, a.rstd,
-                 static_cast<const float2*>(parts), g, g.tile_cols * Vec<T>::N, a.eps);
-  if (e != cudaSuccess) return e;
-  auto kernel = a.silu ? gn_apply_kernel<T, true> : gn_apply_kernel<T, false>;
-  return launch_pdl(kernel, dim3(grid), dim3(threads), 0, s, static_cast<T*>(a.out), x,
-                    static_cast<const float*>(a.mean), static_cast<const float*>(a.rstd), prm, g);
+int64_t gn_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups) {
+  const int64_t f =
+      gn_scratch_bytes<T, false>(gn_geometry<T, false>(samples, space, channels, groups));
+  const int64_t b =
+      gn_scratch_bytes<T, true>(gn_geometry<T, true>(samples, space, channels, groups));
+  return f > b ? f : b;
 }
 
 template <typename T>
-cudaError_t gn_backward(const GroupNormArgs& a, cudaStream_t s) {
-  const GnGeom g = gn_geometry(a.samples, a.space, a.channels, a.groups, Vec<T>::N, kGnGradPerSm);
-  const GnGradIn in{a.dy, a.x, a.mean, a.rstd, GnParams{a.w, a.b, a.w_is_bf16}};
-  float2* parts = static_cast<float2*>(a.workspace);
-  float2* sums = parts + a.samples * g.chunks * a.channels;
-  const unsigned grid = gn_grid(g, a.samples);
-  const unsigned threads = gn_threads(g);
-  auto stats = a.silu ? gn_grad_stats_kernel<T, true> : gn_grad_stats_kernel<T, false>;
-  cudaError_t e = launch_pdl(stats, dim3(grid), dim3(threads), 0, s, parts, in, g);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(gn_grad_join_kernel,
-                 dim3(static_cast<unsigned>(a.samples * ((a.channels + 31) / 32))),
-                 dim3(32 * kGnSumLanes), 0, s, sums, static_cast<const float2*>(parts), a.rstd, g);
-  if (e != cudaSuccess) return e;
-  auto apply = a.silu ? gn_grad_apply_kernel<T, true> : gn_grad_apply_kernel<T, false>;
-  // groups that one tile can touch
-  const int width = g.tile_cols * Vec<T>::N;
-  const size_t smem = sizeof(float2) * static_cast<size_t>((width - 1) / g.cpg + 2);
-  return launch_pdl(apply, dim3(grid), dim3(threads), smem, s, static_cast<T*>(a.out), a.dw, a.db,
-                    static_cast<const float2*>(sums), in, g, static_cast<int>(a.samples));
+int64_t gn_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups) {
+  const GnGeom f = gn_geometry<T, false>(samples, space, channels, groups);
+  const GnGeom b = gn_geometry<T, true>(samples, space, channels, groups);
+  const int64_t most = static_cast<int64_t>(f.chunks) * f.tiles;
+  const int64_t more = static_cast<int64_t>(b.chunks) * b.tiles;
+  return samples * (most > more ? most : more);
 }
 
 }  // namespace
 
 int64_t group_norm_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                              int is_bf16) {
-  const int vec = is_bf16 ? 8 : 4;
-  const GnGeom f = gn_geometry(samples, space, channels, groups, vec, kGnPerSm);
-  const GnGeom b = gn_geometry(samples, space, channels, groups, vec, kGnGradPerSm);
-  const int64_t forward = samples * f.chunks * (groups + f.tiles);
-  const int64_t backward = samples * (b.chunks + 1) * channels;
-  return static_cast<int64_t>(sizeof(float2)) * (forward > backward ? forward : backward);
+  return is_bf16 ? gn_workspace<__nv_bfloat16>(samples, space, channels, groups)
+                 : gn_workspace<float>(samples, space, channels, groups);
 }
 
 int64_t group_norm_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                           int is_bf16) {
-  const GnGeom g = gn_geometry(samples, space, channels, groups, is_bf16 ? 8 : 4, kGnPerSm);
-  const int64_t blocks = g.chunks * static_cast<int64_t>(g.tiles);
-  const int64_t joins = groups > (channels + 31) / 32 ? groups : (channels + 31) / 32;
-  return samples * (blocks > joins ? blocks : joins);
+  return is_bf16 ? gn_blocks<__nv_bfloat16>(samples, space, channels, groups)
+                 : gn_blocks<float>(samples, space, channels, groups);
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, int is_bf16, cudaStream_t stream) {
-  return is_bf16 ? gn_forward<__nv_bfloat16>(a, stream) : gn_forward<float>(a, stream);
+  return is_bf16 ? gn_launch_act<__nv_bfloat16, false>(a, stream)
+                 : gn_launch_act<float, false>(a, stream);
 }
 
 cudaError_t launch_group_norm_backward(const GroupNormArgs& a, int is_bf16, cudaStream_t stream) {
-  return is_bf16 ? gn_backward<__nv_bfloat16>(a, stream) : gn_backward<float>(a, stream);
+  return is_bf16 ? gn_launch_act<__nv_bfloat16, true>(a, stream)
+                 : gn_launch_act<float, true>(a, stream);
 }
 
 }  // namespace nr

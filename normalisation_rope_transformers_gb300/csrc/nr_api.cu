@@ -697,7 +697,9 @@ nr_status check_group_norm_sizes(const char* fn, int64_t samples, int64_t space,
   if (channels % vec != 0)
     return fail(NR_ERR_UNSUPPORTED, "%s: channels = %lld is not a multiple of %d", fn,
                 (long long)channels, vec);
-  if (channels > (1 << 20) || samples > INT32_MAX || space > INT64_MAX / 16 / channels ||
+  if (channels > 65536)
+    return fail(NR_ERR_UNSUPPORTED, "%s: channels = %lld is above 65536", fn, (long long)channels);
+  if (samples > INT32_MAX || space > INT64_MAX / 16 / channels ||
       (samples > 0 && space * channels > INT64_MAX / 16 / samples))
     return fail(NR_ERR_SHAPE, "%s: samples, space or channels too large", fn);
   if (samples > 0 && space > 0 &&
