@@ -285,7 +285,7 @@ nr_status nr_kv_cache_write(const nr_kv_cache* cache, const void* k, const void*
  * head_dim    bf16: 64, 128, 256 or 512; f32: 32, 64, 128 or 256.  With
  *             NR_CACHE_MXFP4 a multiple of 64, and so is rotary_dim for
  *             rotate-half pairs.
- * Errors: as nr_rmsnorm; nr_device_status as nr_qk_norm_rope.
+ * Errors: as nr_rmsnorm.
  */
 nr_status nr_qk_norm_rope_cache(const nr_kv_cache* cache, void* q_out, const void* q,
                                 const void* k, const void* v, const void* wq, const void* wk,
@@ -446,8 +446,8 @@ nr_status nr_gelu_and_mul(void* out, const void* x, int64_t rows, int64_t inter,
 
 /*
  * Device-side failure report.  Kernels that wait on hardware events (the
- * bulk-copy paths of nr_qk_norm_rope and nr_qk_norm_rope_cache wait for their
- * copies on shared-memory barriers) bound every wait (about one second of SM clock); a wait that runs
+ * bulk-copy path of nr_qk_norm_rope waits for its copies on shared-memory
+ * barriers) bound every wait (about one second of SM clock); a wait that runs
  * out sets a bit in a status word the library keeps on each device, the
  * kernel lets its copies in flight finish and returns, and the outputs of
  * that call are not valid.  nr_device_status works on the device that owns

@@ -133,52 +133,6 @@ int64_t gn_scratch_bytes(const GnGeom& g) {
   return g.samples * g.chunks * row * static_cast<int64_t>(sizeof(float2));
 }
 
-// Two f32 values side by side; one instruction works on both.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-// A 128-bit vector as pairs of values.
-template <typename T>
-struct Pairs {
-  static constexpr int N = Vec<T>::N / 2;
-  __device__ __forceinline__ static void unpack(const uint4& v, F2 (&p)[N]) {
-    float f[Vec<T>::N];
-    Vec<T>::unpack(v, f);
-#pragma unroll
-    for (int i = 0; i < N; i++) p[i] = f2(f[2 * i], f[2 * i + 1]);
-  }
-  __device__ __forceinline__ static uint4 pack(const F2 (&p)[N]) {
-    float f[Vec<T>::N];
-#pragma unroll
-    for (int i = 0; i < N; i++) split(p[i], f[2 * i], f[2 * i + 1]);
-    return Vec<T>::pack(f);
-  }
-};
-
 // A parameter vector's N values of this thread's channels (`none` without one).
 template <int N>
 __device__ __forceinline__ void gn_params(const void* p, int is_bf16, int channel, float none,

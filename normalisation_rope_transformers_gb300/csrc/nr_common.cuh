@@ -344,6 +344,66 @@ struct Vec<__nv_bfloat16> {
 };
 
 // ---------------------------------------------------------------------------
+// Two f32 values side by side; one instruction works on both, each rounded as
+// the f32 operation is.
+// ---------------------------------------------------------------------------
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+template <int P>
+__device__ __forceinline__ void from_pairs(const F2 (&p)[P], float (&v)[2 * P]) {
+#pragma unroll
+  for (int i = 0; i < P; i++) split(p[i], v[2 * i], v[2 * i + 1]);
+}
+
+// A 128-bit vector as pairs of values.
+template <typename T>
+struct Pairs {
+  static constexpr int N = Vec<T>::N / 2;
+  __device__ __forceinline__ static void unpack(const uint4& v, F2 (&p)[N]) {
+    float f[Vec<T>::N];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < N; i++) p[i] = f2(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ static uint4 pack(const F2 (&p)[N]) {
+    float f[Vec<T>::N];
+#pragma unroll
+    for (int i = 0; i < N; i++) split(p[i], f[2 * i], f[2 * i + 1]);
+    return Vec<T>::pack(f);
+  }
+};
+
+// ---------------------------------------------------------------------------
 // FP8 e4m3 codes: round to nearest even, finite values beyond +-448 saturate
 // (CUDA's conversion, two values per call).
 // ---------------------------------------------------------------------------

@@ -192,7 +192,6 @@ cudaError_t launch_group_norm_backward(const GroupNormArgs& args, int is_bf16,
 // Device status word: bits set by kernels whose bounded waits ran out.
 constexpr unsigned kStatusBitQkBulkWait = 1u;
 constexpr unsigned kStatusBitProbeWait = 2u;
-constexpr unsigned kStatusBitCacheBulkWait = 4u;
 
 // Device address of the current device's status word (status.cu), looked up
 // once per device.  Kernels that bound a wait take it as an argument.

@@ -8,16 +8,18 @@
 // re-reading K.
 //
 // Design.  A token's head rows (Q, then K, then V) are one list, cut into
-// items of `chunk` rows (about 8 KB); an item may span the tensors.  A block
-// of four warps takes items b, b + grid, ...: bulk copies bring an item's rows
-// (up to three contiguous pieces) into one of NST shared-memory stages ahead
-// of time, the warps work on it, Q rows are written back in place and leave by
-// one bulk copy, codes and scales leave from registers.  A group of L lanes
-// owns one head row, a lane the two vectors that rotate into one another.
-// The next item's angles are computed beside the current rows, into the other
-// of two tables, with the exact turn arithmetic of the Q/K kernels.  Waits on
-// the copies are bounded and report through the device status word.  Small
-// items keep many blocks busy for single tokens and fit any number of heads.
+// items of whole warp passes; a warp takes items w, w + W, ... and works on its
+// own: it copies its rows RING passes ahead into a ring of its own (cp.async),
+// computes an item's angles once into a table of its own, and no block barrier
+// follows the set-up.  A group of L lanes owns one head row, a lane the two
+// vectors that rotate into one another; the arithmetic is on pairs of f32
+// values.  Calls of many tokens take whole tokens as items; small ones cut them
+// until every warp has work.  Angles are the exact turns of the Q/K kernels.
+//
+// At [26598, 24 + 24 + 24, 128] bf16 -> fp8 a block of four warps with bulk-copy
+// stages and one barrier an item took 166 us (whole tokens) to 307 us (items
+// of a third): about 2 us an item whatever its rows, in the chain from the
+// barrier through the angles to the next barrier.
 #include <atomic>
 #include <type_traits>
 
@@ -28,12 +30,10 @@ namespace {
 
 constexpr int kFusedThreads = 128;
 constexpr int kFusedWarps = kFusedThreads / kWarp;
-constexpr int kStages = 3;
-// Bytes of an item: calls of many tokens take whole tokens where they fit (one
-// barrier and one angle table for more rows), small calls spread their rows.
-constexpr int kItemBytesMany = 20 * 1024;
-constexpr int kItemBytesFew = 8 * 1024;
-constexpr long long kFusedWaitLimit = 1LL << 31;  // SM cycles, about one second
+// Passes in flight of a warp: 3, 5 and 8 ran [26598, 24 + 24 + 24, 128] in 135,
+// 133 and 133 us.
+constexpr int kRing = 5;
+constexpr int kFusedPerSm = 4;  // resident blocks (three: 144 us)
 
 struct FusedArgs {
   void* q_out;
@@ -51,10 +51,8 @@ struct FusedArgs {
   int hq, hk;
   int chunk;  // rows of an item
   int items;  // items of a token
-  unsigned stage_bytes;
   float eps, inv_d, w_add;
   int rot_vec, interleaved, mrope;
-  unsigned* status;
 };
 
 __device__ __forceinline__ float weight_of(const float* w, int i) { return __ldg(w + i); }
@@ -67,116 +65,38 @@ struct FusedSmem {
   static constexpr int N = Vec<T>::N;
   static constexpr int HALF = L * N;
   static constexpr int D = 2 * HALF;
-  // [kStages stages][2 angle tables of HALF float2][2D weights][HALF turns][mbarriers][flag]
-  static size_t bytes(unsigned stage_bytes) {
-    return static_cast<size_t>(kStages) * stage_bytes + 2 * HALF * sizeof(float2) +
-           2 * D * sizeof(float) + HALF * sizeof(unsigned long long) +
-           kStages * sizeof(unsigned long long) + 16;
-  }
+  // a warp: ring of two vectors a lane, angle table (cos, sin); a block: turns, axes
+  static constexpr int kWarpBytes =
+      kRing * kWarp * 2 * static_cast<int>(sizeof(uint4)) + HALF * static_cast<int>(sizeof(float2));
+  static constexpr int kBytes = kFusedWarps * kWarpBytes +
+                                HALF * static_cast<int>(sizeof(unsigned long long)) + HALF;
 };
 
 // GEN: partial rotation, GPT-J pairs and M-RoPE, chosen at run time.
 template <typename T, typename WT, int L, bool FP4, bool GEN>
-__global__ void __launch_bounds__(kFusedThreads) qk_cache_kernel(const FusedArgs a,
-                                                                 const RopeTurns turns) {
+__global__ void __launch_bounds__(kFusedThreads, kFusedPerSm)
+    qk_cache_kernel(const FusedArgs a, const RopeTurns turns) {
   using S = FusedSmem<T, L>;
-  constexpr int N = S::N;
+  constexpr int N = S::N, P = N / 2;
   constexpr int HALF = S::HALF;
   constexpr int D = S::D;
-  constexpr int GW = kWarp / L;           // head rows of a warp pass
+  constexpr int GW = kWarp / L;               // head rows of a pass
   constexpr int W = 32 / N < L ? 32 / N : L;  // lanes of one 32-element group
 
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char* stages = smem;
-  float2* table = reinterpret_cast<float2*>(stages + kStages * static_cast<size_t>(a.stage_bytes));
-  float* wsm = reinterpret_cast<float*>(table + 2 * HALF);
-  unsigned long long* turn_sm = reinterpret_cast<unsigned long long*>(wsm + 2 * D);
-  unsigned long long* bars = turn_sm + HALF;
-  int* abort_flag = reinterpret_cast<int*>(bars + kStages);
-
-  const int tid = threadIdx.x;
-  const int warp = tid / kWarp, lane32 = tid % kWarp;
-  for (int i = tid; i < HALF; i += kFusedThreads) turn_sm[i] = turns.turn[i];
-  if (tid == 0) {
-    for (int st = 0; st < kStages; st++) mbar_init(smem_addr(bars + st), 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+  const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  uint4* ring = reinterpret_cast<uint4*>(smem + warp * S::kWarpBytes) + lane32;  // [kRing][2][32]
+  float2* table = reinterpret_cast<float2*>(smem + warp * S::kWarpBytes +
+                                            kRing * kWarp * 2 * sizeof(uint4));
+  unsigned long long* turn_sm =
+      reinterpret_cast<unsigned long long*>(smem + kFusedWarps * S::kWarpBytes);
+  unsigned char* axis_sm = reinterpret_cast<unsigned char*>(turn_sm + HALF);
+  for (int i = threadIdx.x; i < HALF; i += kFusedThreads) {
+    turn_sm[i] = turns.turn[i];
+    if (GEN) axis_sm[i] = turns.axis[i];
   }
-
-  const int rows = a.hq + 2 * a.hk;
-  const T* q = static_cast<const T*>(a.q);
-  const T* k = static_cast<const T*>(a.k);
-  const T* v = static_cast<const T*>(a.v);
-
-  // An item: token and first row.  A block's items are `step` apart.
-  struct Item {
-    int64_t tok;
-    int c;
-  };
-  const int64_t step_tok = gridDim.x / a.items;
-  const int step_c = static_cast<int>(gridDim.x % a.items);
-  auto next = [&](Item& it) {
-    it.tok += step_tok;
-    it.c += step_c;
-    if (it.c >= a.items) {
-      it.c -= a.items;
-      it.tok++;
-    }
-  };
-  Item cur{static_cast<int64_t>(blockIdx.x / a.items), static_cast<int>(blockIdx.x % a.items)};
-  Item ahead = cur;  // producer (thread 0): the next item to load
-  int64_t issued = 0;
-  const uint64_t policy = l2_evict_first_policy();
-  auto stage = [&](int64_t j) { return stages + (j % kStages) * static_cast<size_t>(a.stage_bytes); };
-  auto issue = [&]() {
-    const unsigned bar = smem_addr(bars + issued % kStages);
-    unsigned dst = smem_addr(stage(issued));
-    const int r0 = ahead.c * a.chunk, r1 = min(r0 + a.chunk, rows);
-    mbar_arrive_expect_tx(bar, static_cast<unsigned>((r1 - r0) * D * sizeof(T)));
-    auto piece = [&](const T* base, int lo, int hi) {  // rows [lo, hi) of one tensor
-      if (hi <= lo) return;
-      const unsigned bytes = static_cast<unsigned>((hi - lo) * D * sizeof(T));
-      bulk_load_hint(dst, base + static_cast<int64_t>(lo) * D, bytes, bar, policy);
-      dst += bytes;
-    };
-    piece(q + ahead.tok * a.q_stride, r0, min(r1, a.hq));
-    piece(k + ahead.tok * a.k_stride, max(r0 - a.hq, 0), min(r1 - a.hq, a.hk));
-    piece(v + ahead.tok * a.v_stride, max(r0 - a.hq - a.hk, 0), r1 - a.hq - a.hk);
-    issued++;
-    next(ahead);
-  };
-  pdl_enter();  // before any global read: the previous kernel may still run
-  if (tid == 0)
-    for (int j = 0; j < kStages - 1 && ahead.tok < a.tokens; j++) issue();
-  const WT* wq = static_cast<const WT*>(a.wq);
-  const WT* wk = static_cast<const WT*>(a.wk);
-  for (int i = tid; i < 2 * D; i += kFusedThreads)
-    wsm[i] = (i < D ? weight_of(wq, i) : weight_of(wk, i - D)) + a.w_add;
-
-  // This thread's pairs of an item's angle table (threads below the pair count).
-  const int pairs = GEN ? a.rot_vec * N / 2 : HALF;
-  auto position = [&](const Item& it, int i) -> int {
-    return a.pos[(GEN && a.mrope ? turns.axis[i] * a.tokens : 0) + it.tok];
-  };
-  auto angle = [&](float2* t, int i, int p) {
-    const unsigned long long prod = static_cast<unsigned long long>(static_cast<long long>(p)) *
-                                    turn_sm[i];
-    const int hi = static_cast<int>(prod >> 32);  // signed turn fraction * 2^32
-    float sn, cn;
-    sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);
-    t[i] = make_float2(cn, sn);
-  };
-  __syncthreads();  // weights, turns and barriers visible
-  Item nxt = cur;
-  next(nxt);
-  int pos_next = 0;
-  int64_t slot = -1;
-  if (cur.tok < a.tokens) {
-    slot = __ldg(a.slots + cur.tok);
-    for (int i = tid; i < pairs; i += kFusedThreads) angle(table, i, position(cur, i));
-    if (nxt.tok < a.tokens && tid < pairs) pos_next = position(nxt, tid);
-  }
-  __syncthreads();
+  __syncthreads();  // the only block-level barrier
+  pdl_enter();      // before any global read: the previous kernel may still run
 
   const int g = lane32 / L, l = lane32 % L;
   // The two vectors of this lane: rotate-half partners, the halves of what is
@@ -193,118 +113,228 @@ __global__ void __launch_bounds__(kFusedThreads) qk_cache_kernel(const FusedArgs
       rotates = false;
     }
   }
-  float wqa[N], wqb[N], wka[N], wkb[N];
+  const int rows = a.hq + 2 * a.hk;
+
+  // An item: its token and first row.  A cursor walks this warp's items pass by pass.
+  struct Cursor {
+    int64_t tok;
+    int row, end;  // next pass's first row, end of the item's rows
+    int c;         // item of the token
+  };
+  const int64_t W_items = static_cast<int64_t>(gridDim.x) * kFusedWarps;
+  const int64_t step_tok = W_items / a.items;
+  const int step_c = static_cast<int>(W_items % a.items);
+  auto open = [&](Cursor& u) {
+    u.row = u.c * a.chunk;
+    u.end = min(u.row + a.chunk, rows);
+  };
+  auto next_item = [&](Cursor& u) {
+    u.tok += step_tok;
+    u.c += step_c;
+    if (u.c >= a.items) {
+      u.c -= a.items;
+      u.tok++;
+    }
+    open(u);
+  };
+  Cursor cur;
+  {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kFusedWarps + warp;
+    cur.tok = first / a.items;
+    cur.c = static_cast<int>(first - cur.tok * a.items);
+    open(cur);
+  }
+  if (cur.tok >= a.tokens) return;
+  Cursor cp = cur;
+  // Starts the copies of the copy cursor's pass into a ring slot, one group.
+  auto issue = [&](int slot) {
+    if (cp.tok < a.tokens) {
+      const int row = cp.row + g;
+      if (row < cp.end) {
+        const bool is_q = row < a.hq, is_v = row >= a.hq + a.hk;
+        const T* p = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) +
+                     cp.tok * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) +
+                     (row - (is_q ? 0 : is_v ? a.hq + a.hk : a.hq)) * D;
+        cp_async16(smem_addr(ring + slot * 2 * kWarp), p + va * N);
+        cp_async16(smem_addr(ring + (slot * 2 + 1) * kWarp), p + vb * N);
+      }
+      cp.row += GW;
+      if (cp.row >= cp.end) next_item(cp);
+    }
+    cp_async_commit();  // possibly empty: keeps one group a pass
+  };
+  for (int s = 0; s < kRing; s++) issue(s);
+
+  // This lane's weights.
+  F2 wqa[P], wqb[P], wka[P], wkb[P];
+  {
+    const WT* wq = static_cast<const WT*>(a.wq);
+    const WT* wk = static_cast<const WT*>(a.wk);
+    auto get = [&](const WT* w, int vec, F2 (&o)[P]) {
 #pragma unroll
-  for (int e = 0; e < N; e++) {
-    wqa[e] = wsm[va * N + e];
-    wqb[e] = wsm[vb * N + e];
-    wka[e] = wsm[D + va * N + e];
-    wkb[e] = wsm[D + vb * N + e];
+      for (int i = 0; i < P; i++) {
+        const int e = vec * N + 2 * i;
+        o[i] = f2(weight_of(w, e) + a.w_add, weight_of(w, e + 1) + a.w_add);
+      }
+    };
+    get(wq, va, wqa);
+    get(wq, vb, wqb);
+    get(wk, va, wka);
+    get(wk, vb, wkb);
   }
 
-  int64_t j = 0;
-  for (; cur.tok < a.tokens; j++) {
-    unsigned char* st = stage(j);
-    int64_t slot_next = -1;
-    if (nxt.tok < a.tokens) slot_next = __ldg(a.slots + nxt.tok);
-    if (!mbar_wait_bounded(smem_addr(bars + j % kStages), static_cast<unsigned>((j / kStages) & 1),
-                           kFusedWaitLimit)) {
-      atomicOr(a.status, kStatusBitCacheBulkWait);
-      *abort_flag = 1;
+  // Position and slot of an item's token, loaded one item ahead.
+  constexpr int NPOS = GEN ? 3 : 1;
+  int pos[NPOS];
+  int64_t slot_of_token = -1;
+  auto fetch = [&](const Cursor& u) {
+    slot_of_token = -1;
+    if (u.tok < a.tokens) {
+      slot_of_token = __ldg(a.slots + u.tok);
+#pragma unroll
+      for (int ax = 0; ax < NPOS; ax++)
+        pos[ax] = (ax == 0 || a.mrope) ? __ldg(a.pos + ax * a.tokens + u.tok) : 0;
     }
-    const float2* tb = table + (j & 1) * HALF;
-    float2 cs[N];
+  };
+  fetch(cur);
+  const int pairs = GEN ? a.rot_vec * N / 2 : HALF;
+
+  int slot = 0;
+  while (cur.tok < a.tokens) {
+    // A new item: its angles, once a warp, then this lane's; its place in the
+    // cache (a slot outside it keeps nothing).
+    __syncwarp();
+    for (int i = lane32; i < pairs; i += kWarp) {
+      long long p = pos[0];
+      if (GEN && a.mrope) {
+        if (axis_sm[i] == 1) p = pos[NPOS > 1 ? 1 : 0];
+        if (axis_sm[i] == 2) p = pos[NPOS > 2 ? 2 : 0];
+      }
+      // the angle in turns, mod 1: exact for any int32 position
+      const unsigned long long prod = static_cast<unsigned long long>(p) * turn_sm[i];
+      const int hi = static_cast<int>(prod >> 32);  // signed turn fraction * 2^32
+      float sn, cn;
+      sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);  // angle = pi * hi / 2^31
+      table[i] = make_float2(cn, sn);
+    }
+    __syncwarp();
+    // rotate-half: cos and sin of the lane's N pairs; GPT-J: of the pairs inside
+    // its two vectors, N / 2 each
+    F2 co[P], si[P];
     if (!GEN || !a.interleaved) {
       if (rotates) {
 #pragma unroll
-        for (int e = 0; e < N; e++) cs[e] = tb[l * N + e];
+        for (int i = 0; i < P; i++) {
+          const float2 x = table[l * N + 2 * i], y = table[l * N + 2 * i + 1];
+          co[i] = f2(x.x, y.x);
+          si[i] = f2(x.y, y.y);
+        }
       }
     } else {
 #pragma unroll
-      for (int h = 0; h < N / 2; h++) {
-        if (va < a.rot_vec) cs[h] = tb[va * (N / 2) + h];
-        if (vb < a.rot_vec) cs[N / 2 + h] = tb[vb * (N / 2) + h];
+      for (int h = 0; h < P; h++) {  // co[h]: (cos, sin) in va, si[h]: in vb
+        if (va < a.rot_vec) co[h] = f2(table[va * P + h].x, table[va * P + h].y);
+        if (vb < a.rot_vec) si[h] = f2(table[vb * P + h].x, table[vb * P + h].y);
       }
     }
-    const int r0 = cur.c * a.chunk, r1 = min(r0 + a.chunk, rows);
-    // The token's place in the cache; a slot outside it keeps nothing.
-    const bool kept = slot >= 0 && slot < a.geo.slots;
+    const bool kept = slot_of_token >= 0 && slot_of_token < a.geo.slots;
     int64_t code_off = 0, scale_off = 0;
-    if (r1 > a.hq && kept) {
-      const int64_t block = a.geo.block_of(slot);
-      const int64_t place = slot - block * a.geo.block_size;
+    if (kept) {
+      const int64_t block = a.geo.block_of(slot_of_token);
+      const int64_t place = slot_of_token - block * a.geo.block_size;
       code_off = block * a.geo.code_block_stride + place * a.geo.code_row;
       scale_off = block * a.geo.scale_block_stride + place * a.geo.scale_row;
     }
+    Cursor after = cur;
+    next_item(after);
+    fetch(after);
 
     // One pass of GW rows.  KIND 0: all Q, 1: all K, 2: all V, 3: any mix, or
     // past the last row (those lanes still join the shuffles).
     auto pass = [&](auto kind, int first) {
       constexpr int KIND = decltype(kind)::value;
       const int row = first + g;
-      const bool valid = KIND != 3 || row < r1;
+      const bool valid = KIND != 3 || row < cur.end;
       const bool is_q = KIND == 0 || (KIND == 3 && row < a.hq);
       const bool is_v = KIND == 2 || (KIND == 3 && row >= a.hq + a.hk);
-      uint4* r = reinterpret_cast<uint4*>(st + static_cast<size_t>(valid ? row - r0 : 0) * D *
-                                                   sizeof(T));
-      float xa[N], xb[N];
-      Vec<T>::unpack(r[va], xa);
-      Vec<T>::unpack(r[vb], xb);
-      if (KIND != 2) {
-        float ss = 0.0f;
+      F2 xa[P], xb[P];
+      if (valid) {
+        Pairs<T>::unpack(lds128(ring + slot * 2 * kWarp), xa);
+        Pairs<T>::unpack(lds128(ring + (slot * 2 + 1) * kWarp), xb);
+      } else {
 #pragma unroll
-        for (int e = 0; e < N; e++) {
-          ss = fmaf(xa[e], xa[e], ss);
-          ss = fmaf(xb[e], xb[e], ss);
-        }
-        ss = group_sum<L>(ss);
+        for (int i = 0; i < P; i++) xa[i] = xb[i] = f2(0.0f, 0.0f);
+      }
+      if (KIND != 2) {
+        F2 sq = mul2(xa[0], xa[0]);
+#pragma unroll
+        for (int i = 1; i < P; i++) sq = fma2(xa[i], xa[i], sq);
+#pragma unroll
+        for (int i = 0; i < P; i++) sq = fma2(xb[i], xb[i], sq);
+        float s0, s1;
+        split(sq, s0, s1);
+        const float ss = group_sum<L>(s0 + s1);
         if (KIND != 3 || !is_v) {
           const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+          const F2 inv2 = f2(inv, inv);
 #pragma unroll
-          for (int e = 0; e < N; e++) {
-            xa[e] *= inv * (KIND == 0 ? wqa[e] : KIND == 1 ? wka[e] : is_q ? wqa[e] : wka[e]);
-            xb[e] *= inv * (KIND == 0 ? wqb[e] : KIND == 1 ? wkb[e] : is_q ? wqb[e] : wkb[e]);
+          for (int i = 0; i < P; i++) {
+            const bool q_row = KIND == 0 || (KIND == 3 && is_q);
+            xa[i] = mul2(mul2(xa[i], inv2), KIND == 3 ? (q_row ? wqa[i] : wka[i])
+                                                      : KIND == 0 ? wqa[i] : wka[i]);
+            xb[i] = mul2(mul2(xb[i], inv2), KIND == 3 ? (q_row ? wqb[i] : wkb[i])
+                                                      : KIND == 0 ? wqb[i] : wkb[i]);
           }
           if (!GEN || (!a.interleaved && rotates)) {
 #pragma unroll
-            for (int e = 0; e < N; e++) {
-              const float na = xa[e], nb = xb[e];
-              xa[e] = fmaf(na, cs[e].x, -nb * cs[e].y);
-              xb[e] = fmaf(na, cs[e].y, nb * cs[e].x);
+            for (int i = 0; i < P; i++) {
+              const F2 na = xa[i], nb = xb[i];
+              xa[i] = sub2(mul2(na, co[i]), mul2(nb, si[i]));
+              xb[i] = fma2(na, si[i], mul2(nb, co[i]));
             }
           } else if (a.interleaved) {
 #pragma unroll
-            for (int h = 0; h < N / 2; h++) {
-              if (va < a.rot_vec) {
-                const float x0 = xa[2 * h], x1 = xa[2 * h + 1];
-                xa[2 * h] = fmaf(x0, cs[h].x, -x1 * cs[h].y);
-                xa[2 * h + 1] = fmaf(x0, cs[h].y, x1 * cs[h].x);
-              }
-              if (vb < a.rot_vec) {
-                const float x0 = xb[2 * h], x1 = xb[2 * h + 1];
-                xb[2 * h] = fmaf(x0, cs[N / 2 + h].x, -x1 * cs[N / 2 + h].y);
-                xb[2 * h + 1] = fmaf(x0, cs[N / 2 + h].y, x1 * cs[N / 2 + h].x);
-              }
+            for (int h = 0; h < P; h++) {
+              auto turn = [](F2& x, F2 cs) {
+                float x0, x1, c, s;
+                split(x, x0, x1);
+                split(cs, c, s);
+                x = f2(fmaf(x0, c, -x1 * s), fmaf(x0, s, x1 * c));
+              };
+              if (va < a.rot_vec) turn(xa[h], co[h]);
+              if (vb < a.rot_vec) turn(xb[h], si[h]);
             }
           }
         }
       }
       if (KIND == 0 || (KIND == 3 && is_q && valid)) {
-        r[va] = Vec<T>::pack(xa);
-        r[vb] = Vec<T>::pack(xb);
+        T* o = static_cast<T*>(a.q_out) + cur.tok * a.q_stride + row * D;
+        st_stream(o + va * N, Pairs<T>::pack(xa));
+        st_stream(o + vb * N, Pairs<T>::pack(xb));
       }
       if (KIND == 0) return;
       const int head = row - a.hq - (is_v ? a.hk : 0);
       const CacheSide side = is_v ? a.side[1] : a.side[0];
       const bool write = kept && valid && !is_q;
+      float fa[N], fb[N];
       if constexpr (!FP4) {
-        const float top = clamp_scale(group_max<L>(fmaxf(max_abs(xa), max_abs(xb))));
+        from_pairs<P>(xa, fa);
+        from_pairs<P>(xb, fb);
+        const float top = clamp_scale(group_max<L>(fmaxf(max_abs(fa), max_abs(fb))));
         if (!write) return;
         const float inv = fp8_inverse(top);
-        unsigned char* o = side.codes + code_off + static_cast<int64_t>(head) * D;
+        const F2 inv2 = f2(inv, inv);
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+          xa[i] = mul2(xa[i], inv2);
+          xb[i] = mul2(xb[i], inv2);
+        }
+        from_pairs<P>(xa, fa);
+        from_pairs<P>(xb, fb);
+        unsigned char* o = side.codes + code_off + head * D;
         uint32_t ca[N / 4], cb[N / 4];
-        fp8_codes(xa, inv, ca);
-        fp8_codes(xb, inv, cb);
+        fp8_codes_scaled(fa, ca);
+        fp8_codes_scaled(fb, cb);
         if constexpr (N == 8) {
           st_stream8(o + va * N, make_uint2(ca[0], ca[N / 4 - 1]));
           st_stream8(o + vb * N, make_uint2(cb[0], cb[N / 4 - 1]));
@@ -314,12 +344,14 @@ __global__ void __launch_bounds__(kFusedThreads) qk_cache_kernel(const FusedArgs
         }
         if (l == 0) reinterpret_cast<float*>(side.scales + scale_off)[head] = fp8_scale(top);
       } else {
-        const uint32_t ba = mx_scale_byte(clamp_scale(group_max<W>(max_abs(xa))));
-        const uint32_t bb = mx_scale_byte(clamp_scale(group_max<W>(max_abs(xb))));
+        from_pairs<P>(xa, fa);
+        from_pairs<P>(xb, fb);
+        const uint32_t ba = mx_scale_byte(clamp_scale(group_max<W>(max_abs(fa))));
+        const uint32_t bb = mx_scale_byte(clamp_scale(group_max<W>(max_abs(fb))));
         if (!write) return;
-        unsigned char* o = side.codes + code_off + static_cast<int64_t>(head) * (D / 2);
-        unsigned char* s = side.scales + scale_off + static_cast<int64_t>(head) * (D / 32);
-        const uint32_t ca = fp4_codes(xa, mx_inverse(ba)), cb = fp4_codes(xb, mx_inverse(bb));
+        unsigned char* o = side.codes + code_off + head * (D / 2);
+        unsigned char* s = side.scales + scale_off + head * (D / 32);
+        const uint32_t ca = fp4_codes(fa, mx_inverse(ba)), cb = fp4_codes(fb, mx_inverse(bb));
         if constexpr (N == 8) {
           st_stream4(o + va * 4, ca);
           st_stream4(o + vb * 4, cb);
@@ -333,105 +365,46 @@ __global__ void __launch_bounds__(kFusedThreads) qk_cache_kernel(const FusedArgs
         }
       }
     };
-    for (int first = r0 + warp * GW; first < r1; first += kFusedWarps * GW) {  // warp-uniform
+    for (int first = cur.row; first < cur.end; first += GW) {  // warp-uniform
+      cp_async_wait<kRing - 1>();  // this pass's group has landed
       const int last = first + GW;
-      if (last <= r1 && last <= a.hq)
+      if (last <= cur.end && last <= a.hq)
         pass(std::integral_constant<int, 0>(), first);
-      else if (last <= r1 && first >= a.hq && last <= a.hq + a.hk)
+      else if (last <= cur.end && first >= a.hq && last <= a.hq + a.hk)
         pass(std::integral_constant<int, 1>(), first);
-      else if (last <= r1 && first >= a.hq + a.hk)
+      else if (last <= cur.end && first >= a.hq + a.hk)
         pass(std::integral_constant<int, 2>(), first);
       else
         pass(std::integral_constant<int, 3>(), first);
+      issue(slot);  // the slot's values have been used
+      slot = slot + 1 == kRing ? 0 : slot + 1;
     }
-    // the next item's angles, into the other table
-    const Item done = cur;
-    cur = nxt;
-    next(nxt);
-    slot = slot_next;
-    if (cur.tok < a.tokens) {
-      float2* t = table + ((j + 1) & 1) * HALF;
-      if (tid < pairs) angle(t, tid, pos_next);
-      for (int i = tid + kFusedThreads; i < pairs; i += kFusedThreads) angle(t, i, position(cur, i));
-      if (nxt.tok < a.tokens && tid < pairs) pos_next = position(nxt, tid);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (*abort_flag) break;
-    if (tid == 0) {
-      if (r0 < a.hq)
-        bulk_store_hint(static_cast<T*>(a.q_out) + done.tok * a.q_stride +
-                            static_cast<int64_t>(r0) * D,
-                        smem_addr(st), static_cast<unsigned>((min(r1, a.hq) - r0) * D * sizeof(T)),
-                        policy);
-      bulk_commit();  // possibly empty: one group per item
-      if (ahead.tok < a.tokens) {
-        bulk_wait_read<1>();  // the stage of item j - 1 has been read out
-        issue();
-      }
-    }
+    cur = after;
   }
-  if (tid == 0) {
-    bulk_wait<0>();  // every store has landed before the block's shared memory is released
-    // After an abandoned wait (at item j), let the loads still in flight
-    // finish (bounded); after a normal finish there are none (j == issued).
-    for (int64_t m = j; m < issued; m++)
-      if (!mbar_wait_bounded(smem_addr(bars + m % kStages),
-                             static_cast<unsigned>((m / kStages) & 1), kFusedWaitLimit))
-        break;
-  }
+  cp_async_wait<0>();  // nothing may land after the block's shared memory is released
 }
 
-// Resident blocks over the current device for this kernel with `smem` bytes;
-// the last answer of each device is kept (a racing thread at worst asks again).
-template <typename Kernel>
-cudaError_t fused_resident(Kernel kernel, size_t smem, std::atomic<uint64_t>* cache,
-                           int64_t* blocks) {
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-  const uint64_t had = cache[device].load(std::memory_order_relaxed);
-  if (had >> 32 == smem) {
-    *blocks = static_cast<int64_t>(had & 0xFFFFFFFFu);
-    return cudaSuccess;
-  }
-  int sms = 0, per_sm = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-  if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kFusedThreads, smem);
-  if (e != cudaSuccess) return e;
-  *blocks = static_cast<int64_t>(sms) * (per_sm > 0 ? per_sm : 1);
-  cache[device].store(static_cast<uint64_t>(smem) << 32 | static_cast<uint64_t>(*blocks),
-                      std::memory_order_relaxed);
-  return cudaSuccess;
-}
+// Warps that reside on the GPU: an SM holds four blocks (128 registers a thread).
+constexpr int64_t kFusedResident = 152 * kFusedPerSm;
 
 template <typename T, typename WT, int L, bool FP4, bool GEN>
 cudaError_t fused_launch(FusedArgs& a, const RopeTurns& turns, cudaStream_t s) {
-  constexpr int row_bytes = FusedSmem<T, L>::D * static_cast<int>(sizeof(T));
-  const int rows = a.hq + 2 * a.hk;
-  const int item_bytes = a.tokens * rows * row_bytes >= 152 * 4 * 2 * int64_t(kItemBytesMany)
-                             ? kItemBytesMany
-                             : kItemBytesFew;
-  a.items = static_cast<int>((static_cast<int64_t>(rows) * row_bytes + item_bytes - 1) / item_bytes);
-  a.chunk = (rows + a.items - 1) / a.items;
-  // whole passes of the four warps, where that does not outgrow the stage
-  constexpr int pass_rows = kFusedWarps * (kWarp / L);
-  const int even = (a.chunk + pass_rows - 1) / pass_rows * pass_rows;
-  if (a.items > 1 && even * row_bytes <= item_bytes) a.chunk = even;
-  a.items = (rows + a.chunk - 1) / a.chunk;
-  a.stage_bytes = (static_cast<unsigned>(a.chunk * row_bytes) + 127u) & ~127u;
-  const size_t smem = FusedSmem<T, L>::bytes(a.stage_bytes);
+  constexpr int GW = kWarp / L;
+  constexpr int smem = FusedSmem<T, L>::kBytes;
   auto kernel = qk_cache_kernel<T, WT, L, FP4, GEN>;
-  static std::atomic<uint64_t> cache[64];
-  int64_t resident = 0;
-  const cudaError_t e = fused_resident(kernel, smem, cache, &resident);
-  if (e != cudaSuccess) return e;
-  const int64_t total = a.tokens * a.items;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(total < resident ? total : resident)),
+  static_assert(smem <= 48 * 1024, "no opt-in to more shared memory is needed");
+  // Whole tokens from four rounds of every warp on; below that they are cut.
+  const int rows = a.hq + 2 * a.hk;
+  const int passes = (rows + GW - 1) / GW;
+  constexpr int64_t warps = kFusedResident * kFusedWarps;
+  int64_t items = (4 * warps + a.tokens - 1) / a.tokens;
+  items = items < passes ? items : passes;
+  const int per = static_cast<int>((passes + items - 1) / items);  // passes of an item
+  a.chunk = per * GW;
+  a.items = (passes + per - 1) / per;
+  const int64_t blocks = (a.tokens * a.items + kFusedWarps - 1) / kFusedWarps;
+  return launch_pdl(kernel,
+                    dim3(static_cast<unsigned>(blocks < kFusedResident ? blocks : kFusedResident)),
                     dim3(kFusedThreads), smem, s, a, turns);
 }
 
@@ -491,8 +464,6 @@ cudaError_t launch_qk_norm_rope_cache(const KvCacheArgs& c, void* q_out, const v
   a.rot_vec = static_cast<int>(rotary_dim / n);
   a.interleaved = interleaved;
   a.mrope = mrope;
-  cudaError_t e = status_word(&a.status);
-  if (e != cudaSuccess) return e;
   const int lanes = static_cast<int>(c.head_dim / (2 * n));
   if (is_bf16)
     return w_is_bf16 ? fused_w<__nv_bfloat16, __nv_bfloat16>(a, c.fp4, lanes, turns, stream)

@@ -63,6 +63,14 @@ __device__ __forceinline__ void fp8_codes(const float (&x)[N], float inv, uint32
            e4m3x2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16;
 }
 
+// The same of values that have been multiplied already.
+template <int N>
+__device__ __forceinline__ void fp8_codes_scaled(const float (&x)[N], uint32_t (&c)[N / 4]) {
+#pragma unroll
+  for (int j = 0; j < N / 4; j++)
+    c[j] = e4m3x2(x[4 * j], x[4 * j + 1]) | e4m3x2(x[4 * j + 2], x[4 * j + 3]) << 16;
+}
+
 // The e8m0 byte s + 127 of a normal a > 0: a = 1.m * 2^e gives s = e - 2 up to
 // 1.m = 1.5 (a / 2^s = 6) and e - 1 above it.
 __device__ __forceinline__ uint32_t mx_scale_byte(float a) {
