@@ -9,7 +9,7 @@
 //
 // Read: a block first resolves the slots of a few output rows (a binary search
 // for the sequence, a page-table lookup) into shared memory, then streams
-// their codes, eight a lane, and writes widened rows.
+// their codes, sixteen a thread, and writes widened rows.
 #include "quant.cuh"
 
 namespace nr {
@@ -17,23 +17,6 @@ namespace {
 
 constexpr int kCacheThreads = 128;
 constexpr int kUnit = 8;  // values a lane handles at a time
-
-template <typename T>
-struct Unit;
-template <>
-struct Unit<__nv_bfloat16> {
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&f)[kUnit]) {
-    st_stream(p, Vec<__nv_bfloat16>::pack(f));
-  }
-};
-template <>
-struct Unit<float> {
-  __device__ __forceinline__ static void store(float* p, const float (&f)[kUnit]) {
-    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
-    st_stream(p, Vec<float>::pack(a));
-    st_stream(p + 4, Vec<float>::pack(b));
-  }
-};
 
 struct WriteArgs {
   const void* src[2];   // k, v
@@ -54,7 +37,10 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = ld_stream(p); }
+  template <bool WIDE>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = ld_stream(p);
+  }
   // Of the packed pairs, sign bits cleared: two values an instruction.
   __device__ __forceinline__ float top() const {
     const uint32_t m = max2(max2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
@@ -75,9 +61,14 @@ template <>
 struct Raw<float> {
   uint4 v, w;
   __device__ __forceinline__ void zero() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+  template <bool WIDE>
   __device__ __forceinline__ void load(const float* p) {
-    v = ld_stream(p);
-    w = ld_stream(p + 4);
+    if (WIDE) {
+      ld_stream32(p, v, w);
+    } else {
+      v = ld_stream(p);
+      w = ld_stream(p + 4);
+    }
   }
   __device__ __forceinline__ float top() const {
     float f[kUnit];
@@ -97,7 +88,8 @@ struct Raw<float> {
 // l + L, ...  blockIdx.y: 0 K, 1 V.  Few lanes and several units a lane: what a
 // row costs once (its slot, its scale's division, the butterfly) is shared by
 // more values.  At [16381, 8, 128] bf16 -> fp8: 16 lanes with one unit 33 us.
-template <typename T, bool FP4, int L, int NV>
+// WIDE: f32 rows are 32-byte aligned, a unit is one access.
+template <typename T, bool FP4, int L, int NV, bool WIDE>
 __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs a) {
   constexpr int GW = kWarp / L;
   pdl_enter();
@@ -124,7 +116,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs
                  tok * (is_v ? a.stride[1] : a.stride[0]) + head * dim;
 #pragma unroll
     for (int j = 0; j < NV; j++)
-      if (l + j * L < a.units) x[j].load(p + (l + j * L) * kUnit);
+      if (l + j * L < a.units) x[j].template load<WIDE>(p + (l + j * L) * kUnit);
   }
   float top[NV], row_top = 0.0f;
 #pragma unroll
@@ -170,11 +162,17 @@ __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs
   }
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 template <typename T, bool FP4, int L, int NV>
 cudaError_t write_l(const WriteArgs& a, cudaStream_t s) {
   constexpr unsigned rows = kCacheThreads / L;
-  return launch_pdl(kv_write_kernel<T, FP4, L, NV>, dim3((a.rows + rows - 1) / rows, 2),
-                    dim3(kCacheThreads), 0, s, a);
+  const dim3 grid((a.rows + rows - 1) / rows, 2);
+  if constexpr (sizeof(T) == 4) {
+    if (aligned32(a.src[0]) && aligned32(a.src[1]) && a.stride[0] % 8 == 0 && a.stride[1] % 8 == 0)
+      return launch_pdl(kv_write_kernel<T, FP4, L, NV, true>, grid, dim3(kCacheThreads), 0, s, a);
+  }
+  return launch_pdl(kv_write_kernel<T, FP4, L, NV, false>, grid, dim3(kCacheThreads), 0, s, a);
 }
 
 template <typename T, bool FP4>
@@ -192,7 +190,9 @@ cudaError_t write_t(const WriteArgs& a, cudaStream_t s) {
 // Read
 // ---------------------------------------------------------------------------
 constexpr int kReadThreads = 256;
-constexpr int kReadMaxRows = 64;  // output rows a block resolves
+constexpr int kReadMaxRows = 64;   // output rows a block resolves
+constexpr int kReadUnit = 16;      // codes a thread widens at a time
+constexpr int kReadSeqs = 1024;    // cu_seqlens entries searched in shared memory
 
 struct ReadArgs {
   void* out[2];
@@ -203,23 +203,23 @@ struct ReadArgs {
   int64_t width;
   int64_t blocks;
   int seqs;
-  int64_t rows;      // rows of the outputs
-  int block_rows;    // output rows of a thread block
-  FastDiv row_units; // heads * head_dim / 8
-  FastDiv head_units;
+  int64_t rows;        // rows of the outputs
+  int block_rows;      // output rows of a thread block
+  FastDiv row_units;   // heads * head_dim / 16
+  FastDiv head_units;  // head_dim / 16
 };
 
 // The slot of output row r: -1 for a row of no sequence (left as it is), -2
 // for one whose page is missing (read as zeros).
-__device__ __forceinline__ int64_t slot_of(const ReadArgs& a, int64_t r) {
-  if (r >= a.rows || r < a.cu[0] || r >= a.cu[a.seqs]) return -1;
+__device__ __forceinline__ int64_t slot_of(const ReadArgs& a, const int32_t* cu, int64_t r) {
+  if (r >= a.rows || r < cu[0] || r >= cu[a.seqs]) return -1;
   int lo = 0, hi = a.seqs;  // cu[lo] <= r < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (a.cu[mid] <= r) lo = mid;
+    if (cu[mid] <= r) lo = mid;
     else hi = mid;
   }
-  const int64_t t = r - a.cu[lo];
+  const int64_t t = r - cu[lo];
   const int64_t page = a.geo.block_of(t);
   if (page >= a.width) return -2;
   const int64_t block = a.table[lo * a.width + page];
@@ -227,14 +227,54 @@ __device__ __forceinline__ int64_t slot_of(const ReadArgs& a, int64_t r) {
   return block * a.geo.block_size + (t - page * a.geo.block_size);
 }
 
-template <typename T, bool FP4>
+// 16 values to an output row; WIDE: 32-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ void put16(__nv_bfloat16* p, const float (&f)[16]) {
+  uint4 v[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) x[e] = f[8 * h + e];
+    v[h] = Vec<__nv_bfloat16>::pack(x);
+  }
+  if (WIDE) {
+    st_stream32(p, v[0], v[1]);
+  } else {
+    st_stream(p, v[0]);
+    st_stream(p + 8, v[1]);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void put16(float* p, const float (&f)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const float x[4] = {f[8 * h], f[8 * h + 1], f[8 * h + 2], f[8 * h + 3]};
+    const float y[4] = {f[8 * h + 4], f[8 * h + 5], f[8 * h + 6], f[8 * h + 7]};
+    if (WIDE) {
+      st_stream32(p + 8 * h, Vec<float>::pack(x), Vec<float>::pack(y));
+    } else {
+      st_stream(p + 8 * h, Vec<float>::pack(x));
+      st_stream(p + 8 * h + 4, Vec<float>::pack(y));
+    }
+  }
+}
+
+template <typename T, bool FP4, bool WIDE>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
   __shared__ int64_t code_at[kReadMaxRows];  // byte offsets, or -1 / -2
   __shared__ int64_t scale_at[kReadMaxRows];
+  __shared__ int32_t cu_sm[kReadSeqs + 1];
   pdl_enter();
+  // One load a thread instead of a chain of them in the search.
+  const bool few = a.seqs <= kReadSeqs;
+  if (few) {
+    for (int i = threadIdx.x; i <= a.seqs; i += kReadThreads) cu_sm[i] = __ldg(a.cu + i);
+    __syncthreads();
+  }
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.block_rows;
   if (threadIdx.x < a.block_rows) {
-    const int64_t slot = slot_of(a, row0 + threadIdx.x);
+    const int64_t slot = slot_of(a, few ? cu_sm : a.cu, row0 + threadIdx.x);
     int64_t c = slot, s = slot;
     if (slot >= 0) {
       const int64_t block = a.geo.block_of(slot);
@@ -248,31 +288,33 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
   __syncthreads();
   const bool is_v = blockIdx.y != 0;
   T* out = static_cast<T*>(is_v ? a.out[1] : a.out[0]) +
-           row0 * static_cast<int64_t>(a.row_units.div) * kUnit;
+           row0 * static_cast<int64_t>(a.row_units.div) * kReadUnit;
   const CacheSide side = is_v ? a.side[1] : a.side[0];
   const uint32_t n = static_cast<uint32_t>(a.block_rows) * a.row_units.div;
   constexpr int U = 4;
   for (uint32_t base = threadIdx.x; base < n; base += U * kReadThreads) {
-    uint2 codes[U];
+    uint4 codes[U];
     float scale[U];
     int64_t where[U];
 #pragma unroll
     for (int j = 0; j < U; j++) {
       const uint32_t i = base + j * kReadThreads;
       where[j] = -1;
-      codes[j] = make_uint2(0u, 0u);
+      codes[j] = make_uint4(0u, 0u, 0u, 0u);
       scale[j] = 0.0f;
       if (i >= n) continue;
       const uint32_t r = a.row_units.quot(i), u = i - r * a.row_units.div;
       where[j] = code_at[r];
       if (where[j] < 0) continue;
       if (FP4) {
-        codes[j].x = __ldg(reinterpret_cast<const uint32_t*>(side.codes + where[j]) + u);
-        const uint32_t byte = __ldg(side.scales + scale_at[r] + u / 4);
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(side.codes + where[j]) + u);
+        codes[j].x = c.x;
+        codes[j].y = c.y;
+        const uint32_t byte = __ldg(side.scales + scale_at[r] + u / 2);
         // 2^(byte - 127); bytes 0 and 255 (2^-127, NaN) as the format has them
         scale[j] = byte == 0 ? 0x1p-127f : __uint_as_float(byte == 255 ? 0x7FC00000u : byte << 23);
       } else {
-        codes[j] = __ldg(reinterpret_cast<const uint2*>(side.codes + where[j]) + u);
+        codes[j] = ld_stream(reinterpret_cast<const uint4*>(side.codes + where[j]) + u);
         scale[j] = __ldg(reinterpret_cast<const float*>(side.scales + scale_at[r]) +
                          a.head_units.quot(u));
       }
@@ -280,36 +322,37 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
 #pragma unroll
     for (int j = 0; j < U; j++) {
       if (where[j] == -1) continue;
-      float f[kUnit];
+      float f[kReadUnit];
+      const uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
 #pragma unroll
-      for (int h = 0; h < kUnit / 2; h++) {
-        float2 v;
-        if (FP4) {
-          const __half2_raw p = __nv_cvt_fp4x2_to_halfraw2(
-              static_cast<__nv_fp4x2_storage_t>(codes[j].x >> (8 * h)), __NV_E2M1);
-          v = __half22float2(__half2(p));
-        } else {
-          const uint32_t w = h < 2 ? codes[j].x : codes[j].y;
-          const __half2_raw p = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>(w >> (16 * (h % 2))), __NV_E4M3);
-          v = __half22float2(__half2(p));
-        }
+      for (int h = 0; h < kReadUnit / 2; h++) {
+        __half2_raw p;
+        if (FP4)
+          p = __nv_cvt_fp4x2_to_halfraw2(
+              static_cast<__nv_fp4x2_storage_t>(w[h / 4] >> (8 * (h % 4))), __NV_E2M1);
+        else
+          p = __nv_cvt_fp8x2_to_halfraw2(
+              static_cast<__nv_fp8x2_storage_t>(w[h / 2] >> (16 * (h % 2))), __NV_E4M3);
+        const float2 v = __half22float2(__half2(p));
         f[2 * h] = v.x * scale[j];
         f[2 * h + 1] = v.y * scale[j];
       }
-      Unit<T>::store(out + static_cast<int64_t>(base + j * kReadThreads) * kUnit, f);
+      put16<WIDE>(out + static_cast<int64_t>(base + j * kReadThreads) * kReadUnit, f);
     }
   }
 }
 
 template <typename T, bool FP4>
 cudaError_t read_t(ReadArgs& a, cudaStream_t s) {
-  // About eight units a thread, so that resolving a slot is shared by many.
-  int64_t rows = 8 * kReadThreads / static_cast<int64_t>(a.row_units.div);
+  // About four units a thread, so that resolving a slot is shared by many.
+  int64_t rows = 4 * kReadThreads / static_cast<int64_t>(a.row_units.div);
   rows = rows < 1 ? 1 : rows > kReadMaxRows ? kReadMaxRows : rows;
   a.block_rows = static_cast<int>(rows);
-  const unsigned blocks = static_cast<unsigned>((a.rows + rows - 1) / rows);
-  return launch_pdl(kv_read_kernel<T, FP4>, dim3(blocks, 2), dim3(kReadThreads), 0, s, a);
+  const dim3 grid(static_cast<unsigned>((a.rows + rows - 1) / rows), 2);
+  // rows are multiples of 32 bytes, so the bases decide
+  auto kernel = aligned32(a.out[0]) && aligned32(a.out[1]) ? kv_read_kernel<T, FP4, true>
+                                                           : kv_read_kernel<T, FP4, false>;
+  return launch_pdl(kernel, grid, dim3(kReadThreads), 0, s, a);
 }
 
 }  // namespace
@@ -344,8 +387,8 @@ cudaError_t launch_kv_read(const KvCacheArgs& c, void* k_out, void* v_out, const
              static_cast<int>(seqs),
              rows,
              0,
-             FastDiv(static_cast<uint32_t>(c.heads * c.head_dim / kUnit)),
-             FastDiv(static_cast<uint32_t>(c.head_dim / kUnit))};
+             FastDiv(static_cast<uint32_t>(c.heads * c.head_dim / kReadUnit)),
+             FastDiv(static_cast<uint32_t>(c.head_dim / kReadUnit))};
   if (is_bf16)
     return c.fp4 ? read_t<__nv_bfloat16, true>(a, stream) : read_t<__nv_bfloat16, false>(a, stream);
   return c.fp4 ? read_t<float, true>(a, stream) : read_t<float, false>(a, stream);
