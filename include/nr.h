@@ -359,10 +359,11 @@ nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, c
                                  nr_dtype dtype, void* workspace, int64_t workspace_bytes,
                                  cudaStream_t stream);
 
-/* Workspace bytes of either direction, into *bytes.  Errors: NR_ERR_NULL and the
- * size errors of nr_group_norm. */
+/* Workspace bytes of nr_group_norm (backward 0) or nr_group_norm_backward (1),
+ * into *bytes; 0: the workspace may be NULL.  Errors: NR_ERR_NULL, NR_ERR_VALUE
+ * and the size errors of nr_group_norm. */
 nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channels,
-                                  int64_t groups, nr_dtype dtype, int64_t* bytes);
+                                  int64_t groups, int backward, nr_dtype dtype, int64_t* bytes);
 
 /*
  * LayerNorm (no affine) fused with adaLN modulation.

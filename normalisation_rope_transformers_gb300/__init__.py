@@ -106,7 +106,8 @@ lib.nr_group_norm.restype = _int
 lib.nr_group_norm_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64,
                                        _i64, _i64, _i64, _int, _int, _vp, _i64, _vp]
 lib.nr_group_norm_backward.restype = _int
-lib.nr_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.POINTER(_i64)]
+lib.nr_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, _int,
+                                        ctypes.POINTER(_i64)]
 lib.nr_group_norm_workspace.restype = _int
 lib.nr_device_status.argtypes = [_vp]
 lib.nr_device_status.restype = _int
@@ -566,9 +567,10 @@ def _activation(name):
     raise ValueError("activation must be None or 'silu', got %r" % (name,))
 
 
-def _group_norm_workspace(samples, space, channels, groups, code):
+def _group_norm_workspace(samples, space, channels, groups, backward, code):
     n = ctypes.c_int64()
-    _check(lib.nr_group_norm_workspace(samples, space, channels, groups, code, ctypes.byref(n)))
+    _check(lib.nr_group_norm_workspace(samples, space, channels, groups, backward, code,
+                                       ctypes.byref(n)))
     return n.value
 
 
@@ -613,21 +615,21 @@ def group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, s
         _cuda(x, w, b, out)
         code = _dtype_code(x)
         known = _remember(key, (wcode, (samples, space, channels, groups, float(eps), act, code),
-                                _group_norm_workspace(samples, space, channels, groups, code),
+                                _group_norm_workspace(samples, space, channels, groups, 0, code),
                                 x.device))
     wcode, sizes, need, device = known
     if out is None:
         out = torch.empty_like(x)
-    samples, groups = sizes[0], sizes[3]
+    shape = (sizes[0], sizes[3])
     # with no elements nothing is written
     held = torch.empty if sizes[1] else torch.zeros
-    both = held((2, samples, groups), dtype=torch.float32, device=device)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    mean = both.data_ptr()
-    _launch(device.index, lib.nr_group_norm, out.data_ptr(), mean, mean + 4 * samples * groups,
+    mean = held(shape, dtype=torch.float32, device=device)
+    rstd = held(shape, dtype=torch.float32, device=device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _launch(device.index, lib.nr_group_norm, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
             x.data_ptr(), None if w is None else w.data_ptr(), None if b is None else b.data_ptr(),
-            wcode, *sizes, workspace.data_ptr(), need)
-    return (out, *both.unbind(0)) if stats else out
+            wcode, *sizes, None if workspace is None else workspace.data_ptr(), need)
+    return (out, mean, rstd) if stats else out
 
 
 def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=None):
@@ -651,7 +653,7 @@ def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=N
         _cuda(x, dy, mean, rstd, w, b, dx)
         code = _dtype_code(x)
         known = _remember(key, (wcode, (samples, space, channels, groups, act, code),
-                                _group_norm_workspace(samples, space, channels, groups, code),
+                                _group_norm_workspace(samples, space, channels, groups, 1, code),
                                 x.device))
     wcode, sizes, need, device = known
     if dx is None:

@@ -47,6 +47,16 @@ struct GnBlock {
   static constexpr int kMostSmem = kRing * kStepBytes > kScratch ? kRing * kStepBytes : kScratch;
 };
 
+// What a block of the one-launch forward kernel holds: rows of a thread, groups.
+template <typename T>
+struct GnSmall {
+  using B = GnBlock<T, false>;
+  static constexpr int kRows = 20;
+  static constexpr int kGroups = 64;
+  static constexpr int kSlot = B::kThreads * static_cast<int>(sizeof(uint4));
+  static constexpr int smem(int rows) { return B::kScratch + rows * kSlot; }
+};
+
 // How a call is laid out.  Block (sample, chunk, tile) has the tile's columns of
 // every chunks-th step of step_rows rows of its sample, so that at any time the
 // blocks read one window of the tensor.
@@ -114,6 +124,41 @@ GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t gro
   g.last_chunk = static_cast<int>((g.steps - 1) % g.chunks);
   g.missing = static_cast<int>(g.steps * g.step_rows - space);
   return g;
+}
+
+// The layout of the one-launch forward kernel: tiles of whole groups, one chunk.
+// False where a sample's rows do not fit.
+template <typename T>
+bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups,
+                       GnGeom* out) {
+  using B = GnBlock<T, false>;
+  // the fewest groups that make whole vectors, and sectors of 32 bytes if they can
+  const int64_t cpg = channels / groups;
+  int64_t tile_groups = 1;
+  while (tile_groups * cpg % B::N != 0) tile_groups *= 2;
+  const int64_t sector = 32 / static_cast<int64_t>(sizeof(T));
+  while (tile_groups * cpg < sector && groups % (2 * tile_groups) == 0) tile_groups *= 2;
+  const int64_t cols = tile_groups * cpg / B::N;
+  if (cols > B::kThreads || tile_groups > GnSmall<T>::kGroups) return false;
+  const int64_t lanes = B::kThreads / cols, rows = (space + lanes - 1) / lanes;
+  if (rows > GnSmall<T>::kRows || samples * (groups / tile_groups) > INT32_MAX) return false;
+  GnGeom& g = *out;
+  g.samples = samples;
+  g.space = space;
+  g.steps = 1;
+  g.channels = static_cast<int>(channels);
+  g.groups = static_cast<int>(groups);
+  g.cpg = static_cast<int>(cpg);
+  g.cols = static_cast<int>(channels / B::N);
+  g.tile_cols = static_cast<int>(cols);
+  g.tiles = static_cast<int>(groups / tile_groups);
+  g.lanes = static_cast<int>(lanes);
+  g.unroll = static_cast<int>(rows);
+  g.step_rows = g.lanes * g.unroll;
+  g.chunks = g.chunk_steps = 1;
+  g.more_steps = g.last_chunk = 0;
+  g.missing = static_cast<int>(g.step_rows - space);
+  return true;
 }
 
 // Global scratch: partial results of the blocks.  A group that lies in two tiles
@@ -334,55 +379,54 @@ struct GnSubs {
 // channel's values minus the first of them that it sees, so a channel far from
 // zero cancels nothing and one outlier spoils no other thread's sums; parts are
 // joined by their means and counts (the update of Chan, Golub and LeVeque).
+
+// Sums of one thread's rows.
 template <typename T>
-__global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
-    gn_stats_kernel(const GnArgs a, const GnGeom g) {
-  using B = GnBlock<T, false>;
-  constexpr int N = B::N, P = N / 2, R = B::kRows;
-  extern __shared__ __align__(16) unsigned char smem[];
-  float2* sm = reinterpret_cast<float2*>(smem);  // after the walk: [lane][channel] mean, M2
-  pdl_enter();
-  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
-  const int width = g.tile_cols * N;
-  const GnLaneRows rows(g, at.chunk);
-  F2 minus[P], s1[P], s2[P];  // minus the first value of each channel
+struct GnSums {
+  static constexpr int P = Vec<T>::N / 2;
+  F2 minus[P], s1[P], s2[P];  // minus the first value of each channel; sums of d and d^2
+  bool begun;
+  __device__ __forceinline__ GnSums() : begun(false) {
 #pragma unroll
-  for (int i = 0; i < P; i++) minus[i] = s1[i] = s2[i] = f2(0.0f, 0.0f);
-  if (at.active) {
-    const void* const src[1] = {a.x};
-    bool begun = false;
-    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][1]) {
-      if (!begun && n > 0) {
-        Pairs<T>::unpack(v[0][0], minus);
-#pragma unroll
-        for (int i = 0; i < P; i++) minus[i] = mul2(minus[i], f2(-1.0f, -1.0f));
-        begun = true;
-      }
-#pragma unroll
-      for (int u = 0; u < R; u++)
-        if (u < n) {
-          F2 f[P];
-          Pairs<T>::unpack(v[u][0], f);
-#pragma unroll
-          for (int i = 0; i < P; i++) {
-            const F2 d = add2(f[i], minus[i]);
-            s1[i] = add2(s1[i], d);
-            s2[i] = fma2(d, d, s2[i]);
-          }
-        }
-    });
+    for (int i = 0; i < P; i++) minus[i] = s1[i] = s2[i] = f2(0.0f, 0.0f);
   }
-  __syncthreads();  // the rings are done with
+  __device__ __forceinline__ void begin(const uint4& v) {
+    Pairs<T>::unpack(v, minus);
+#pragma unroll
+    for (int i = 0; i < P; i++) minus[i] = mul2(minus[i], f2(-1.0f, -1.0f));
+    begun = true;
+  }
+  __device__ __forceinline__ void add(const uint4& v) {
+    F2 f[P];
+    Pairs<T>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      const F2 d = add2(f[i], minus[i]);
+      s1[i] = add2(s1[i], d);
+      s2[i] = fma2(d, d, s2[i]);
+    }
+  }
+};
+
+// Joins a block's threads: use(group, mean, M2) is called by one lane for each of
+// the tile's groups, over its channels in the tile.  `rows` are the lanes' rows,
+// `total_rows` their sum; sm holds threads * N values.
+template <typename T, typename Use>
+__device__ __forceinline__ void gn_join_lanes(const GnGeom& g, const GnPlace& at,
+                                              const GnSums<T>& sums, const GnLaneRows& rows,
+                                              float total_rows, float2* sm, Use use) {
+  using B = GnBlock<T, false>;
+  const int width = g.tile_cols * B::N;
   if (at.active) {
     const float count = static_cast<float>(rows.of(at.lane, at.lane + 1));
     const float inv = count > 0.0f ? 1.0f / count : 0.0f;
     float2* o = sm + at.lane * width + (at.channel - at.c0);
 #pragma unroll
-    for (int i = 0; i < P; i++) {
+    for (int i = 0; i < GnSums<T>::P; i++) {
       float m0, m1, a0, a1, b0, b1;
-      split(minus[i], m0, m1);
-      split(s1[i], a0, a1);
-      split(s2[i], b0, b1);
+      split(sums.minus[i], m0, m1);
+      split(sums.s1[i], a0, a1);
+      split(sums.s2[i], b0, b1);
       o[2 * i] = make_float2(fmaf(a0, inv, -m0), fmaf(-a0 * inv, a0, b0));
       o[2 * i + 1] = make_float2(fmaf(a1, inv, -m1), fmaf(-a1 * inv, a1, b1));
     }
@@ -416,12 +460,12 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     const int ca = max(at.c0, grp * g.cpg), cn = min(at.c1, (grp + 1) * g.cpg) - ca;
     // element i: sub i / cn, channel i % cn; a lane's elements are 32 apart
     const int ds = kWarp / cn, dc = kWarp % cn;
-    auto each = [&](auto use) {
+    auto each = [&](auto take) {
       int s = lane32 / cn, c = lane32 % cn;
       while (s < sub.subs) {
         const int l0 = s * sub.per;
         const float k = static_cast<float>(rows.of(l0, min(l0 + sub.per, g.lanes)));
-        use(k, sm[l0 * width + ca - at.c0 + c]);
+        take(k, sm[l0 * width + ca - at.c0 + c]);
         s += ds;
         c += dc;
         if (c >= cn) c -= cn, s++;
@@ -429,17 +473,46 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     };
     float sum = 0.0f, m2 = 0.0f;
     each([&](float k, const float2& v) { sum = fmaf(k, v.x, sum); });
-    const float total = static_cast<float>(g.rows_of(at.chunk)) * static_cast<float>(cn);
-    const float mean = __fdiv_rn(group_sum<kWarp>(sum), total);
+    const float mean =
+        __fdiv_rn(group_sum<kWarp>(sum), total_rows * static_cast<float>(cn));
     each([&](float k, const float2& v) {
       const float d = v.x - mean;
       if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
     });
     m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0)
-      a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
-          make_float2(mean, m2);
+    if (lane32 == 0) use(grp, mean, m2);
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
+    gn_stats_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, false>;
+  constexpr int R = B::kRows;
+  extern __shared__ __align__(16) unsigned char smem[];
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  GnSums<T> sums;
+  if (at.active) {
+    const void* const src[1] = {a.x};
+    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][1]) {
+      if (!sums.begun && n > 0) sums.begin(v[0][0]);
+#pragma unroll
+      for (int u = 0; u < R; u++)
+        if (u < n) sums.add(v[u][0]);
+    });
+  }
+  __syncthreads();  // the rings are done with
+  gn_join_lanes<T>(g, at, sums, GnLaneRows(g, at.chunk), static_cast<float>(g.rows_of(at.chunk)),
+                   reinterpret_cast<float2*>(smem), [&](int grp, float mean, float m2) {
+    a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
+        make_float2(mean, m2);
+  });
+}
+
+__device__ __forceinline__ float gn_rstd(float m2, float total, float eps) {
+  m2 = m2 < 0.0f ? 0.0f : m2;  // rounding may leave a constant group just below zero
+  return 1.0f / sqrtf(__fdiv_rn(m2, total) + eps);
 }
 
 // Joins the parts of one group of the sample into mean and rstd (a warp's work).
@@ -487,24 +560,56 @@ __device__ __forceinline__ float2 gn_join(const GnArgs& a, const GnGeom& g, int6
     const float d = v.x - mean;
     m2 += fmaf(count * d, d, v.y);
   }
-  m2 = group_sum<kWarp>(m2);
-  m2 = m2 < 0.0f ? 0.0f : m2;  // rounding may leave a constant group just below zero
-  return make_float2(mean, 1.0f / sqrtf(__fdiv_rn(m2, total) + a.eps));
+  return make_float2(mean, gn_rstd(group_sum<kWarp>(m2), total, a.eps));
 }
+
+// This thread's channels of the output: y = act((x - mean) * sc + sh).
+template <typename T, bool SILU>
+struct GnOut {
+  static constexpr int N = Vec<T>::N, P = N / 2;
+  F2 mu[P], sc[P], sh[P];  // minus the mean, rstd * w, b
+  // `stats`: mean and rstd of the tile's groups.
+  __device__ __forceinline__ GnOut(const GnArgs& a, const GnGeom& g, const GnPlace& at,
+                                   const float2* stats) {
+    float fm[N], fa[N], fb[N];
+    gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
+    gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
+    int grp[N];
+    gn_groups_of<N>(at.channel, g.cpg, grp);
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+      const float2 v = stats[grp[e] - at.g0];
+      fm[e] = -v.x;
+      fa[e] *= v.y;
+    }
+    to_pairs<P>(fm, mu);
+    to_pairs<P>(fa, sc);
+    to_pairs<P>(fb, sh);
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
+    F2 f[P];
+    Pairs<T>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      f[i] = fma2(add2(f[i], mu[i]), sc[i], sh[i]);
+      if (SILU) f[i] = mul2(f[i], gn_sigmoid2<T>(f[i]));
+    }
+    return Pairs<T>::pack(f);
+  }
+};
 
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     gn_apply_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, false>;
-  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  constexpr int R = B::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: mean, rstd of the groups
   pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
-  const int width = g.tile_cols * N;
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
-    const float2 v = gn_join(a, g, at.sample, grp, width);
+    const float2 v = gn_join(a, g, at.sample, grp, g.tile_cols * B::N);
     if (lane32 == 0) {
       sm[grp - at.g0] = v;
       if (at.chunk == 0 && grp * g.cpg >= at.c0) {  // one block of the sample writes a group's
@@ -514,23 +619,10 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     }
   }
   __syncthreads();
-  F2 mu[P], sc[P], sh[P];  // minus the mean, rstd * w, b
-  if (at.active) {
-    float fm[N], fa[N], fb[N];
-    gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
-    gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
-    int grp[N];
-    gn_groups_of<N>(at.channel, g.cpg, grp);
-#pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float2 v = sm[grp[e] - at.g0];
-      fm[e] = -v.x;
-      fa[e] *= v.y;
-    }
-    to_pairs<P>(fm, mu);
-    to_pairs<P>(fa, sc);
-    to_pairs<P>(fb, sh);
-  }
+  // (an inactive thread's column may lie past the tile: it takes the first one)
+  GnPlace mine = at;
+  if (!at.active) mine.channel = at.c0;
+  const GnOut<T, SILU> value(a, g, mine, sm);
   __syncthreads();  // the rings take the place of sm
   if (!at.active) return;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
@@ -539,17 +631,47 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     uint4* o = static_cast<uint4*>(a.out) + off;
 #pragma unroll
     for (int u = 0; u < R; u++, o += row_step)
-      if (u < n) {
-        F2 f[P];
-        Pairs<T>::unpack(v[u][0], f);
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-          f[i] = fma2(add2(f[i], mu[i]), sc[i], sh[i]);
-          if (SILU) f[i] = mul2(f[i], gn_sigmoid2<T>(f[i]));
-        }
-        st_stream(o, Pairs<T>::pack(f));
-      }
+      if (u < n) st_stream(o, value(v[u][0]));
   });
+}
+
+// Both passes in one launch, for samples so small that a block holds all rows of
+// a few groups in shared memory: block (sample, tile), a tile being whole groups
+// and one chunk.  Two launches take [2, 256, 1280] bf16 in 11 us.
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
+    gn_small_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, false>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float2* sm = reinterpret_cast<float2*>(smem);
+  unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
+  constexpr int kSlot = GnSmall<T>::kSlot;
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  const GnLaneRows rows(g, 0);
+  const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
+  const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
+  const int n = at.active ? rows.of(at.lane, at.lane + 1) : 0;
+  const uint4* p = static_cast<const uint4*>(a.x) + base;
+  for (int i = 0; i < n; i++) cp_async16(smem_addr(held + i * kSlot), p + i * row_step);
+  cp_async_commit();
+  cp_async_wait<0>();  // a thread reads back only what it copied
+  GnSums<T> sums;
+  if (n > 0) sums.begin(lds128(held));
+  for (int i = 0; i < n; i++) sums.add(lds128(held + i * kSlot));
+  __shared__ float2 stats[GnSmall<T>::kGroups];
+  const float total = static_cast<float>(g.space);
+  gn_join_lanes<T>(g, at, sums, rows, total, sm, [&](int grp, float mean, float m2) {
+    const float rstd = gn_rstd(m2, total * static_cast<float>(g.cpg), a.eps);
+    stats[grp - at.g0] = make_float2(mean, rstd);
+    a.mean[at.sample * g.groups + grp] = mean;
+    a.rstd[at.sample * g.groups + grp] = rstd;
+  });
+  __syncthreads();
+  if (!at.active) return;
+  const GnOut<T, SILU> value(a, g, at, stats);
+  uint4* o = static_cast<uint4*>(a.out) + base;
+  for (int i = 0; i < n; i++) st_stream(o + i * row_step, value(lds128(held + i * kSlot)));
 }
 
 // ---------------------------------------------------------------------------
@@ -766,37 +888,41 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   });
 }
 
-// Raises the shared-memory limit of two kernels, once a device.
-template <typename K1, typename K2>
-cudaError_t gn_raise(K1 k1, K2 k2, int bytes, std::atomic<int>* done) {
+// Raises the shared-memory limit of kernels, once a device.
+template <typename... Kernels>
+cudaError_t gn_raise(std::atomic<int>* done, int bytes, Kernels... kernels) {
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (done[device].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done[device].store(1, std::memory_order_release);
-  return e;
+  for (auto kernel : {kernels...}) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  done[device].store(1, std::memory_order_release);
+  return cudaSuccess;
 }
 
 template <typename T, bool BACK, bool SILU>
 cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   using B = GnBlock<T, BACK>;
+  static std::atomic<int> done[64];
   void (*stats)(const GnArgs, const GnGeom);
   void (*apply)(const GnArgs, const GnGeom);
+  cudaError_t e;
   if constexpr (BACK) {
     stats = gn_grad_stats_kernel<T, SILU>;
     apply = gn_grad_apply_kernel<T, SILU>;
+    e = gn_raise(done, B::kMostSmem, stats, apply);
   } else {
     stats = gn_stats_kernel<T>;
     apply = gn_apply_kernel<T, SILU>;
+    constexpr int small = GnSmall<T>::smem(GnSmall<T>::kRows);
+    e = gn_raise(done, B::kMostSmem > small ? B::kMostSmem : small, stats, apply,
+                 gn_small_kernel<T, SILU>);
   }
-  static std::atomic<int> done[64];
-  cudaError_t e = gn_raise(stats, apply, B::kMostSmem, done);
   if (e != cudaSuccess) return e;
-  const GnGeom g = gn_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups);
   GnArgs a;
   a.out = in.out;
   a.x = in.x;
@@ -807,6 +933,13 @@ cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   a.dw = in.dw;
   a.db = in.db;
   a.eps = in.eps;
+  GnGeom g;
+  if constexpr (!BACK) {
+    if (gn_small_geometry<T>(in.samples, in.space, in.channels, in.groups, &g))
+      return launch_pdl(gn_small_kernel<T, SILU>, dim3(static_cast<unsigned>(in.samples * g.tiles)),
+                        dim3(B::kThreads), GnSmall<T>::smem(g.unroll), s, a, g);
+  }
+  g = gn_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups);
   a.scratch.parts = static_cast<float2*>(in.workspace);
   a.scratch.sums = a.scratch.parts + g.samples * g.chunks * (g.groups + g.tiles);
   // the ring's used part, or what joining needs
@@ -824,36 +957,28 @@ cudaError_t gn_launch_act(const GroupNormArgs& in, cudaStream_t s) {
   return in.silu ? gn_launch<T, BACK, true>(in, s) : gn_launch<T, BACK, false>(in, s);
 }
 
+// Bytes of scratch, and blocks of a launch.
 template <typename T>
-int64_t gn_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups) {
-  const int64_t f =
-      gn_scratch_bytes<T, false>(gn_geometry<T, false>(samples, space, channels, groups));
-  const int64_t b =
-      gn_scratch_bytes<T, true>(gn_geometry<T, true>(samples, space, channels, groups));
-  return f > b ? f : b;
-}
-
-template <typename T>
-int64_t gn_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups) {
-  const GnGeom f = gn_geometry<T, false>(samples, space, channels, groups);
-  const GnGeom b = gn_geometry<T, true>(samples, space, channels, groups);
-  const int64_t most = static_cast<int64_t>(f.chunks) * f.tiles;
-  const int64_t more = static_cast<int64_t>(b.chunks) * b.tiles;
-  return samples * (most > more ? most : more);
+int64_t gn_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups, int backward,
+                     int64_t* blocks) {
+  GnGeom g;
+  if (!backward && gn_small_geometry<T>(samples, space, channels, groups, &g)) {
+    *blocks = samples * g.tiles;
+    return 0;
+  }
+  g = backward ? gn_geometry<T, true>(samples, space, channels, groups)
+               : gn_geometry<T, false>(samples, space, channels, groups);
+  *blocks = samples * g.chunks * g.tiles;
+  return backward ? gn_scratch_bytes<T, true>(g) : gn_scratch_bytes<T, false>(g);
 }
 
 }  // namespace
 
 int64_t group_norm_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups,
-                             int is_bf16) {
-  return is_bf16 ? gn_workspace<__nv_bfloat16>(samples, space, channels, groups)
-                 : gn_workspace<float>(samples, space, channels, groups);
-}
-
-int64_t group_norm_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups,
-                          int is_bf16) {
-  return is_bf16 ? gn_blocks<__nv_bfloat16>(samples, space, channels, groups)
-                 : gn_blocks<float>(samples, space, channels, groups);
+                             int backward, int is_bf16, int64_t* blocks) {
+  return is_bf16
+             ? gn_workspace<__nv_bfloat16>(samples, space, channels, groups, backward, blocks)
+             : gn_workspace<float>(samples, space, channels, groups, backward, blocks);
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, int is_bf16, cudaStream_t stream) {

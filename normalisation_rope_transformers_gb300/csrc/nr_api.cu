@@ -685,8 +685,9 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
 
 namespace {
 
+// Sizes, and the workspace bytes that they need.
 nr_status check_group_norm_sizes(const char* fn, int64_t samples, int64_t space, int64_t channels,
-                                 int64_t groups, nr_dtype dtype) {
+                                 int64_t groups, int backward, nr_dtype dtype, int64_t* need) {
   if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
   if (samples < 0 || space < 0 || channels <= 0 || groups <= 0)
     return fail(NR_ERR_SHAPE, "%s: need samples, space >= 0 and channels, groups > 0", fn);
@@ -702,29 +703,32 @@ nr_status check_group_norm_sizes(const char* fn, int64_t samples, int64_t space,
   if (samples > INT32_MAX || space > INT64_MAX / 16 / channels ||
       (samples > 0 && space * channels > INT64_MAX / 16 / samples))
     return fail(NR_ERR_SHAPE, "%s: samples, space or channels too large", fn);
-  if (samples > 0 && space > 0 &&
-      nr::group_norm_blocks(samples, space, channels, groups, dtype == NR_BF16) > INT32_MAX)
-    return fail(NR_ERR_SHAPE, "%s: too many samples for one launch", fn);
+  *need = 0;
+  if (samples > 0 && space > 0) {
+    int64_t blocks = 0;
+    *need = nr::group_norm_workspace(samples, space, channels, groups, backward,
+                                     dtype == NR_BF16, &blocks);
+    if (blocks > INT32_MAX)
+      return fail(NR_ERR_SHAPE, "%s: too many samples for one launch", fn);
+  }
   return NR_OK;
 }
 
 // What both directions share.
 nr_status check_group_norm(const char* fn, const nr::GroupNormArgs& a, nr_dtype w_dtype,
-                           nr_activation act, nr_dtype dtype, int64_t workspace_bytes) {
+                           nr_activation act, int64_t need, int64_t workspace_bytes) {
   if (!valid_dtype(w_dtype))
     return fail(NR_ERR_DTYPE, "%s: unknown weight dtype %d", fn, (int)w_dtype);
   if (act != NR_ACT_NONE && act != NR_ACT_SILU)
     return fail(NR_ERR_VALUE, "%s: unknown activation %d", fn, (int)act);
   if (a.samples == 0 || a.space == 0) return NR_OK;
-  if (!a.out || !a.x || !a.mean || !a.rstd || !a.workspace)
+  if (!a.out || !a.x || !a.mean || !a.rstd || (need > 0 && !a.workspace))
     return fail(NR_ERR_NULL, "%s: the tensors, mean, rstd and workspace must be non-NULL", fn);
   if ((a.w == nullptr) != (a.b == nullptr))
     return fail(NR_ERR_NULL, "%s: w and b are given together or not at all", fn);
   if (!aligned16(a.out) || !aligned16(a.x) || !aligned16(a.w) || !aligned16(a.b) ||
       !aligned16(a.workspace) || misaligned(a.mean, 4) || misaligned(a.rstd, 4))
     return fail(NR_ERR_ALIGN, "%s: pointers must be 16-byte aligned (mean and rstd 4-byte)", fn);
-  const int64_t need = nr::group_norm_workspace(a.samples, a.space, a.channels, a.groups,
-                                                dtype == NR_BF16);
   if (workspace_bytes < need)
     return fail(NR_ERR_SHAPE, "%s: the workspace has %lld bytes, %lld are needed", fn,
                 (long long)workspace_bytes, (long long)need);
@@ -742,14 +746,16 @@ bool any_overlap(const Region* all, int n, const Region& one) {
 extern "C" {
 
 nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channels,
-                                  int64_t groups, nr_dtype dtype, int64_t* bytes) {
+                                  int64_t groups, int backward, nr_dtype dtype, int64_t* bytes) {
   const char* fn = "nr_group_norm_workspace";
-  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+  if (backward != 0 && backward != 1)
+    return fail(NR_ERR_VALUE, "%s: backward must be 0 or 1", fn);
+  int64_t need = 0;
+  if (const nr_status s =
+          check_group_norm_sizes(fn, samples, space, channels, groups, backward, dtype, &need))
     return s;
   if (bytes == nullptr) return fail(NR_ERR_NULL, "%s: bytes must be non-NULL", fn);
-  *bytes = samples == 0 || space == 0
-               ? 0
-               : nr::group_norm_workspace(samples, space, channels, groups, dtype == NR_BF16);
+  *bytes = need;
   return ok();
 }
 
@@ -760,7 +766,9 @@ nr_status nr_group_norm(void* out, float* mean, float* rstd, const void* x, cons
                         cudaStream_t stream) {
   CallRange range("nr_group_norm");
   const char* fn = "nr_group_norm";
-  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+  int64_t need = 0;
+  if (const nr_status s =
+          check_group_norm_sizes(fn, samples, space, channels, groups, 0, dtype, &need))
     return s;
   if (!eps_ok(eps)) return fail(NR_ERR_VALUE, "%s: eps must be finite and >= 0", fn);
   nr::GroupNormArgs a = {};
@@ -778,13 +786,13 @@ nr_status nr_group_norm(void* out, float* mean, float* rstd, const void* x, cons
   a.eps = eps;
   a.silu = act == NR_ACT_SILU;
   a.workspace = workspace;
-  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, dtype, workspace_bytes)) return s;
+  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, need, workspace_bytes)) return s;
   if (samples == 0 || space == 0) return ok();
   const int64_t bytes = samples * space * channels * elem_size(dtype);
   const int64_t wb = channels * elem_size(w_dtype), stats = samples * groups * 4;
   const Region ro = dense(out, bytes), rx = dense(x, bytes);
   const Region rm = dense(mean, stats), rr = dense(rstd, stats);
-  const Region ws = dense(workspace, workspace_bytes);
+  const Region ws = dense(workspace, workspace ? workspace_bytes : 0);
   const Region ins[] = {rx, dense(w, w ? wb : 0), dense(b, b ? wb : 0)};
   if ((out != x && overlap(ro, rx)) || any_overlap(ins + 1, 2, ro) || any_overlap(ins, 3, rm) ||
       any_overlap(ins, 3, rr) || any_overlap(ins, 3, ws) || overlap(ro, rm) || overlap(ro, rr) ||
@@ -801,7 +809,9 @@ nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, c
                                  cudaStream_t stream) {
   CallRange range("nr_group_norm_backward");
   const char* fn = "nr_group_norm_backward";
-  if (const nr_status s = check_group_norm_sizes(fn, samples, space, channels, groups, dtype))
+  int64_t need = 0;
+  if (const nr_status s =
+          check_group_norm_sizes(fn, samples, space, channels, groups, 1, dtype, &need))
     return s;
   nr::GroupNormArgs a = {};
   a.out = dx;
@@ -820,7 +830,7 @@ nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, c
   a.groups = groups;
   a.silu = act == NR_ACT_SILU;
   a.workspace = workspace;
-  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, dtype, workspace_bytes)) return s;
+  if (const nr_status s = check_group_norm(fn, a, w_dtype, act, need, workspace_bytes)) return s;
   if (samples == 0 || space == 0) return ok();
   if (!dy) return fail(NR_ERR_NULL, "%s: dy must be non-NULL", fn);
   if ((dw != nullptr) != (w != nullptr) || (db != nullptr) != (w != nullptr))
@@ -830,7 +840,7 @@ nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, c
   const int64_t bytes = samples * space * channels * elem_size(dtype);
   const int64_t wb = channels * elem_size(w_dtype), stats = samples * groups * 4;
   const Region ro = dense(dx, bytes), rw = dense(dw, dw ? wb : 0), rb = dense(db, db ? wb : 0);
-  const Region ws = dense(workspace, workspace_bytes);
+  const Region ws = dense(workspace, workspace ? workspace_bytes : 0);
   const Region ins[] = {dense(dy, bytes),        dense(x, bytes),          dense(mean, stats),
                         dense(rstd, stats),      dense(w, w ? wb : 0),     dense(b, b ? wb : 0)};
   if ((dx != dy && overlap(ro, ins[0])) || (dx != x && overlap(ro, ins[1])) ||

@@ -180,11 +180,9 @@ struct GroupNormArgs {
   void* workspace;
 };
 
-// Bytes that either direction needs, and blocks of its largest launch.
+// Workspace bytes of one direction, and the blocks of its largest launch.
 int64_t group_norm_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups,
-                             int is_bf16);
-int64_t group_norm_blocks(int64_t samples, int64_t space, int64_t channels, int64_t groups,
-                          int is_bf16);
+                             int backward, int is_bf16, int64_t* blocks);
 cudaError_t launch_group_norm(const GroupNormArgs& args, int is_bf16, cudaStream_t stream);
 cudaError_t launch_group_norm_backward(const GroupNormArgs& args, int is_bf16,
                                        cudaStream_t stream);
