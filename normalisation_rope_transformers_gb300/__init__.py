@@ -663,10 +663,10 @@ def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=N
         held = torch.empty_like if sizes[0] and sizes[1] else torch.zeros_like
         dw, db = held(w), held(b)
         pw, pb, pdw, pdb = w.data_ptr(), b.data_ptr(), dw.data_ptr(), db.data_ptr()
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _launch(device.index, lib.nr_group_norm_backward, dx.data_ptr(), pdw, pdb, dy.data_ptr(),
             x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), pw, pb, wcode, *sizes,
-            workspace.data_ptr(), need)
+            None if workspace is None else workspace.data_ptr(), need)
     return dx, dw, db
 
 

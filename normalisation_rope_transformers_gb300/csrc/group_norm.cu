@@ -47,14 +47,14 @@ struct GnBlock {
   static constexpr int kMostSmem = kRing * kStepBytes > kScratch ? kRing * kStepBytes : kScratch;
 };
 
-// What a block of the one-launch forward kernel holds: rows of a thread, groups.
-template <typename T>
+// What a block of the one-launch kernels holds: rows of a thread, groups.
+template <typename T, bool BACK>
 struct GnSmall {
-  using B = GnBlock<T, false>;
-  static constexpr int kRows = 20;
+  using B = GnBlock<T, BACK>;
+  static constexpr int kRows = BACK ? 12 : 20;
   static constexpr int kGroups = 64;
   static constexpr int kSlot = B::kThreads * static_cast<int>(sizeof(uint4));
-  static constexpr int smem(int rows) { return B::kScratch + rows * kSlot; }
+  static constexpr int smem(int rows) { return B::kScratch + rows * B::kTensors * kSlot; }
 };
 
 // How a call is laid out.  Block (sample, chunk, tile) has the tile's columns of
@@ -126,12 +126,13 @@ GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t gro
   return g;
 }
 
-// The layout of the one-launch forward kernel: tiles of whole groups, one chunk.
-// False where a sample's rows do not fit.
-template <typename T>
+// The layout of the one-launch kernels: tiles of whole groups, one chunk.  False
+// where a sample's rows do not fit.
+template <typename T, bool BACK>
 bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                        GnGeom* out) {
-  using B = GnBlock<T, false>;
+  using B = GnBlock<T, BACK>;
+  using S = GnSmall<T, BACK>;
   // the fewest groups that make whole vectors, and sectors of 32 bytes if they can
   const int64_t cpg = channels / groups;
   int64_t tile_groups = 1;
@@ -139,9 +140,9 @@ bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t
   const int64_t sector = 32 / static_cast<int64_t>(sizeof(T));
   while (tile_groups * cpg < sector && groups % (2 * tile_groups) == 0) tile_groups *= 2;
   const int64_t cols = tile_groups * cpg / B::N;
-  if (cols > B::kThreads || tile_groups > GnSmall<T>::kGroups) return false;
+  if (cols > B::kThreads || tile_groups > S::kGroups) return false;
   const int64_t lanes = B::kThreads / cols, rows = (space + lanes - 1) / lanes;
-  if (rows > GnSmall<T>::kRows || samples * (groups / tile_groups) > INT32_MAX) return false;
+  if (rows > S::kRows || samples * (groups / tile_groups) > INT32_MAX) return false;
   GnGeom& g = *out;
   g.samples = samples;
   g.space = space;
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   extern __shared__ __align__(16) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
-  constexpr int kSlot = GnSmall<T>::kSlot;
+  constexpr int kSlot = GnSmall<T, false>::kSlot;
   pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
   const GnLaneRows rows(g, 0);
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   GnSums<T> sums;
   if (n > 0) sums.begin(lds128(held));
   for (int i = 0; i < n; i++) sums.add(lds128(held + i * kSlot));
-  __shared__ float2 stats[GnSmall<T>::kGroups];
+  __shared__ float2 stats[GnSmall<T, false>::kGroups];
   const float total = static_cast<float>(g.space);
   gn_join_lanes<T>(g, at, sums, rows, total, sm, [&](int grp, float mean, float m2) {
     const float rstd = gn_rstd(m2, total * static_cast<float>(g.cpg), a.eps);
@@ -707,49 +708,45 @@ __device__ __forceinline__ void gn_grad_params(const GnArgs& a, const GnGeom& g,
   to_pairs<P>(fb, sh);
 }
 
-// Sums of a chunk: S1 and S2 per channel, and weighted by w per group.
+// Sums of one thread's rows, of dz and of dz (x - mean).
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
-    gn_grad_stats_kernel(const GnArgs a, const GnGeom g) {
-  using B = GnBlock<T, true>;
-  constexpr int N = B::N, P = N / 2, R = B::kRows;
-  extern __shared__ __align__(16) unsigned char smem[];
-  float2* sm = reinterpret_cast<float2*>(smem);  // after the walk: [lane][channel of the tile]
-  pdl_enter();
-  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
-  const int width = g.tile_cols * N;
-  F2 s1[P], s2[P];  // sums of dz and of dz (x - mean)
+struct GnGradSums {
+  static constexpr int N = Vec<T>::N, P = N / 2;
+  F2 mu[P], sc[P], sh[P], s1[P], s2[P];
+  __device__ __forceinline__ GnGradSums() {
 #pragma unroll
-  for (int i = 0; i < P; i++) s1[i] = s2[i] = f2(0.0f, 0.0f);
-  if (at.active) {
-    F2 mu[P], sc[P], sh[P];
-    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
-    const void* const src[2] = {a.x, a.dy};
-    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][2]) {
-#pragma unroll
-      for (int u = 0; u < R; u++)
-        if (u < n) {
-          F2 f[P], d[P];
-          Pairs<T>::unpack(v[u][0], f);
-          Pairs<T>::unpack(v[u][1], d);
-#pragma unroll
-          for (int i = 0; i < P; i++) {
-            const F2 c = add2(f[i], mu[i]);
-            const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
-            s1[i] = add2(s1[i], dz);
-            s2[i] = fma2(dz, c, s2[i]);
-          }
-        }
-    });
+    for (int i = 0; i < P; i++) mu[i] = sc[i] = sh[i] = s1[i] = s2[i] = f2(0.0f, 0.0f);
   }
-  __syncthreads();  // the rings are done with
+  __device__ __forceinline__ void add(const uint4& x, const uint4& dy) {
+    F2 f[P], d[P];
+    Pairs<T>::unpack(x, f);
+    Pairs<T>::unpack(dy, d);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      const F2 c = add2(f[i], mu[i]);
+      const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
+      s1[i] = add2(s1[i], dz);
+      s2[i] = fma2(dz, c, s2[i]);
+    }
+  }
+};
+
+// Joins a block's threads: of(channel, S1, S2) is called for each of the tile's
+// channels, then use(group, sum of w S1, sum of w S2) for each of its groups,
+// over its channels in the tile, each once.
+template <typename T, bool SILU, typename Of, typename Use>
+__device__ __forceinline__ void gn_grad_join(const GnArgs& a, const GnGeom& g, const GnPlace& at,
+                                             const GnGradSums<T, SILU>& sums, float2* sm, Of of,
+                                             Use use) {
+  using B = GnBlock<T, true>;
+  const int width = g.tile_cols * B::N;
   if (at.active) {
     float2* o = sm + at.lane * width + (at.channel - at.c0);
 #pragma unroll
-    for (int i = 0; i < P; i++) {
+    for (int i = 0; i < B::N / 2; i++) {
       float a0, a1, b0, b1;
-      split(s1[i], a0, a1);
-      split(s2[i], b0, b1);
+      split(sums.s1[i], a0, a1);
+      split(sums.s2[i], b0, b1);
       o[2 * i] = make_float2(a0, b0);
       o[2 * i + 1] = make_float2(a1, b1);
     }
@@ -769,7 +766,6 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     sm[l0 * width + c] = v;
   }
   __syncthreads();
-  const int64_t block = at.sample * g.chunks + at.chunk;
   for (int c = threadIdx.x; c < tile_channels; c += B::kThreads) {
     float2 v = sm[c];
     for (int s = 1; s < sub.subs; s++) {
@@ -777,7 +773,7 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
       v.y += sm[s * sub.per * width + c].y;
     }
     v.y *= a.rstd[at.sample * g.groups + (at.c0 + c) / g.cpg];
-    if (a.dw != nullptr) a.scratch.sums[block * g.channels + at.c0 + c] = v;
+    of(at.c0 + c, v.x, v.y);
     float w[1];
     gn_params<1>(a.prm.w, a.prm.is_bf16, at.c0 + c, 1.0f, w);
     sm[c] = make_float2(w[0] * v.x, w[0] * v.y);
@@ -793,17 +789,111 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     }
     m1 = group_sum<kWarp>(m1);
     m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0)
-      a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
-          make_float2(m1, m2);
+    if (lane32 == 0) use(grp, m1, m2);
   }
 }
 
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
+    gn_grad_stats_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, true>;
+  constexpr int R = B::kRows;
+  extern __shared__ __align__(16) unsigned char smem[];
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  GnGradSums<T, SILU> sums;
+  if (at.active) {
+    gn_grad_params<B::N, B::N / 2>(a, g, at, sums.mu, sums.sc, sums.sh);
+    const void* const src[2] = {a.x, a.dy};
+    gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][2]) {
+#pragma unroll
+      for (int u = 0; u < R; u++)
+        if (u < n) sums.add(v[u][0], v[u][1]);
+    });
+  }
+  __syncthreads();  // the rings are done with
+  const int64_t block = at.sample * g.chunks + at.chunk;
+  gn_grad_join<T, SILU>(
+      a, g, at, sums, reinterpret_cast<float2*>(smem),
+      [&](int c, float s1, float s2) {
+        if (a.dw != nullptr) a.scratch.sums[block * g.channels + c] = make_float2(s1, s2);
+      },
+      [&](int grp, float m1, float m2) {
+        a.scratch.parts[(at.sample * (g.groups + g.tiles) + grp + at.tile) * g.chunks + at.chunk] =
+            make_float2(m1, m2);
+      });
+}
+
+// dw and db of one channel.
+__device__ __forceinline__ void gn_put_grads(const GnArgs& a, int64_t c, float s1, float s2) {
+  if (a.prm.is_bf16) {
+    static_cast<__nv_bfloat16*>(a.db)[c] = __float2bfloat16_rn(s1);
+    static_cast<__nv_bfloat16*>(a.dw)[c] = __float2bfloat16_rn(s2);
+  } else {
+    static_cast<float*>(a.db)[c] = s1;
+    static_cast<float*>(a.dw)[c] = s2;
+  }
+}
+
+// dw and db of channels first, first + step, ... from `rows` rows of channel sums: a
+// warp's work.
+__device__ __forceinline__ void gn_sum_grads(const GnArgs& a, const GnGeom& g, int64_t rows,
+                                             int64_t first, int64_t step) {
+  const int lane32 = threadIdx.x % kWarp;
+  for (int64_t c = first; c < g.channels; c += step) {
+    float t1 = 0.0f, t2 = 0.0f;
+    for (int64_t i = lane32; i < rows; i += kWarp) {
+      const float2 v = __ldg(a.scratch.sums + i * g.channels + c);
+      t1 += v.x;
+      t2 += v.y;
+    }
+    t1 = group_sum<kWarp>(t1);
+    t2 = group_sum<kWarp>(t2);
+    if (lane32 == 0) gn_put_grads(a, c, t1, t2);
+  }
+}
+
+// This thread's channels of the input's gradient:
+// dx = a dz - k1 - (x - mean) k2 with a = rstd w, k1 = rstd m1, k2 = rstd^2 m2.
+template <typename T, bool SILU>
+struct GnGradOut {
+  static constexpr int N = Vec<T>::N, P = N / 2;
+  F2 mu[P], sc[P], sh[P], k1[P], k2[P];  // k1 and k2 negated
+  // `means`: m1 and m2 of the tile's groups.
+  __device__ __forceinline__ GnGradOut(const GnArgs& a, const GnGeom& g, const GnPlace& at,
+                                       const float2* means) {
+    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
+    float f1[N], f3[N];
+    int grp[N];
+    gn_groups_of<N>(at.channel, g.cpg, grp);
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+      const float rs = a.rstd[at.sample * g.groups + grp[e]];
+      f1[e] = -rs * means[grp[e] - at.g0].x;
+      f3[e] = -rs * rs * means[grp[e] - at.g0].y;
+    }
+    to_pairs<P>(f1, k1);
+    to_pairs<P>(f3, k2);
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& x, const uint4& dy) const {
+    F2 f[P], d[P];
+    Pairs<T>::unpack(x, f);
+    Pairs<T>::unpack(dy, d);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      const F2 c = add2(f[i], mu[i]);
+      const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
+      f[i] = fma2(sc[i], dz, fma2(c, k2[i], k1[i]));
+    }
+    return Pairs<T>::pack(f);
+  }
+};
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     gn_grad_apply_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, true>;
-  constexpr int N = B::N, P = N / 2, R = B::kRows;
+  constexpr int N = B::N, R = B::kRows;
   constexpr int kWarps = B::kThreads / kWarp;
   extern __shared__ __align__(16) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: the groups' means
@@ -828,43 +918,13 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   }
   // dw and db: the blocks share the channels, one warp each.
   if (a.dw != nullptr)
-    for (int64_t c = blockIdx.x + static_cast<int64_t>(gridDim.x) * warp; c < g.channels;
-         c += static_cast<int64_t>(gridDim.x) * kWarps) {
-      float t1 = 0.0f, t2 = 0.0f;
-      for (int64_t i = lane32; i < g.samples * g.chunks; i += kWarp) {
-        const float2 v = __ldg(a.scratch.sums + i * g.channels + c);
-        t1 += v.x;
-        t2 += v.y;
-      }
-      t1 = group_sum<kWarp>(t1);
-      t2 = group_sum<kWarp>(t2);
-      if (lane32 == 0) {
-        if (a.prm.is_bf16) {
-          static_cast<__nv_bfloat16*>(a.db)[c] = __float2bfloat16_rn(t1);
-          static_cast<__nv_bfloat16*>(a.dw)[c] = __float2bfloat16_rn(t2);
-        } else {
-          static_cast<float*>(a.db)[c] = t1;
-          static_cast<float*>(a.dw)[c] = t2;
-        }
-      }
-    }
+    gn_sum_grads(a, g, g.samples * g.chunks, blockIdx.x + static_cast<int64_t>(gridDim.x) * warp,
+                 static_cast<int64_t>(gridDim.x) * kWarps);
   __syncthreads();
-  // dx = a dz - k1 - (x - mean) k2: a = rstd w, k1 = rstd m1, k2 = rstd^2 m2
-  F2 mu[P], sc[P], sh[P], k1[P], k2[P];  // k1 and k2 negated
-  if (at.active) {
-    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
-    float f1[N], f3[N];
-    int grp[N];
-    gn_groups_of<N>(at.channel, g.cpg, grp);
-#pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float rs = a.rstd[at.sample * g.groups + grp[e]];
-      f1[e] = -rs * sm[grp[e] - at.g0].x;
-      f3[e] = -rs * rs * sm[grp[e] - at.g0].y;
-    }
-    to_pairs<P>(f1, k1);
-    to_pairs<P>(f3, k2);
-  }
+  // (an inactive thread's column may lie past the tile: it takes the first one)
+  GnPlace mine = at;
+  if (!at.active) mine.channel = at.c0;
+  const GnGradOut<T, SILU> value(a, g, mine, sm);
   __syncthreads();  // the rings take the place of sm
   if (!at.active) return;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
@@ -873,19 +933,65 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     uint4* o = static_cast<uint4*>(a.out) + off;
 #pragma unroll
     for (int u = 0; u < R; u++, o += row_step)
-      if (u < n) {
-        F2 f[P], d[P];
-        Pairs<T>::unpack(v[u][0], f);
-        Pairs<T>::unpack(v[u][1], d);
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-          const F2 c = add2(f[i], mu[i]);
-          const F2 dz = gn_dz<T, SILU>(d[i], fma2(c, sc[i], sh[i]));
-          f[i] = fma2(sc[i], dz, fma2(c, k2[i], k1[i]));
-        }
-        st_stream(o, Pairs<T>::pack(f));
-      }
+      if (u < n) st_stream(o, value(v[u][0], v[u][1]));
   });
+}
+
+// Both passes in one launch, as gn_small_kernel.  The channel sums of one sample
+// are dw and db; those of several are added by gn_grad_sum_kernel.
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
+    gn_grad_small_kernel(const GnArgs a, const GnGeom g) {
+  using B = GnBlock<T, true>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float2 means[GnSmall<T, true>::kGroups];
+  unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
+  constexpr int kSlot = GnSmall<T, true>::kSlot;
+  pdl_enter();
+  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
+  const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
+  const int n = at.active ? GnLaneRows(g, 0).of(at.lane, at.lane + 1) : 0;
+  const uint4* px = static_cast<const uint4*>(a.x) + base;
+  const uint4* pd = static_cast<const uint4*>(a.dy) + base;
+  for (int i = 0; i < n; i++) {
+    cp_async16(smem_addr(held + 2 * i * kSlot), px + i * row_step);
+    cp_async16(smem_addr(held + (2 * i + 1) * kSlot), pd + i * row_step);
+  }
+  cp_async_commit();
+  GnGradSums<T, SILU> sums;
+  if (n > 0) gn_grad_params<B::N, B::N / 2>(a, g, at, sums.mu, sums.sc, sums.sh);
+  cp_async_wait<0>();  // a thread reads back only what it copied
+  for (int i = 0; i < n; i++)
+    sums.add(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot));
+  const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
+  gn_grad_join<T, SILU>(
+      a, g, at, sums, reinterpret_cast<float2*>(smem),
+      [&](int c, float s1, float s2) {
+        if (a.dw == nullptr) return;
+        if (g.samples == 1)
+          gn_put_grads(a, c, s1, s2);
+        else
+          a.scratch.sums[at.sample * g.channels + c] = make_float2(s1, s2);
+      },
+      [&](int grp, float m1, float m2) { means[grp - at.g0] = make_float2(m1 * inv, m2 * inv); });
+  __syncthreads();
+  if (!at.active) return;
+  const GnGradOut<T, SILU> value(a, g, at, means);
+  uint4* o = static_cast<uint4*>(a.out) + base;
+  for (int i = 0; i < n; i++)
+    st_stream(o + i * row_step,
+              value(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot)));
+}
+
+constexpr int kGnSumThreads = 256;
+
+__global__ void __launch_bounds__(kGnSumThreads)
+    gn_grad_sum_kernel(const GnArgs a, const GnGeom g) {
+  pdl_enter();
+  constexpr int kWarps = kGnSumThreads / kWarp;
+  gn_sum_grads(a, g, g.samples, static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / kWarp,
+               static_cast<int64_t>(gridDim.x) * kWarps);
 }
 
 // Raises the shared-memory limit of kernels, once a device.
@@ -910,18 +1016,21 @@ cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   static std::atomic<int> done[64];
   void (*stats)(const GnArgs, const GnGeom);
   void (*apply)(const GnArgs, const GnGeom);
-  cudaError_t e;
+  void (*small)(const GnArgs, const GnGeom);
   if constexpr (BACK) {
     stats = gn_grad_stats_kernel<T, SILU>;
     apply = gn_grad_apply_kernel<T, SILU>;
-    e = gn_raise(done, B::kMostSmem, stats, apply);
+    small = gn_grad_small_kernel<T, SILU>;
   } else {
     stats = gn_stats_kernel<T>;
     apply = gn_apply_kernel<T, SILU>;
-    constexpr int small = GnSmall<T>::smem(GnSmall<T>::kRows);
-    e = gn_raise(done, B::kMostSmem > small ? B::kMostSmem : small, stats, apply,
-                 gn_small_kernel<T, SILU>);
+    small = gn_small_kernel<T, SILU>;
   }
+  using S = GnSmall<T, BACK>;
+  constexpr int most = S::smem(S::kRows);
+  static_assert(most <= 232448 - 1024, "a block's shared memory");
+  cudaError_t e =
+      gn_raise(done, B::kMostSmem > most ? B::kMostSmem : most, stats, apply, small);
   if (e != cudaSuccess) return e;
   GnArgs a;
   a.out = in.out;
@@ -934,10 +1043,16 @@ cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   a.db = in.db;
   a.eps = in.eps;
   GnGeom g;
-  if constexpr (!BACK) {
-    if (gn_small_geometry<T>(in.samples, in.space, in.channels, in.groups, &g))
-      return launch_pdl(gn_small_kernel<T, SILU>, dim3(static_cast<unsigned>(in.samples * g.tiles)),
-                        dim3(B::kThreads), GnSmall<T>::smem(g.unroll), s, a, g);
+  if (gn_small_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups, &g)) {
+    a.scratch.sums = static_cast<float2*>(in.workspace);
+    e = launch_pdl(small, dim3(static_cast<unsigned>(in.samples * g.tiles)), dim3(B::kThreads),
+                   S::smem(g.unroll), s, a, g);
+    if (e != cudaSuccess || in.dw == nullptr || in.samples == 1) return e;
+    // a warp a channel, up to the SMs' worth of blocks
+    const int64_t blocks = (in.channels * kWarp + kGnSumThreads - 1) / kGnSumThreads;
+    return launch_pdl(gn_grad_sum_kernel,
+                      dim3(static_cast<unsigned>(blocks < 4 * kGnSms ? blocks : 4 * kGnSms)),
+                      dim3(kGnSumThreads), 0, s, a, g);
   }
   g = gn_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups);
   a.scratch.parts = static_cast<float2*>(in.workspace);
@@ -962,9 +1077,10 @@ template <typename T>
 int64_t gn_workspace(int64_t samples, int64_t space, int64_t channels, int64_t groups, int backward,
                      int64_t* blocks) {
   GnGeom g;
-  if (!backward && gn_small_geometry<T>(samples, space, channels, groups, &g)) {
+  if (backward ? gn_small_geometry<T, true>(samples, space, channels, groups, &g)
+               : gn_small_geometry<T, false>(samples, space, channels, groups, &g)) {
     *blocks = samples * g.tiles;
-    return 0;
+    return backward && samples > 1 ? samples * channels * static_cast<int64_t>(sizeof(float2)) : 0;
   }
   g = backward ? gn_geometry<T, true>(samples, space, channels, groups)
                : gn_geometry<T, false>(samples, space, channels, groups);
