@@ -5,6 +5,7 @@
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <string.h>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -245,11 +246,18 @@ nr_status check_rope(const char* fn, const nr_rope_config& rope, int64_t head_di
   return NR_OK;
 }
 
-void fill_turns(const nr_rope_config& rope, int64_t rot, bool mrope, nr::RopeTurns* out) {
+// The rotary constants of a configuration.  They depend on it alone, and a
+// program's calls mostly share one, so the last one's stay at hand (per thread):
+// 64 powers cost about 2 us of a decode call's host time.
+const nr::RopeTurns& rope_turns(const nr_rope_config& rope, int64_t rot, bool mrope) {
+  thread_local nr_rope_config had;
+  thread_local int64_t had_rot = 0;  // no rotary dimension is 0
+  thread_local nr::RopeTurns turns;
+  if (had_rot == rot && memcmp(&had, &rope, sizeof rope) == 0) return turns;
+  had_rot = 0;
   // turn_i = frac(freq_i / 2pi) * 2^64, freq_i = theta^(-2i/rot) (Llama-3
   // rescaled when asked), in double.  Positions are integers, so
   // pos * freq_i mod 2pi = pos * (freq_i mod 2pi) mod 2pi.
-  nr::RopeTurns& turns = *out;
   for (int64_t i = 0; i < nr::kMaxHalfDim; i++) {
     turns.turn[i] = 0;
     turns.axis[i] = 0;
@@ -264,6 +272,9 @@ void fill_turns(const nr_rope_config& rope, int64_t rot, bool mrope, nr::RopeTur
         scaled >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(scaled);
     turns.axis[i] = mrope ? mrope_row(i, rope) : 0;
   }
+  memcpy(&had, &rope, sizeof rope);
+  had_rot = rot;
+  return turns;
 }
 
 nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void* q, const void* k,
@@ -324,8 +335,7 @@ nr_status qk_norm_rope_impl(const char* fn, void* q_out, void* k_out, const void
       overlap(rko, rwk) || overlap(rko, rpos))
     return fail(NR_ERR_ALIAS, "%s: k_out overlaps an input", fn);
 
-  nr::RopeTurns turns;
-  fill_turns(rope, rot, mrope, &turns);
+  const nr::RopeTurns& turns = rope_turns(rope, rot, mrope);
   return from_cuda(nr::launch_qk_norm_rope(q_out, k_out, q, k, wq, wk, w_dtype == NR_BF16,
                                            positions, tokens, hq, hk, head_dim, q_tok_stride,
                                            k_tok_stride, eps, turns, gemma, rot, rope.interleaved,
@@ -638,8 +648,7 @@ nr_status nr_qk_norm_rope_cache(const nr_kv_cache* cache, void* q_out, const voi
   for (const Region& in : ins)
     if (overlap(rqo, in) || held.overlaps(in))
       return fail(NR_ERR_ALIAS, "%s: q_out or the cache overlaps an input", fn);
-  nr::RopeTurns turns;
-  fill_turns(*rope, rot, mrope, &turns);
+  const nr::RopeTurns& turns = rope_turns(*rope, rot, mrope);
   return from_cuda(nr::launch_qk_norm_rope_cache(args, q_out, q, k, v, wq, wk, w_dtype == NR_BF16,
                                                  positions, slots, tokens, hq, q_tok_stride,
                                                  k_tok_stride, v_tok_stride, eps, turns, gemma,
