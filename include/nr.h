@@ -31,7 +31,8 @@
  *     time of the host call (validation and launch), so profilers can tell
  *     which call launched which kernel.
  *   - Every pointer must be 16-byte aligned, and every row start (row stride in
- *     bytes) a multiple of 16, so that each thread moves 128-bit vectors.
+ *     bytes) a multiple of 16, so that each thread moves 128-bit vectors; index
+ *     arrays, scales and statistics need the alignment of their elements.
  *   - Work is enqueued asynchronously on `stream` (0 = the legacy default
  *     stream); the call returns once the kernel is launched.
  *   - All arithmetic is f32 (bf16 values are widened exactly); each stored
@@ -313,6 +314,8 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
                            const int32_t* cu_seqlens, int64_t seqs, int64_t rows, nr_dtype dtype,
                            cudaStream_t stream);
 
+typedef enum nr_activation { NR_ACT_NONE = 0, NR_ACT_SILU = 1 } nr_activation;
+
 /*
  * Group norm over channels-last tensors, with an optional activation.
  *
@@ -333,8 +336,6 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
  * eps finite >= 0.
  * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
  */
-typedef enum nr_activation { NR_ACT_NONE = 0, NR_ACT_SILU = 1 } nr_activation;
-
 nr_status nr_group_norm(void* out, float* mean, float* rstd, const void* x, const void* w,
                         const void* b, nr_dtype w_dtype, int64_t samples, int64_t space,
                         int64_t channels, int64_t groups, float eps, nr_activation act,

@@ -21,7 +21,7 @@ or ``__graft_entry__.build()``).
                                rows_per_sample=None, out=None)
     kv_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
     kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, rows=None,
-                  dtype=torch.bfloat16, k_out=None, v_out=None)
+                  dtype=None, k_out=None, v_out=None)
     qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_scale, v_scale,
                        ..., q_out=None)
     group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, stats=False)
@@ -489,8 +489,10 @@ def qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_sc
                        llama3=None, mrope_sections=None, mrope_interleaved=False, q_out=None):
     """qk_norm_rope_ex with K (quantised from its f32 value) and V written into
     the cache as kv_cache_write does.  Returns q_out."""
-    options = (eps, gemma, rotary_dim, interleaved, theta, llama3,
-               None if mrope_sections is None else tuple(mrope_sections), mrope_interleaved)
+    if mrope_sections is not None:
+        mrope_sections = tuple(mrope_sections)
+    options = (eps, gemma, rotary_dim, interleaved, theta, llama3, mrope_sections,
+               mrope_interleaved)
     key, known = _known("fused", options, (q, k, v, wq, wk, positions, slots, k_cache, v_cache,
                                            k_scale, v_scale, q_out))
     if known is None:
@@ -517,12 +519,13 @@ def qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_sc
 
 
 def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, rows=None,
-                  dtype=torch.bfloat16, k_out=None, v_out=None):
+                  dtype=None, k_out=None, v_out=None):
     """Reads sequences back from the cache: row cu_seqlens[s] + t of k and v
     [rows, heads, head_dim] is token t of sequence s, found through
     block_table [seqs, n] int32; cu_seqlens is [seqs + 1] int32.  Give `rows`
     (at least cu_seqlens[-1], which is not read on the host) or outputs to fill;
-    rows behind the last sequence are left as they were.  Returns (k, v)."""
+    `dtype` is float32 or bfloat16 (the outputs', else bfloat16).  Rows behind
+    the last sequence are left as they were.  Returns (k, v)."""
     key, known = _known("read", (rows, dtype), (k_cache, v_cache, k_scale, v_scale, block_table,
                                                 cu_seqlens, k_out, v_out))
     if known is None:
@@ -532,8 +535,10 @@ def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, r
         _expect(block_table, "block_table", torch.int32, block_table.shape)
         _expect(cu_seqlens, "cu_seqlens", torch.int32, (block_table.shape[0] + 1,))
         for t in (k_out, v_out):
-            if rows is None and isinstance(t, torch.Tensor) and t.dim() == 3:
-                rows, dtype = t.shape[0], t.dtype
+            if isinstance(t, torch.Tensor):
+                rows = t.shape[0] if rows is None and t.dim() == 3 else rows
+                dtype = t.dtype if dtype is None else dtype
+        dtype = torch.bfloat16 if dtype is None else dtype
         if rows is None:
             raise ValueError("kv_cache_read needs rows or outputs [rows, heads, head_dim]")
         if int(rows) < 0:
@@ -602,7 +607,8 @@ def group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, s
     axes between) with w and b [channels] (float32 or bfloat16; both or
     neither), then `activation` (None or "silu").  Returns out, or (out, mean,
     rstd) with stats=True: the [samples, groups] float32 statistics that
-    group_norm_backward takes."""
+    group_norm_backward takes.  No autograd graph is recorded: the gradient is
+    a call of its own."""
     key, known = _known("norm", (groups, eps, activation), (x, w, b, out))
     if known is None:
         samples, space, channels, wcode = _check_norm(x, w, b)

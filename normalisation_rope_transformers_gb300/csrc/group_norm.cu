@@ -13,21 +13,26 @@
 // output kernel, both bound by HBM.  The output kernel takes the rows in the
 // opposite order, so that what was read last still comes from L2.  One block
 // fills an SM; each thread copies its vectors many rows ahead into a ring of
-// its own in shared memory (cp.async), which keeps about 150 KB an SM in flight
-// without registers or barriers.
+// its own in shared memory (cp.async), which keeps 64 to 98 KB an SM in flight
+// without registers or barriers.  Samples so small that a block holds all rows
+// of a few groups take one launch.
 //
 // Any channels / groups works: a thread keeps one 128-bit column of N channels
 // and walks down the rows, sums stay per channel until the block's end, and a
 // vector may span several groups.  Every sum has a fixed order (no atomics):
 // the same inputs give the same bits.
 //
-// Tried and slower for [1, 1048576, 128] bf16: one cooperative kernel with a
-// barrier between the passes and 170 KB an SM of rows kept on chip (178 us
-// against 134 us for plain loads in two kernels and a joining one).
+// [1, 1048576, 128] bf16 with SiLU takes 136 us: the statistics 45 us (268 MB at
+// 6.0 TB/s), the output pass the rest (486 MB, some 50 MB of x coming from L2; 132 us
+// in all without the activation, so the traffic bounds it).  The gradient at
+// [2, 262144, 256] takes 205 us, 1285 MB at 6.3 TB/s.  Slower: one cooperative
+// kernel with a barrier between the passes and 170 KB an SM of rows kept on chip
+// (178 us), loads into registers and a joining kernel between the passes (144
+// us), two blocks an SM (150 us: 64 registers are too few).
 #include <atomic>
 
-#include "nr_common.cuh"
 #include "nr_internal.h"
+#include "nr_pairs.cuh"
 
 namespace nr {
 namespace {
@@ -165,9 +170,8 @@ bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t
 // Global scratch: partial results of the blocks.  A group that lies in two tiles
 // has a part in each; part (group, tile) is in row group + tile, which no other
 // part has, as the groups of a tile are never below those of the tile before.
-// The chunks of a part are side by side, so that joining them reads whole
-// sectors (every block of the output kernel does: [chunks][groups + tiles] cost
-// 4 us more with 304 chunks).
+// The chunks of a part are side by side, so that joining them (every block of
+// the output kernel does) reads whole sectors.
 struct GnScratch {
   float2* parts;  // [samples][groups + tiles][chunks]
   float2* sums;   // backward: [samples][chunks][channels]
@@ -221,12 +225,6 @@ __device__ __forceinline__ F2 gn_sigmoid2<__nv_bfloat16>(F2 z) {
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
   return f2(lo, hi);
-}
-
-template <int P>
-__device__ __forceinline__ void to_pairs(const float (&v)[2 * P], F2 (&p)[P]) {
-#pragma unroll
-  for (int i = 0; i < P; i++) p[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 // Where a block and a thread stand.

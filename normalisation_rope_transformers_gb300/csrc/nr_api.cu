@@ -86,7 +86,7 @@ bool eps_ok(float eps) { return isfinite(eps) && eps >= 0.0f; }
 
 extern "C" {
 
-int nr_version(void) { return 100; }
+int nr_version(void) { return 200; }
 
 const char* nr_last_error_message(void) { return g_message; }
 

@@ -14,8 +14,8 @@
 
 #include <cuda_fp4.h>
 
-#include "nr_common.cuh"
 #include "nr_internal.h"
+#include "nr_pairs.cuh"
 
 namespace nr {
 

@@ -97,6 +97,7 @@ SIZES = [
 @pytest.mark.parametrize("n,space,chan,groups", SIZES)
 @pytest.mark.parametrize("dtype,wdtype,act", [(bf, bf, "silu"), (bf, torch.float32, None),
                                               (torch.float32, torch.float32, "silu"),
+                                              (torch.float32, bf, "silu"),
                                               (torch.float32, None, None)])
 def test_forward(nr, n, space, chan, groups, dtype, wdtype, act):
     x, w, b = inputs(n, space, chan, dtype, wdtype, seed=chan + groups)

@@ -168,6 +168,55 @@ def test_scales_are_the_correctly_rounded_quotients(nr):
     assert np.array_equal(flat(parts[0]), want[0])
 
 
+@pytest.mark.parametrize("dtype", [bf, torch.float32])
+def test_rows_of_nan_and_infinity(nr, dtype):
+    """All NaN: the scale's floor.  fp8 codes stay NaN; 4-bit codes have no NaN and
+    become 6 of either sign.  Infinities take the largest code, others zero."""
+    x = torch.randn(3, 1, 64)
+    x[0] = float("nan")
+    x[1, 0, ::2] = float("inf")
+    x[2, 0, 33] = float("-inf")
+    k = x.to(dtype).cuda()
+    parts = make_cache("fp8", 3, 1, 1, 64)
+    nr.kv_cache_write(k, k, torch.arange(3, device="cuda"), *parts)
+    want = ref.quant_fp8(f32(k))
+    got = flat(parts[0])
+    assert np.array_equal(got[1:], want[0][1:]) and np.all((got[0] & 0x7F) == 0x7F)
+    assert np.array_equal(flat(parts[2]), want[1])
+    parts = make_cache("mxfp4", 3, 1, 1, 64)
+    nr.kv_cache_write(k, k, torch.arange(3, device="cuda"), *parts)
+    want = ref.quant_mxfp4(f32(k))
+    got = flat(parts[0])
+    assert np.array_equal(got[1:], want[0][1:]) and np.all((got[0] & 0x77) == 0x77)
+    assert np.array_equal(flat(parts[2]), want[1])
+
+
+def test_one_token_of_any_stride_and_side_streams(nr):
+    """A single token's stride says nothing; inputs made on another stream are
+    used after a wait."""
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        k = torch.randn(1, 5, 64, device="cuda").to(bf).as_strided((1, 5, 64), (3, 64, 1))
+        parts = make_cache("fp8", 1, 2, 5, 64)
+        before = [flat(p) for p in parts]
+        slots = torch.tensor([1], device="cuda")
+    torch.cuda.current_stream().wait_stream(s)
+    nr.kv_cache_write(k, k, slots, *parts)
+    check_written(parts, before, k, k, [1], "fp8")
+
+
+def test_read_takes_its_type_from_given_outputs(nr):
+    parts = make_cache("fp8", 2, 4, 1, 16)
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    out = torch.empty(8, 1, 16, device="cuda")
+    for kw in (dict(k_out=out), dict(rows=8, k_out=out), dict(rows=8, v_out=out)):
+        k, v = nr.kv_cache_read(*parts, table, cu, **kw)
+        assert k.dtype == v.dtype == torch.float32
+    k, v = nr.kv_cache_read(*parts, table, cu, 8)
+    assert k.dtype == v.dtype == bf
+
+
 def test_no_tokens(nr):
     parts = make_cache("fp8", 2, 4, 2, 64)
     before = [flat(p) for p in parts]

@@ -126,6 +126,46 @@ def test_partial_rotary_fp8(nr, rot):
     run(nr, 19, 3, 2, 128, "fp8", seed=rot, rotary_dim=rot)
 
 
+@pytest.mark.parametrize("kw", [dict(rotary_dim=64), dict(rotary_dim=64, interleaved=True),
+                                dict(rotary_dim=8, interleaved=True), dict(rotary_dim=24)])
+def test_f32_variants(nr, kw):
+    run(nr, 17, 3, 2, 128, "fp8", dtype=torch.float32, wdtype=bf, seed=6, **kw)
+
+
+def test_mrope_4bit_f32_sections_from_an_iterator(nr):
+    pos = torch.from_numpy(np.random.default_rng(7).integers(0, 8192, (3, 9)).astype(np.int32))
+    run(nr, 9, 6, 2, 128, "mxfp4", dtype=torch.float32, pos=pos, seed=8,
+        mrope_sections=(16, 24, 24), theta=1e6)
+    q, k, wq, wk, _ = (dev(t) for t in synth.qk_inputs(9, 4, 2, 128, 3, bf, torch.float32))
+    v, slots = torch.randn(9, 2, 128, device="cuda").to(bf), torch.arange(9, device="cuda")
+    a, b = make_cache("fp8", 2, 8, 2, 128), make_cache("fp8", 2, 8, 2, 128)
+    qa = nr.qk_norm_rope_cache(q, k, v, wq, wk, dev(pos), slots, *a, mrope_sections=(16, 24, 24))
+    qb = nr.qk_norm_rope_cache(q, k, v, wq, wk, dev(pos), slots, *b,
+                               mrope_sections=iter((16, 24, 24)))
+    assert torch.equal(qa, qb) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_alternating_configurations(nr):
+    """Calls that take turns with different rotary constants, as two models in one
+    process would."""
+    q, k, wq, wk, p = (dev(t) for t in synth.qk_inputs(20, 4, 2, 128, 3, bf, torch.float32,
+                                                       pos_start=900))
+    v, slots = torch.randn(20, 2, 128, device="cuda").to(bf), torch.arange(20, device="cuda")
+    kws = [dict(), dict(theta=5e5), dict(rotary_dim=64), dict(theta=5e5,
+                                                              llama3=(8.0, 1.0, 4.0, 8192.0))]
+    first = []
+    for _ in range(2):
+        for i, kw in enumerate(kws):
+            out = nr.qk_norm_rope_cache(q, k, v, wq, wk, p, slots,
+                                        *make_cache("fp8", 3, 8, 2, 128), **kw)
+            plain = nr.qk_norm_rope_ex(q, k, wq, wk, p, **kw)[0]
+            # the two kernels' f32 roundings differ by far less than a bf16 step
+            assert (out.float() - plain.float()).abs().max() <= 2.0 ** -7 * plain.float().abs().max()
+            if len(first) < len(kws):
+                first.append(out)
+            assert torch.equal(out, first[i])
+
+
 def test_bf16_weights_and_far_positions(nr):
     pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 131072, 7, 99999999], dtype=torch.int32)
     run(nr, 8, 4, 2, 128, wdtype=bf, pos=pos, seed=2)
