@@ -525,7 +525,8 @@ def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, r
     block_table [seqs, n] int32; cu_seqlens is [seqs + 1] int32.  Give `rows`
     (at least cu_seqlens[-1], which is not read on the host) or outputs to fill;
     `dtype` is float32 or bfloat16 (the outputs', else bfloat16).  Rows behind
-    the last sequence are left as they were.  Returns (k, v)."""
+    the last sequence are left as they were (in outputs made here: anything).
+    Returns (k, v)."""
     key, known = _known("read", (rows, dtype), (k_cache, v_cache, k_scale, v_scale, block_table,
                                                 cu_seqlens, k_out, v_out))
     if known is None:
@@ -603,8 +604,8 @@ def _check_norm(x, w, b):
 
 
 def group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, stats=False):
-    """Group norm of x [samples, ..., channels] (channels last, any number of
-    axes between) with w and b [channels] (float32 or bfloat16; both or
+    """Group norm of x [samples, ..., channels] (contiguous, any number of axes
+    between; a torch channels_last [N, C, H, W] is x.permute(0, 2, 3, 1)) with w and b [channels] (float32 or bfloat16; both or
     neither), then `activation` (None or "silu").  Returns out, or (out, mean,
     rstd) with stats=True: the [samples, groups] float32 statistics that
     group_norm_backward takes.  No autograd graph is recorded: the gradient is

@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   using B = GnBlock<T, false>;
   constexpr int R = B::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   GnSums<T> sums;
   if (at.active) {
     const void* const src[1] = {a.x};
@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   constexpr int R = B::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: mean, rstd of the groups
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
     const float2 v = gn_join(a, g, at.sample, grp, g.tile_cols * B::N);
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   float2* sm = reinterpret_cast<float2*>(smem);
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, false>::kSlot;
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   const GnLaneRows rows(g, 0);
   const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
@@ -797,8 +797,8 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   using B = GnBlock<T, true>;
   constexpr int R = B::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   GnGradSums<T, SILU> sums;
   if (at.active) {
     gn_grad_params<B::N, B::N / 2>(a, g, at, sums.mu, sums.sc, sums.sh);
@@ -895,8 +895,8 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   constexpr int kWarps = B::kThreads / kWarp;
   extern __shared__ __align__(16) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: the groups' means
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   const int width = g.tile_cols * N;
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
@@ -945,8 +945,8 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   __shared__ float2 means[GnSmall<T, true>::kGroups];
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, true>::kSlot;
-  pdl_enter();
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  pdl_enter();  // before any global read: the previous kernel may still run
   const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
   const int n = at.active ? GnLaneRows(g, 0).of(at.lane, at.lane + 1) : 0;

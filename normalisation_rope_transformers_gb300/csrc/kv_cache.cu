@@ -94,7 +94,6 @@ struct Raw<float> {
 template <typename T, bool FP4, int L, int NV, bool WIDE>
 __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs a) {
   constexpr int GW = kWarp / L;
-  pdl_enter();
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   const int l = lane32 % L;
   const uint32_t row =
@@ -110,8 +109,9 @@ __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs
   uint32_t head = 0;
 #pragma unroll
   for (int j = 0; j < NV; j++) x[j].zero();
+  const uint32_t tok = a.heads.quot(row < a.rows ? row : 0);
+  pdl_enter();  // before any global read: the previous kernel may still run
   if (row < a.rows) {
-    const uint32_t tok = a.heads.quot(row);
     head = row - tok * a.heads.div;
     slot = __ldg(a.slots + tok);
     const T* p = static_cast<const T*>(is_v ? a.src[1] : a.src[0]) +

@@ -166,6 +166,46 @@ def test_alternating_configurations(nr):
             assert torch.equal(out, first[i])
 
 
+def test_host_threads_on_streams_of_their_own(nr):
+    """Four host threads, each with its stream, cache and rotary configuration."""
+    import threading
+
+    kws = [dict(), dict(theta=5e5), dict(rotary_dim=64), dict(interleaved=True)]
+    q, k, wq, wk, p = (dev(t) for t in synth.qk_inputs(40, 4, 2, 128, 3, bf, torch.float32))
+    v, slots = torch.randn(40, 2, 128, device="cuda").to(bf), torch.arange(40, device="cuda")
+    x = torch.randn(1, 30000, 64, device="cuda").to(bf)
+    caches = [make_cache("fp8", 5, 8, 2, 128) for _ in kws]
+
+    def call(kw, parts):
+        out = nr.qk_norm_rope_cache(q, k, v, wq, wk, p, slots, *parts, **kw)
+        y, mean, rstd = nr.group_norm(x, 8, activation="silu", stats=True)
+        dx = nr.group_norm_backward(x, x, mean, rstd, activation="silu")[0]
+        return out, y, dx, parts[0].clone(), parts[2].clone()
+
+    want = [call(kw, parts) for kw, parts in zip(kws, caches)]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(kws), []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i] = call(kws[i], caches[i])
+            s.synchronize()
+        except Exception as e:  # reported below, in the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(kws))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
 def test_bf16_weights_and_far_positions(nr):
     pos = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 131072, 7, 99999999], dtype=torch.int32)
     run(nr, 8, 4, 2, 128, wdtype=bf, pos=pos, seed=2)
