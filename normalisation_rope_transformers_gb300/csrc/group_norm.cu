@@ -22,7 +22,7 @@
 // vector may span several groups.  Every sum has a fixed order (no atomics):
 // the same inputs give the same bits.
 //
-// [1, 1048576, 128] bf16 with SiLU takes 136 us: the statistics 45 us (268 MB at
+// [1, 1048576, 128] bf16 with SiLU takes 135 us: the statistics 45 us (268 MB at
 // 6.0 TB/s), the output pass the rest (486 MB, some 50 MB of x coming from L2; 132 us
 // in all without the activation, so the traffic bounds it).  The gradient at
 // [2, 262144, 256] takes 205 us, 1285 MB at 6.3 TB/s.  Slower: one cooperative
@@ -272,6 +272,10 @@ struct GnLaneRows {
   }
 };
 
+// (The kernels' dynamic shared memory is aligned to 128 bytes: behind 192 bytes of
+// static arrays every 512-byte access of a warp would straddle a fifth line, 2 us
+// of the 134 at [1, 1048576, 128].)
+
 // Walks this thread's rows of a chunk, from the first step to the last or
 // (REVERSE) back, copying kRing steps ahead: visit(offset, n, v) gets the n rows
 // of a step, one vector of each tensor, `offset` in vectors from the tensors'
@@ -407,6 +411,13 @@ struct GnSums {
   }
 };
 
+// Warps that share one group of `elements` values in a join: one, but where few
+// and wide groups would leave most warps idle.  [1, 436, 1824] f32 in one group:
+// 10.1 us, 13.5 us with one warp; groups of 58 to 139 values lose 0.7 us by it.
+__device__ __forceinline__ int gn_group_warps(int groups, int elements, int warps) {
+  return groups < warps && elements >= 512 ? warps / groups : 1;
+}
+
 // Joins a block's threads: use(group, mean, M2) is called by one lane for each of
 // the tile's groups, over its channels in the tile.  `rows` are the lanes' rows,
 // `total_rows` their sum; sm holds threads * N values.
@@ -453,33 +464,71 @@ __device__ __forceinline__ void gn_join_lanes(const GnGeom& g, const GnPlace& at
     col[l0 * width] = make_float2(mean, m2);
   }
   __syncthreads();
-  // The group's channels in this tile: one warp a group.
+  // A group's channels in this tile: one warp a group, or several that take a
+  // share each of the (sub, channel) elements.
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
-  for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
-    const int ca = max(at.c0, grp * g.cpg), cn = min(at.c1, (grp + 1) * g.cpg) - ca;
-    // element i: sub i / cn, channel i % cn; a lane's elements are 32 apart
+  constexpr int kWarps = B::kThreads / kWarp;
+  // Elements [from, end) of a group: sub i / cn, channel i % cn; a lane's are 32 apart.
+  auto each = [&](int ca, int cn, int from, int end, auto take) {
+    int i = from + lane32, s = i / cn, c = i - s * cn;
     const int ds = kWarp / cn, dc = kWarp % cn;
-    auto each = [&](auto take) {
-      int s = lane32 / cn, c = lane32 % cn;
-      while (s < sub.subs) {
-        const int l0 = s * sub.per;
-        const float k = static_cast<float>(rows.of(l0, min(l0 + sub.per, g.lanes)));
-        take(k, sm[l0 * width + ca - at.c0 + c]);
-        s += ds;
-        c += dc;
-        if (c >= cn) c -= cn, s++;
-      }
-    };
-    float sum = 0.0f, m2 = 0.0f;
-    each([&](float k, const float2& v) { sum = fmaf(k, v.x, sum); });
-    const float mean =
-        __fdiv_rn(group_sum<kWarp>(sum), total_rows * static_cast<float>(cn));
-    each([&](float k, const float2& v) {
+    for (; i < end; i += kWarp) {
+      const int l0 = s * sub.per;
+      const float k = static_cast<float>(rows.of(l0, min(l0 + sub.per, g.lanes)));
+      take(k, sm[l0 * width + ca - at.c0 + c]);
+      s += ds;
+      c += dc;
+      if (c >= cn) c -= cn, s++;
+    }
+  };
+  const int groups = at.g1 - at.g0 + 1;
+  const int split_by = gn_group_warps(groups, sub.subs * min(g.cpg, tile_channels), kWarps);
+  if (split_by == 1) {
+    for (int grp = at.g0 + warp; grp <= at.g1; grp += kWarps) {
+      const int ca = max(at.c0, grp * g.cpg), cn = min(at.c1, (grp + 1) * g.cpg) - ca;
+      const int n = sub.subs * cn;
+      float sum = 0.0f, m2 = 0.0f;
+      each(ca, cn, 0, n, [&](float k, const float2& v) { sum = fmaf(k, v.x, sum); });
+      const float mean = __fdiv_rn(group_sum<kWarp>(sum), total_rows * static_cast<float>(cn));
+      each(ca, cn, 0, n, [&](float k, const float2& v) {
+        const float d = v.x - mean;
+        if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
+      });
+      m2 = group_sum<kWarp>(m2);
+      if (lane32 == 0) use(grp, mean, m2);
+    }
+    return;
+  }
+  __shared__ float3 shares[kWarps];  // rows, mean, M2
+  if (warp < groups * split_by) {
+    const int grp = at.g0 + warp / split_by, part = warp % split_by;
+    const int ca = max(at.c0, grp * g.cpg), cn = min(at.c1, (grp + 1) * g.cpg) - ca;
+    const int share = (sub.subs * cn + split_by - 1) / split_by;
+    const int from = part * share, end = min(sub.subs * cn, from + share);
+    float sum = 0.0f, count = 0.0f, m2 = 0.0f;
+    each(ca, cn, from, end, [&](float k, const float2& v) {
+      sum = fmaf(k, v.x, sum);
+      count += k;
+    });
+    sum = group_sum<kWarp>(sum);
+    count = group_sum<kWarp>(count);
+    const float mean = count > 0.0f ? __fdiv_rn(sum, count) : 0.0f;
+    each(ca, cn, from, end, [&](float k, const float2& v) {
       const float d = v.x - mean;
       if (k > 0.0f) m2 += fmaf(k * d, d, v.y);
     });
     m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0) use(grp, mean, m2);
+    if (lane32 == 0) shares[warp] = make_float3(count, mean, m2);
+  }
+  __syncthreads();
+  if (warp < groups) {
+    const float3 v = lane32 < split_by ? shares[warp * split_by + lane32]
+                                       : make_float3(0.0f, 0.0f, 0.0f);
+    const float count = group_sum<kWarp>(v.x);
+    const float mean = __fdiv_rn(group_sum<kWarp>(v.x * v.y), count);
+    const float d = v.y - mean;
+    const float m2 = group_sum<kWarp>(v.x > 0.0f ? fmaf(v.x * d, d, v.z) : 0.0f);
+    if (lane32 == 0) use(at.g0 + warp, mean, m2);
   }
 }
 
@@ -488,7 +537,7 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     gn_stats_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, false>;
   constexpr int R = B::kRows;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
   GnSums<T> sums;
@@ -562,28 +611,30 @@ __device__ __forceinline__ float2 gn_join(const GnArgs& a, const GnGeom& g, int6
   return make_float2(mean, gn_rstd(group_sum<kWarp>(m2), total, a.eps));
 }
 
-// This thread's channels of the output: y = act((x - mean) * sc + sh).
+// This thread's channels of the output: y = act((x - mean) * sc + sh).  Made from
+// w and b, whose reads then overlap what comes before the statistics.
 template <typename T, bool SILU>
 struct GnOut {
   static constexpr int N = Vec<T>::N, P = N / 2;
   F2 mu[P], sc[P], sh[P];  // minus the mean, rstd * w, b
-  // `stats`: mean and rstd of the tile's groups.
-  __device__ __forceinline__ GnOut(const GnArgs& a, const GnGeom& g, const GnPlace& at,
-                                   const float2* stats) {
-    float fm[N], fa[N], fb[N];
-    gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
-    gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
-    int grp[N];
-    gn_groups_of<N>(at.channel, g.cpg, grp);
-#pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float2 v = stats[grp[e] - at.g0];
-      fm[e] = -v.x;
-      fa[e] *= v.y;
-    }
-    to_pairs<P>(fm, mu);
+  __device__ __forceinline__ GnOut(const GnArgs& a, int channel) {
+    float fa[N], fb[N];
+    gn_params<N>(a.prm.w, a.prm.is_bf16, channel, 1.0f, fa);
+    gn_params<N>(a.prm.b, a.prm.is_bf16, channel, 0.0f, fb);
     to_pairs<P>(fa, sc);
     to_pairs<P>(fb, sh);
+  }
+  // `stats`: mean and rstd of the tile's groups.
+  __device__ __forceinline__ void take(const GnGeom& g, const GnPlace& at, int channel,
+                                       const float2* stats) {
+    int grp[N];
+    gn_groups_of<N>(channel, g.cpg, grp);
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      const float2 u = stats[grp[2 * i] - at.g0], v = stats[grp[2 * i + 1] - at.g0];
+      mu[i] = f2(-u.x, -v.x);
+      sc[i] = mul2(sc[i], f2(u.y, v.y));
+    }
   }
   __device__ __forceinline__ uint4 operator()(const uint4& v) const {
     F2 f[P];
@@ -602,11 +653,14 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     gn_apply_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, false>;
   constexpr int R = B::kRows;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: mean, rstd of the groups
   const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+  // (an inactive thread's column may lie past the tile: it takes the first one)
+  const int channel = at.active ? at.channel : at.c0;
+  GnOut<T, SILU> value(a, channel);
   for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
     const float2 v = gn_join(a, g, at.sample, grp, g.tile_cols * B::N);
     if (lane32 == 0) {
@@ -618,10 +672,7 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     }
   }
   __syncthreads();
-  // (an inactive thread's column may lie past the tile: it takes the first one)
-  GnPlace mine = at;
-  if (!at.active) mine.channel = at.c0;
-  const GnOut<T, SILU> value(a, g, mine, sm);
+  value.take(g, at, channel, sm);
   __syncthreads();  // the rings take the place of sm
   if (!at.active) return;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
@@ -636,12 +687,12 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
 
 // Both passes in one launch, for samples so small that a block holds all rows of
 // a few groups in shared memory: block (sample, tile), a tile being whole groups
-// and one chunk.  Two launches take [2, 256, 1280] bf16 in 11 us.
+// and one chunk.  [2, 256, 1280] bf16: 6.2 us, 11 us in two launches.
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     gn_small_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, false>;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, false>::kSlot;
@@ -654,6 +705,8 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   const uint4* p = static_cast<const uint4*>(a.x) + base;
   for (int i = 0; i < n; i++) cp_async16(smem_addr(held + i * kSlot), p + i * row_step);
   cp_async_commit();
+  const int channel = at.active ? at.channel : at.c0;
+  GnOut<T, SILU> value(a, channel);
   cp_async_wait<0>();  // a thread reads back only what it copied
   GnSums<T> sums;
   if (n > 0) sums.begin(lds128(held));
@@ -668,7 +721,7 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   });
   __syncthreads();
   if (!at.active) return;
-  const GnOut<T, SILU> value(a, g, at, stats);
+  value.take(g, at, channel, stats);
   uint4* o = static_cast<uint4*>(a.out) + base;
   for (int i = 0; i < n; i++) st_stream(o + i * row_step, value(lds128(held + i * kSlot)));
 }
@@ -688,16 +741,17 @@ __device__ __forceinline__ F2 gn_dz(F2 dy, F2 z) {
 
 // This thread's channels: minus the mean, rstd * w, b.
 template <int N, int P>
-__device__ __forceinline__ void gn_grad_params(const GnArgs& a, const GnGeom& g, const GnPlace& at,
-                                               F2 (&mu)[P], F2 (&sc)[P], F2 (&sh)[P]) {
+__device__ __forceinline__ void gn_grad_params(const GnArgs& a, const GnGeom& g, int64_t sample,
+                                               int channel, F2 (&mu)[P], F2 (&sc)[P],
+                                               F2 (&sh)[P]) {
   float fm[N], fa[N], fb[N];
-  gn_params<N>(a.prm.w, a.prm.is_bf16, at.channel, 1.0f, fa);
-  gn_params<N>(a.prm.b, a.prm.is_bf16, at.channel, 0.0f, fb);
+  gn_params<N>(a.prm.w, a.prm.is_bf16, channel, 1.0f, fa);
+  gn_params<N>(a.prm.b, a.prm.is_bf16, channel, 0.0f, fb);
   int grp[N];
-  gn_groups_of<N>(at.channel, g.cpg, grp);
+  gn_groups_of<N>(channel, g.cpg, grp);
 #pragma unroll
   for (int e = 0; e < N; e++) {
-    const int64_t i = at.sample * g.groups + grp[e];
+    const int64_t i = sample * g.groups + grp[e];
     fm[e] = -a.mean[i];
     fa[e] *= a.rstd[i];
   }
@@ -778,16 +832,38 @@ __device__ __forceinline__ void gn_grad_join(const GnArgs& a, const GnGeom& g, c
   }
   __syncthreads();
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
-  for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
-    const int ca = max(at.c0, grp * g.cpg), cb = min(at.c1, (grp + 1) * g.cpg);
+  constexpr int kWarps = B::kThreads / kWarp;
+  const int groups = at.g1 - at.g0 + 1;
+  const int split_by = gn_group_warps(groups, min(g.cpg, tile_channels), kWarps);
+  auto sum = [&](int from, int end) {  // of channels [from, end)
     float m1 = 0.0f, m2 = 0.0f;
-    for (int c = ca + lane32; c < cb; c += kWarp) {
+    for (int c = from + lane32; c < end; c += kWarp) {
       m1 += sm[c - at.c0].x;
       m2 += sm[c - at.c0].y;
     }
-    m1 = group_sum<kWarp>(m1);
-    m2 = group_sum<kWarp>(m2);
-    if (lane32 == 0) use(grp, m1, m2);
+    return make_float2(group_sum<kWarp>(m1), group_sum<kWarp>(m2));
+  };
+  if (split_by == 1) {
+    for (int grp = at.g0 + warp; grp <= at.g1; grp += kWarps) {
+      const float2 v = sum(max(at.c0, grp * g.cpg), min(at.c1, (grp + 1) * g.cpg));
+      if (lane32 == 0) use(grp, v.x, v.y);
+    }
+    return;
+  }
+  __shared__ float2 shares[kWarps];
+  if (warp < groups * split_by) {
+    const int grp = at.g0 + warp / split_by, part = warp % split_by;
+    const int ca = max(at.c0, grp * g.cpg), cb = min(at.c1, (grp + 1) * g.cpg);
+    const int share = (cb - ca + split_by - 1) / split_by;
+    const float2 v = sum(ca + part * share, min(cb, ca + (part + 1) * share));
+    if (lane32 == 0) shares[warp] = v;
+  }
+  __syncthreads();
+  if (warp < groups) {
+    const float2 v = lane32 < split_by ? shares[warp * split_by + lane32]
+                                       : make_float2(0.0f, 0.0f);
+    const float m1 = group_sum<kWarp>(v.x), m2 = group_sum<kWarp>(v.y);
+    if (lane32 == 0) use(at.g0 + warp, m1, m2);
   }
 }
 
@@ -796,12 +872,12 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     gn_grad_stats_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, true>;
   constexpr int R = B::kRows;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
   GnGradSums<T, SILU> sums;
   if (at.active) {
-    gn_grad_params<B::N, B::N / 2>(a, g, at, sums.mu, sums.sc, sums.sh);
+    gn_grad_params<B::N, B::N / 2>(a, g, at.sample, at.channel, sums.mu, sums.sc, sums.sh);
     const void* const src[2] = {a.x, a.dy};
     gn_walk<B, false>(g, at, src, smem, [&](int64_t, int n, const uint4 (&v)[R][2]) {
 #pragma unroll
@@ -858,20 +934,18 @@ struct GnGradOut {
   static constexpr int N = Vec<T>::N, P = N / 2;
   F2 mu[P], sc[P], sh[P], k1[P], k2[P];  // k1 and k2 negated
   // `means`: m1 and m2 of the tile's groups.
-  __device__ __forceinline__ GnGradOut(const GnArgs& a, const GnGeom& g, const GnPlace& at,
-                                       const float2* means) {
-    gn_grad_params<N, P>(a, g, at, mu, sc, sh);
-    float f1[N], f3[N];
+  __device__ __forceinline__ void take(const GnArgs& a, const GnGeom& g, const GnPlace& at,
+                                       int channel, const float2* means) {
     int grp[N];
-    gn_groups_of<N>(at.channel, g.cpg, grp);
+    gn_groups_of<N>(channel, g.cpg, grp);
+    const float* rstd = a.rstd + at.sample * g.groups;
 #pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float rs = a.rstd[at.sample * g.groups + grp[e]];
-      f1[e] = -rs * means[grp[e] - at.g0].x;
-      f3[e] = -rs * rs * means[grp[e] - at.g0].y;
+    for (int i = 0; i < P; i++) {
+      const float2 u = means[grp[2 * i] - at.g0], v = means[grp[2 * i + 1] - at.g0];
+      const float ru = rstd[grp[2 * i]], rv = rstd[grp[2 * i + 1]];
+      k1[i] = f2(-ru * u.x, -rv * v.x);
+      k2[i] = f2(-ru * ru * u.y, -rv * rv * v.y);
     }
-    to_pairs<P>(f1, k1);
-    to_pairs<P>(f3, k2);
   }
   __device__ __forceinline__ uint4 operator()(const uint4& x, const uint4& dy) const {
     F2 f[P], d[P];
@@ -893,13 +967,17 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   using B = GnBlock<T, true>;
   constexpr int N = B::N, R = B::kRows;
   constexpr int kWarps = B::kThreads / kWarp;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   float2* sm = reinterpret_cast<float2*>(smem);  // before the walk: the groups' means
   const GnPlace at = GnPlace::of<B>(g, gridDim.x - 1 - blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
   const int width = g.tile_cols * N;
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
+  // (an inactive thread's column may lie past the tile: it takes the first one)
+  const int channel = at.active ? at.channel : at.c0;
+  GnGradOut<T, SILU> value;
+  gn_grad_params<N, N / 2>(a, g, at.sample, channel, value.mu, value.sc, value.sh);
   for (int grp = at.g0 + warp; grp <= at.g1; grp += kWarps) {
     const int t0 = grp * g.cpg / width, tn = ((grp + 1) * g.cpg - 1) / width - t0 + 1;
     float m1 = 0.0f, m2 = 0.0f;
@@ -919,10 +997,7 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     gn_sum_grads(a, g, g.samples * g.chunks, blockIdx.x + static_cast<int64_t>(gridDim.x) * warp,
                  static_cast<int64_t>(gridDim.x) * kWarps);
   __syncthreads();
-  // (an inactive thread's column may lie past the tile: it takes the first one)
-  GnPlace mine = at;
-  if (!at.active) mine.channel = at.c0;
-  const GnGradOut<T, SILU> value(a, g, mine, sm);
+  value.take(a, g, at, channel, sm);
   __syncthreads();  // the rings take the place of sm
   if (!at.active) return;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
@@ -941,7 +1016,7 @@ template <typename T, bool SILU>
 __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     gn_grad_small_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, true>;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 means[GnSmall<T, true>::kGroups];
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, true>::kSlot;
@@ -958,7 +1033,7 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   }
   cp_async_commit();
   GnGradSums<T, SILU> sums;
-  if (n > 0) gn_grad_params<B::N, B::N / 2>(a, g, at, sums.mu, sums.sc, sums.sh);
+  if (n > 0) gn_grad_params<B::N, B::N / 2>(a, g, at.sample, at.channel, sums.mu, sums.sc, sums.sh);
   cp_async_wait<0>();  // a thread reads back only what it copied
   for (int i = 0; i < n; i++)
     sums.add(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot));
@@ -975,7 +1050,14 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
       [&](int grp, float m1, float m2) { means[grp - at.g0] = make_float2(m1 * inv, m2 * inv); });
   __syncthreads();
   if (!at.active) return;
-  const GnGradOut<T, SILU> value(a, g, at, means);
+  GnGradOut<T, SILU> value;
+#pragma unroll
+  for (int i = 0; i < B::N / 2; i++) {
+    value.mu[i] = sums.mu[i];
+    value.sc[i] = sums.sc[i];
+    value.sh[i] = sums.sh[i];
+  }
+  value.take(a, g, at, at.channel, means);
   uint4* o = static_cast<uint4*>(a.out) + base;
   for (int i = 0; i < n; i++)
     st_stream(o + i * row_step,

@@ -90,7 +90,8 @@ SIZES = [
     (2, (16, 16), 640, 32), (1, (5, 9, 11), 128, 32), (4, 33, 512, 1), (1, 2560, 128, 32),
     (1, 2561, 128, 32), (5, 700, 40, 5), (1, 5000, 8, 1), (1, 5000, 8, 8), (3, (77, 93), 320, 32),
     (200, 65, 64, 4), (1, 300, 4104, 3), (2, 90, 8208, 3), (1, 40, 12288, 6), (1, 30, 65536, 1),
-    (1, 100000, 16, 2), (160, 4000, 16, 1),
+    (1, 100000, 16, 2), (160, 4000, 16, 1), (1, 436, 1824, 1), (3, 19, 1112, 8), (2, 9000, 96, 6),
+    (1, 500, 120, 15), (1, 20000, 4096, 16), (2, 50, 680, 17),
 ]
 
 
