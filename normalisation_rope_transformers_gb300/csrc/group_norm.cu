@@ -14,8 +14,8 @@
 // opposite order, so that what was read last still comes from L2.  One block
 // fills an SM; each thread copies its vectors many rows ahead into a ring of
 // its own in shared memory (cp.async), which keeps 64 to 98 KB an SM in flight
-// without registers or barriers.  Samples so small that a block holds all rows
-// of a few groups take one launch.
+// without registers or barriers.  Samples so small that a cluster of up to eight
+// blocks holds all rows of a few groups take one launch and are read once.
 //
 // Any channels / groups works: a thread keeps one 128-bit column of N channels
 // and walks down the rows, sums stay per channel until the block's end, and a
@@ -52,12 +52,16 @@ struct GnBlock {
   static constexpr int kMostSmem = kRing * kStepBytes > kScratch ? kRing * kStepBytes : kScratch;
 };
 
-// What a block of the one-launch kernels holds: rows of a thread, groups.
+// What a block of the one-launch kernels holds at most: rows of a thread, groups.
 template <typename T, bool BACK>
 struct GnSmall {
   using B = GnBlock<T, BACK>;
   static constexpr int kRows = BACK ? 12 : 20;
   static constexpr int kGroups = 64;
+  // Costs besides a block's rows: of a block, of two launches, of summing samples.
+  static constexpr int kBlockCost = BACK ? 12 : 13;
+  static constexpr int kTwoCost = BACK ? 24 : 20;
+  static constexpr int kSumCost = 5;
   static constexpr int kSlot = B::kThreads * static_cast<int>(sizeof(uint4));
   static constexpr int smem(int rows) { return B::kScratch + rows * B::kTensors * kSlot; }
 };
@@ -131,8 +135,15 @@ GnGeom gn_geometry(int64_t samples, int64_t space, int64_t channels, int64_t gro
   return g;
 }
 
-// The layout of the one-launch kernels: tiles of whole groups, one chunk.  False
-// where a sample's rows do not fit.
+// The layout of the one-launch kernels: tiles of whole groups, and chunks of one
+// step, the blocks of a cluster.  False where eight blocks do not hold a tile's rows
+// of a sample, or where two launches are faster.  Costs are in rows of a thread
+// (0.4 us forward, 0.55 us backward), fitted to: forward [2, 256, 1280] 6.2 / 11 us
+// (one / two launches), [8, 159, 464] f32 6.7 / 8.6 us (clusters of 4 / single
+// blocks), [3, 7161, 320] f32 24.4 / 15.8 us, [1, 26229, 48] 16.5 / 8.4 us; backward
+// [4, 1024, 640] 12.8 / 16.0 us.
+constexpr int kGnCluster = 8;
+
 template <typename T, bool BACK>
 bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t groups,
                        GnGeom* out) {
@@ -146,24 +157,38 @@ bool gn_small_geometry(int64_t samples, int64_t space, int64_t channels, int64_t
   while (tile_groups * cpg < sector && groups % (2 * tile_groups) == 0) tile_groups *= 2;
   const int64_t cols = tile_groups * cpg / B::N;
   if (cols > B::kThreads || tile_groups > S::kGroups) return false;
-  const int64_t lanes = B::kThreads / cols, rows = (space + lanes - 1) / lanes;
-  if (rows > S::kRows || samples * (groups / tile_groups) > INT32_MAX) return false;
+  const int64_t lanes = B::kThreads / cols, sets = (space + lanes - 1) / lanes;
+  const int64_t tiles = groups / tile_groups;
+  // Blocks a cluster: waves of blocks, each with a fixed cost and its rows.
+  int64_t chunks = 0, best = INT64_MAX;
+  for (int64_t c = 1; c <= kGnCluster; c *= 2) {
+    const int64_t rows = (sets + c - 1) / c, waves = (samples * tiles * c + kGnSms - 1) / kGnSms;
+    const int64_t cost = waves * (S::kBlockCost + rows) + (c > 1 ? 2 : 0);
+    if (rows <= S::kRows && cost < best) chunks = c, best = cost;
+  }
+  const int64_t all = samples * space * (channels / B::N);
+  const int64_t two = S::kTwoCost + all / (kGnSms * B::kThreads);
+  if (BACK && samples > 1) best += S::kSumCost;  // its third kernel
+  if (chunks == 0 || best > two || samples * tiles * chunks > INT32_MAX) return false;
+  const int64_t rows = (sets + chunks - 1) / chunks;
   GnGeom& g = *out;
   g.samples = samples;
   g.space = space;
-  g.steps = 1;
   g.channels = static_cast<int>(channels);
   g.groups = static_cast<int>(groups);
   g.cpg = static_cast<int>(cpg);
   g.cols = static_cast<int>(channels / B::N);
   g.tile_cols = static_cast<int>(cols);
-  g.tiles = static_cast<int>(groups / tile_groups);
+  g.tiles = static_cast<int>(tiles);
   g.lanes = static_cast<int>(lanes);
   g.unroll = static_cast<int>(rows);
   g.step_rows = g.lanes * g.unroll;
-  g.chunks = g.chunk_steps = 1;
-  g.more_steps = g.last_chunk = 0;
-  g.missing = static_cast<int>(g.step_rows - space);
+  g.chunks = static_cast<int>(chunks);
+  g.steps = (space + g.step_rows - 1) / g.step_rows;
+  g.chunk_steps = static_cast<int>(g.steps / chunks);  // 0 where some blocks have no rows
+  g.more_steps = static_cast<int>(g.steps % chunks);
+  g.last_chunk = static_cast<int>(g.steps - 1);
+  g.missing = static_cast<int>(g.steps * g.step_rows - space);
   return true;
 }
 
@@ -235,13 +260,16 @@ struct GnPlace {
   int c0, c1;              // the tile's channels
   int g0, g1;              // the groups that they belong to
   bool active;
-  template <typename B>
+  // Blocks of a chunk (its tiles) follow one another, or (CLUSTER) those of a tile.
+  template <typename B, bool CLUSTER = false>
   __device__ __forceinline__ static GnPlace of(const GnGeom& g, unsigned block) {
     GnPlace p;
-    p.tile = static_cast<int>(block % g.tiles);
-    const unsigned rest = block / g.tiles;
-    p.chunk = static_cast<int>(rest % g.chunks);
-    p.sample = rest / g.chunks;
+    const unsigned inner = CLUSTER ? g.chunks : g.tiles, outer = CLUSTER ? g.tiles : g.chunks;
+    const unsigned rest = block / inner;
+    const int i = static_cast<int>(block % inner), o = static_cast<int>(rest % outer);
+    p.tile = CLUSTER ? o : i;
+    p.chunk = CLUSTER ? i : o;
+    p.sample = rest / outer;
     p.lane = static_cast<int>(threadIdx.x) / g.tile_cols;
     p.col = p.tile * g.tile_cols + static_cast<int>(threadIdx.x) % g.tile_cols;
     p.active = p.col < g.cols && p.lane < g.lanes;
@@ -364,6 +392,23 @@ struct GnArgs {
   float eps;
   GnScratch scratch;
 };
+
+// The blocks of a cluster: everyone arrives (its shared-memory writes are then
+// visible to the others) and waits; and one float2 of another block's memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
+  unsigned at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at)
+               : "memory");
+  return v;
+}
 
 // How the lanes of a channel are joined: `subs` threads a channel, `per` lanes each.
 struct GnSubs {
@@ -685,21 +730,23 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   });
 }
 
-// Both passes in one launch, for samples so small that a block holds all rows of
-// a few groups in shared memory: block (sample, tile), a tile being whole groups
-// and one chunk.  [2, 256, 1280] bf16: 6.2 us, 11 us in two launches.
+// Both passes in one launch, for samples so small that a cluster of blocks holds
+// all rows of a few groups in shared memory: x is read once.  Block (sample, tile,
+// chunk), a tile being whole groups; the blocks of a cluster join their means and M2
+// through distributed shared memory, in the order of their ranks.
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
     gn_small_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, false>;
   extern __shared__ __align__(128) unsigned char smem[];
-  float2* sm = reinterpret_cast<float2*>(smem);
+  __shared__ float2 parts[GnSmall<T, false>::kGroups], stats[GnSmall<T, false>::kGroups];
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, false>::kSlot;
-  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  const GnPlace at = GnPlace::of<B, true>(g, blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
-  const GnLaneRows rows(g, 0);
-  const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
+  const GnLaneRows rows(g, at.chunk);
+  const int64_t row0 = static_cast<int64_t>(at.chunk) * g.step_rows;
+  const int64_t base = (at.sample * g.space + row0 + at.lane) * g.cols + at.col;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
   const int n = at.active ? rows.of(at.lane, at.lane + 1) : 0;
   const uint4* p = static_cast<const uint4*>(a.x) + base;
@@ -711,19 +758,48 @@ __global__ void __launch_bounds__(GnBlock<T, false>::kThreads, 1)
   GnSums<T> sums;
   if (n > 0) sums.begin(lds128(held));
   for (int i = 0; i < n; i++) sums.add(lds128(held + i * kSlot));
-  __shared__ float2 stats[GnSmall<T, false>::kGroups];
-  const float total = static_cast<float>(g.space);
-  gn_join_lanes<T>(g, at, sums, rows, total, sm, [&](int grp, float mean, float m2) {
-    const float rstd = gn_rstd(m2, total * static_cast<float>(g.cpg), a.eps);
+  const float total = static_cast<float>(g.space) * static_cast<float>(g.cpg);
+  auto finish = [&](int grp, float mean, float m2) {
+    const float rstd = gn_rstd(m2, total, a.eps);
     stats[grp - at.g0] = make_float2(mean, rstd);
-    a.mean[at.sample * g.groups + grp] = mean;
-    a.rstd[at.sample * g.groups + grp] = rstd;
+    if (at.chunk == 0) {
+      a.mean[at.sample * g.groups + grp] = mean;
+      a.rstd[at.sample * g.groups + grp] = rstd;
+    }
+  };
+  const float part_rows = static_cast<float>(g.rows_of(at.chunk));
+  gn_join_lanes<T>(g, at, sums, rows, part_rows, reinterpret_cast<float2*>(smem),
+                   [&](int grp, float mean, float m2) {
+    if (g.chunks == 1)
+      finish(grp, mean, m2);
+    else
+      parts[grp - at.g0] = make_float2(mean, m2);
   });
+  if (g.chunks > 1) {
+    cluster_arrive();
+    cluster_wait();
+    const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
+    for (int grp = at.g0 + warp; grp <= at.g1; grp += B::kThreads / kWarp) {
+      float2 v = make_float2(0.0f, 0.0f);
+      float count = 0.0f;
+      if (lane32 < g.chunks && g.steps_of(lane32) > 0) {  // a block without rows has no part
+        v = cluster_read(parts + grp - at.g0, lane32);
+        count = static_cast<float>(g.rows_of(lane32)) * static_cast<float>(g.cpg);
+      }
+      const float mean = __fdiv_rn(group_sum<kWarp>(count * v.x), total);
+      const float d = v.x - mean;
+      const float m2 = group_sum<kWarp>(count > 0.0f ? fmaf(count * d, d, v.y) : 0.0f);
+      if (lane32 == 0) finish(grp, mean, m2);
+    }
+    cluster_arrive();  // this block has read the others' parts
+  }
   __syncthreads();
-  if (!at.active) return;
-  value.take(g, at, channel, stats);
-  uint4* o = static_cast<uint4*>(a.out) + base;
-  for (int i = 0; i < n; i++) st_stream(o + i * row_step, value(lds128(held + i * kSlot)));
+  if (at.active) {
+    value.take(g, at, channel, stats);
+    uint4* o = static_cast<uint4*>(a.out) + base;
+    for (int i = 0; i < n; i++) st_stream(o + i * row_step, value(lds128(held + i * kSlot)));
+  }
+  if (g.chunks > 1) cluster_wait();  // nobody reads this block's memory any more
 }
 
 // ---------------------------------------------------------------------------
@@ -784,8 +860,9 @@ struct GnGradSums {
 };
 
 // Joins a block's threads: of(channel, S1, S2) is called for each of the tile's
-// channels, then use(group, sum of w S1, sum of w S2) for each of its groups,
-// over its channels in the tile, each once.
+// channels (and sm is left with them, from the tile's first), then use(group, sum
+// of w S1, sum of w S2) for each of its groups, over its channels in the tile,
+// each once.
 template <typename T, bool SILU, typename Of, typename Use>
 __device__ __forceinline__ void gn_grad_join(const GnArgs& a, const GnGeom& g, const GnPlace& at,
                                              const GnGradSums<T, SILU>& sums, float2* sm, Of of,
@@ -826,20 +903,20 @@ __device__ __forceinline__ void gn_grad_join(const GnArgs& a, const GnGeom& g, c
     }
     v.y *= a.rstd[at.sample * g.groups + (at.c0 + c) / g.cpg];
     of(at.c0 + c, v.x, v.y);
-    float w[1];
-    gn_params<1>(a.prm.w, a.prm.is_bf16, at.c0 + c, 1.0f, w);
-    sm[c] = make_float2(w[0] * v.x, w[0] * v.y);
+    sm[c] = v;
   }
   __syncthreads();
   const int warp = threadIdx.x / kWarp, lane32 = threadIdx.x % kWarp;
   constexpr int kWarps = B::kThreads / kWarp;
   const int groups = at.g1 - at.g0 + 1;
   const int split_by = gn_group_warps(groups, min(g.cpg, tile_channels), kWarps);
-  auto sum = [&](int from, int end) {  // of channels [from, end)
+  auto sum = [&](int from, int end) {  // of channels [from, end), by w
     float m1 = 0.0f, m2 = 0.0f;
     for (int c = from + lane32; c < end; c += kWarp) {
-      m1 += sm[c - at.c0].x;
-      m2 += sm[c - at.c0].y;
+      float w[1];
+      gn_params<1>(a.prm.w, a.prm.is_bf16, c, 1.0f, w);
+      m1 = fmaf(w[0], sm[c - at.c0].x, m1);
+      m2 = fmaf(w[0], sm[c - at.c0].y, m2);
     }
     return make_float2(group_sum<kWarp>(m1), group_sum<kWarp>(m2));
   };
@@ -1017,14 +1094,16 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     gn_grad_small_kernel(const GnArgs a, const GnGeom g) {
   using B = GnBlock<T, true>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 means[GnSmall<T, true>::kGroups];
+  __shared__ float2 parts[GnSmall<T, true>::kGroups], means[GnSmall<T, true>::kGroups];
+  float2* sm = reinterpret_cast<float2*>(smem);
   unsigned char* held = smem + B::kScratch + threadIdx.x * sizeof(uint4);
   constexpr int kSlot = GnSmall<T, true>::kSlot;
-  const GnPlace at = GnPlace::of<B>(g, blockIdx.x);
+  const GnPlace at = GnPlace::of<B, true>(g, blockIdx.x);
   pdl_enter();  // before any global read: the previous kernel may still run
-  const int64_t base = (at.sample * g.space + at.lane) * g.cols + at.col;
+  const int64_t row0 = static_cast<int64_t>(at.chunk) * g.step_rows;
+  const int64_t base = (at.sample * g.space + row0 + at.lane) * g.cols + at.col;
   const int64_t row_step = static_cast<int64_t>(g.lanes) * g.cols;
-  const int n = at.active ? GnLaneRows(g, 0).of(at.lane, at.lane + 1) : 0;
+  const int n = at.active ? GnLaneRows(g, at.chunk).of(at.lane, at.lane + 1) : 0;
   const uint4* px = static_cast<const uint4*>(a.x) + base;
   const uint4* pd = static_cast<const uint4*>(a.dy) + base;
   for (int i = 0; i < n; i++) {
@@ -1033,35 +1112,65 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
   }
   cp_async_commit();
   GnGradSums<T, SILU> sums;
-  if (n > 0) gn_grad_params<B::N, B::N / 2>(a, g, at.sample, at.channel, sums.mu, sums.sc, sums.sh);
+  if (n > 0)
+    gn_grad_params<B::N, B::N / 2>(a, g, at.sample, at.channel, sums.mu, sums.sc, sums.sh);
   cp_async_wait<0>();  // a thread reads back only what it copied
   for (int i = 0; i < n; i++)
     sums.add(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot));
   const float inv = 1.0f / (static_cast<float>(g.space) * static_cast<float>(g.cpg));
+  auto channel_sums = [&](int c, float s1, float s2) {
+    if (a.dw == nullptr) return;
+    if (g.samples == 1)
+      gn_put_grads(a, c, s1, s2);
+    else
+      a.scratch.sums[at.sample * g.channels + c] = make_float2(s1, s2);
+  };
   gn_grad_join<T, SILU>(
-      a, g, at, sums, reinterpret_cast<float2*>(smem),
+      a, g, at, sums, sm,
       [&](int c, float s1, float s2) {
-        if (a.dw == nullptr) return;
-        if (g.samples == 1)
-          gn_put_grads(a, c, s1, s2);
-        else
-          a.scratch.sums[at.sample * g.channels + c] = make_float2(s1, s2);
+        if (g.chunks == 1) channel_sums(c, s1, s2);
       },
-      [&](int grp, float m1, float m2) { means[grp - at.g0] = make_float2(m1 * inv, m2 * inv); });
-  __syncthreads();
-  if (!at.active) return;
-  GnGradOut<T, SILU> value;
-#pragma unroll
-  for (int i = 0; i < B::N / 2; i++) {
-    value.mu[i] = sums.mu[i];
-    value.sc[i] = sums.sc[i];
-    value.sh[i] = sums.sh[i];
+      [&](int grp, float m1, float m2) {
+        (g.chunks == 1 ? means : parts)[grp - at.g0] =
+            g.chunks == 1 ? make_float2(m1 * inv, m2 * inv) : make_float2(m1, m2);
+      });
+  if (g.chunks > 1) {
+    cluster_arrive();
+    cluster_wait();
+    const int tile_channels = at.c1 - at.c0;
+    // the blocks share the channels, and each adds up every group's parts
+    for (int i = threadIdx.x; i < tile_channels + at.g1 - at.g0 + 1; i += B::kThreads) {
+      const bool is_channel = i < tile_channels;
+      if (is_channel && i % g.chunks != at.chunk) continue;
+      float s1 = 0.0f, s2 = 0.0f;
+      for (int r = 0; r < g.chunks; r++) {
+        const float2 v = cluster_read(is_channel ? sm + i : parts + i - tile_channels, r);
+        s1 += v.x;
+        s2 += v.y;
+      }
+      if (is_channel)
+        channel_sums(at.c0 + i, s1, s2);
+      else
+        means[i - tile_channels] = make_float2(s1 * inv, s2 * inv);
+    }
+    cluster_arrive();  // this block has read the others' parts
   }
-  value.take(a, g, at, at.channel, means);
-  uint4* o = static_cast<uint4*>(a.out) + base;
-  for (int i = 0; i < n; i++)
-    st_stream(o + i * row_step,
-              value(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot)));
+  __syncthreads();
+  if (at.active) {
+    GnGradOut<T, SILU> value;
+#pragma unroll
+    for (int i = 0; i < B::N / 2; i++) {
+      value.mu[i] = sums.mu[i];
+      value.sc[i] = sums.sc[i];
+      value.sh[i] = sums.sh[i];
+    }
+    value.take(a, g, at, at.channel, means);
+    uint4* o = static_cast<uint4*>(a.out) + base;
+    for (int i = 0; i < n; i++)
+      st_stream(o + i * row_step,
+                value(lds128(held + 2 * i * kSlot), lds128(held + (2 * i + 1) * kSlot)));
+  }
+  if (g.chunks > 1) cluster_wait();  // nobody reads this block's memory any more
 }
 
 constexpr int kGnSumThreads = 256;
@@ -1108,7 +1217,7 @@ cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   }
   using S = GnSmall<T, BACK>;
   constexpr int most = S::smem(S::kRows);
-  static_assert(most <= 232448 - 1024, "a block's shared memory");
+  static_assert(most <= 232448 - 2048, "a block's shared memory, less its static arrays");
   cudaError_t e =
       gn_raise(done, B::kMostSmem > most ? B::kMostSmem : most, stats, apply, small);
   if (e != cudaSuccess) return e;
@@ -1125,8 +1234,20 @@ cudaError_t gn_launch(const GroupNormArgs& in, cudaStream_t s) {
   GnGeom g;
   if (gn_small_geometry<T, BACK>(in.samples, in.space, in.channels, in.groups, &g)) {
     a.scratch.sums = static_cast<float2*>(in.workspace);
-    e = launch_pdl(small, dim3(static_cast<unsigned>(in.samples * g.tiles)), dim3(B::kThreads),
-                   S::smem(g.unroll), s, a, g);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(in.samples * g.tiles * g.chunks));
+    cfg.blockDim = dim3(B::kThreads);
+    cfg.dynamicSmemBytes = S::smem(g.unroll);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(g.chunks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = NR_PDL ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, small, a, g);
     if (e != cudaSuccess || in.dw == nullptr || in.samples == 1) return e;
     // a warp a channel, up to the SMs' worth of blocks
     const int64_t blocks = (in.channels * kWarp + kGnSumThreads - 1) / kGnSumThreads;
@@ -1159,7 +1280,7 @@ int64_t gn_workspace(int64_t samples, int64_t space, int64_t channels, int64_t g
   GnGeom g;
   if (backward ? gn_small_geometry<T, true>(samples, space, channels, groups, &g)
                : gn_small_geometry<T, false>(samples, space, channels, groups, &g)) {
-    *blocks = samples * g.tiles;
+    *blocks = samples * g.tiles * g.chunks;
     return backward && samples > 1 ? samples * channels * static_cast<int64_t>(sizeof(float2)) : 0;
   }
   g = backward ? gn_geometry<T, true>(samples, space, channels, groups)

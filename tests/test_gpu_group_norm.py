@@ -92,6 +92,10 @@ SIZES = [
     (200, 65, 64, 4), (1, 300, 4104, 3), (2, 90, 8208, 3), (1, 40, 12288, 6), (1, 30, 65536, 1),
     (1, 100000, 16, 2), (160, 4000, 16, 1), (1, 436, 1824, 1), (3, 19, 1112, 8), (2, 9000, 96, 6),
     (1, 500, 120, 15), (1, 20000, 4096, 16), (2, 50, 680, 17),
+    # one launch, clusters of 2, 4 and 8 blocks, the last of them short or without rows
+    (1, 9, 2048, 1), (1, 33, 1024, 2), (3, 2600, 128, 32), (1, 20480, 64, 32), (1, 20481, 64, 32),
+    (2, 10239, 64, 8), (7, 41, 1280, 4), (1, 40960, 16, 1), (1, 40961, 16, 1),
+    (9, 1000, 256, 8),
 ]
 
 
