@@ -359,8 +359,10 @@ def _rope_config(rotary_dim, interleaved, theta, llama3, mrope_sections, mrope_i
 
 
 # Checked argument layouts of the calls below.  What the checks look at (types,
-# shapes, strides, devices and options, no addresses and no values) is the key,
-# so a layout that passed once costs one look-up; what they found is the entry.
+# shapes, strides and devices, no addresses and no values) is the key, with the
+# options as plain numbers: an option may be a 0-d tensor, which counts with the
+# value that it has at the call.  A layout that passed once costs one look-up;
+# what they found is the entry.
 _checked = {}
 _CHECKED_MOST = 4096
 
@@ -489,8 +491,14 @@ def qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_sc
                        llama3=None, mrope_sections=None, mrope_interleaved=False, q_out=None):
     """qk_norm_rope_ex with K (quantised from its f32 value) and V written into
     the cache as kv_cache_write does.  Returns q_out."""
+    eps, theta, gemma = float(eps), float(theta), bool(gemma)
+    interleaved, mrope_interleaved = bool(interleaved), bool(mrope_interleaved)
+    if rotary_dim is not None:
+        rotary_dim = int(rotary_dim)
+    if llama3 is not None:
+        llama3 = tuple([float(v) for v in llama3])
     if mrope_sections is not None:
-        mrope_sections = tuple(mrope_sections)
+        mrope_sections = tuple([int(v) for v in mrope_sections])
     options = (eps, gemma, rotary_dim, interleaved, theta, llama3, mrope_sections,
                mrope_interleaved)
     key, known = _known("fused", options, (q, k, v, wq, wk, positions, slots, k_cache, v_cache,
@@ -506,7 +514,7 @@ def qk_norm_rope_cache(q, k, v, wq, wk, positions, slots, k_cache, v_cache, k_sc
                            mrope_interleaved)
         known = _remember(key, (layout, _dtype_code(wq),
                                 (q.shape[0], q.shape[1], _tok_stride(q), _tok_stride(k),
-                                 _tok_stride(v), float(eps), int(bool(gemma)), cfg,
+                                 _tok_stride(v), eps, int(gemma), cfg,
                                  _dtype_code(q)), q.get_device()))
     layout, wcode, sizes, device = known
     if q_out is None:
@@ -527,6 +535,8 @@ def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, r
     `dtype` is float32 or bfloat16 (the outputs', else bfloat16).  Rows behind
     the last sequence are left as they were (in outputs made here: anything).
     Returns (k, v)."""
+    if rows is not None:
+        rows = int(rows)
     key, known = _known("read", (rows, dtype), (k_cache, v_cache, k_scale, v_scale, block_table,
                                                 cu_seqlens, k_out, v_out))
     if known is None:
@@ -542,11 +552,11 @@ def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, r
         dtype = torch.bfloat16 if dtype is None else dtype
         if rows is None:
             raise ValueError("kv_cache_read needs rows or outputs [rows, heads, head_dim]")
-        if int(rows) < 0:
+        if rows < 0:
             raise ValueError("rows must be >= 0")
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("dtype must be bfloat16 or float32, got %s" % dtype)
-        shape = (int(rows), layout[2], layout[3])
+        shape = (rows, layout[2], layout[3])
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             if t is not None:
                 _expect(t, name, dtype, shape)
@@ -610,18 +620,17 @@ def group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, s
     rstd) with stats=True: the [samples, groups] float32 statistics that
     group_norm_backward takes.  No autograd graph is recorded: the gradient is
     a call of its own."""
-    key, known = _known("norm", (groups, eps, activation), (x, w, b, out))
+    groups, eps, act = int(groups), float(eps), _activation(activation)
+    key, known = _known("norm", (groups, eps, act), (x, w, b, out))
     if known is None:
         samples, space, channels, wcode = _check_norm(x, w, b)
-        groups = int(groups)
         if groups < 1 or channels % groups:
             raise ValueError("%d channels do not divide into %d groups" % (channels, groups))
-        act = _activation(activation)
         if out is not None:
             _expect(out, "out", x.dtype, x.shape)
         _cuda(x, w, b, out)
         code = _dtype_code(x)
-        known = _remember(key, (wcode, (samples, space, channels, groups, float(eps), act, code),
+        known = _remember(key, (wcode, (samples, space, channels, groups, eps, act, code),
                                 _group_norm_workspace(samples, space, channels, groups, 0, code),
                                 x.device))
     wcode, sizes, need, device = known
@@ -643,7 +652,8 @@ def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=N
     """The gradient of group_norm: dy and x [samples, ..., channels], the mean
     and rstd that it returned, the same w, b and activation.  Returns (dx, dw,
     db); dw and db have w's dtype (None without w).  dx may be dy or x."""
-    key, known = _known("norm back", activation, (dy, x, mean, rstd, w, b, dx))
+    act = _activation(activation)
+    key, known = _known("norm back", act, (dy, x, mean, rstd, w, b, dx))
     if known is None:
         samples, space, channels, wcode = _check_norm(x, w, b)
         _expect(dy, "dy", x.dtype, x.shape)
@@ -654,7 +664,6 @@ def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=N
         _expect(rstd, "rstd", torch.float32, (samples, groups))
         if groups < 1 or channels % groups:
             raise ValueError("%d channels do not divide into %d groups" % (channels, groups))
-        act = _activation(activation)
         if dx is not None:
             _expect(dx, "dx", x.dtype, x.shape)
         _cuda(x, dy, mean, rstd, w, b, dx)
