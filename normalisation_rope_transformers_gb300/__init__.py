@@ -391,7 +391,13 @@ def _known(*key_and_tensors):
         return None, None
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The same number by a private name, without making a Stream object each call,
+# where torch has it; builds without CUDA do not.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def _launch(device, fn, *args):
