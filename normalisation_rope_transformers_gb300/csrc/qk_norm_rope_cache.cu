@@ -31,8 +31,8 @@ namespace {
 constexpr int kFusedThreads = 128;
 constexpr int kFusedWarps = kFusedThreads / kWarp;
 // Passes in flight of a warp: 3, 5 and 8 ran [26598, 24 + 24 + 24, 128] in 135,
-// 133 and 133 us (128.5 us, 0.94 of the measured copy rate, once the row
-// addresses were formed per token and not per pass).
+// 133 and 133 us (129.0 us, 0.94 of the measured copy rate, with row addresses
+// formed per token and not per pass).
 constexpr int kRing = 5;
 constexpr int kFusedPerSm = 4;  // resident blocks (three: 144 us)
 
@@ -219,12 +219,22 @@ __global__ void __launch_bounds__(kFusedThreads, kFusedPerSm)
         if (axis_sm[i] == 1) p = pos[NPOS > 1 ? 1 : 0];
         if (axis_sm[i] == 2) p = pos[NPOS > 2 ? 2 : 0];
       }
-      // the angle in turns, mod 1: exact for any int32 position
+      // the angle in turns, mod 1, times 2^32: exact for any int32 position
       const unsigned long long prod = static_cast<unsigned long long>(p) * turn_sm[i];
-      const int hi = static_cast<int>(prod >> 32);  // signed turn fraction * 2^32
+      // The nearest quarter turn comes off before the conversion to 24 bits, which
+      // then round an eighth of a turn and not a half: K's codes are made from the
+      // f32 value, with no bf16 rounding to hide the angle's.  At [26598, 4, 128]
+      // 28 of 13.6 million e4m3 codes differ from those of exact values, 42 before,
+      // for 0.4 us of the 129.0 at [26598, 24 + 24 + 24, 128].
+      const unsigned t = static_cast<unsigned>(prod >> 32) + (1u << 29);
+      const int rest = static_cast<int>(t & 0x3FFFFFFFu) - (1 << 29);  // of quarter t >> 30
       float sn, cn;
-      sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);  // angle = pi * hi / 2^31
-      table[i] = make_float2(cn, sn);
+      sincospif(static_cast<float>(rest) * 0x1p-31f, &sn, &cn);
+      const bool odd = (t & 0x40000000u) != 0;
+      // cos is negative in quarters 1 and 2, sin in 2 and 3
+      table[i] = make_float2(
+          __uint_as_float(__float_as_uint(odd ? sn : cn) ^ ((t + 0x40000000u) & 0x80000000u)),
+          __uint_as_float(__float_as_uint(odd ? cn : sn) ^ (t & 0x80000000u)));
     }
     __syncwarp();
     // rotate-half: cos and sin of the lane's N pairs; GPT-J: of the pairs inside
