@@ -622,7 +622,7 @@ __device__ __forceinline__ float2 gn_join(const GnArgs& a, const GnGeom& g, int6
     const int t = tn == 1 ? 0 : i / g.chunks, chunk = i - t * g.chunks, tile = t0 + t;
     count = static_cast<float>(g.rows_of(chunk)) *
             static_cast<float>(min(cb, (tile + 1) * width) - max(ca, tile * width));
-    return __ldg(parts + i);
+    return parts[i];
   };
   // a lane's first parts stay in registers for the second sum
   constexpr int kHeld = 5;
@@ -994,7 +994,7 @@ __device__ __forceinline__ void gn_sum_grads(const GnArgs& a, const GnGeom& g, i
   for (int64_t c = first; c < g.channels; c += step) {
     float t1 = 0.0f, t2 = 0.0f;
     for (int64_t i = lane32; i < rows; i += kWarp) {
-      const float2 v = __ldg(a.scratch.sums + i * g.channels + c);
+      const float2 v = a.scratch.sums[i * g.channels + c];
       t1 += v.x;
       t2 += v.y;
     }
@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(GnBlock<T, true>::kThreads, 1)
     const float2* parts = a.scratch.parts + (at.sample * (g.groups + g.tiles) + grp + t0) *
                                                 static_cast<int64_t>(g.chunks);
     for (int i = lane32; i < g.chunks * tn; i += kWarp) {
-      const float2 v = __ldg(parts + i);
+      const float2 v = parts[i];
       m1 += v.x;
       m2 += v.y;
     }

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const WriteArgs
   pdl_enter();  // before any global read: the previous kernel may still run
   if (row < a.rows) {
     head = row - tok * a.heads.div;
-    slot = __ldg(a.slots + tok);
+    slot = a.slots[tok];
     const T* p = static_cast<const T*>(is_v ? a.src[1] : a.src[0]) +
                  tok * (is_v ? a.stride[1] : a.stride[0]) + head * dim;
 #pragma unroll
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
   // One load a thread instead of a chain of them in the search.
   const bool few = a.seqs <= kReadSeqs;
   if (few) {
-    for (int i = threadIdx.x; i <= a.seqs; i += kReadThreads) cu_sm[i] = __ldg(a.cu + i);
+    for (int i = threadIdx.x; i <= a.seqs; i += kReadThreads) cu_sm[i] = a.cu[i];
     __syncthreads();
   }
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.block_rows;
@@ -309,16 +309,16 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
       where[j] = code_at[r];
       if (where[j] < 0) continue;
       if (FP4) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(side.codes + where[j]) + u);
+        const uint2 c = reinterpret_cast<const uint2*>(side.codes + where[j])[u];
         codes[j].x = c.x;
         codes[j].y = c.y;
-        const uint32_t byte = __ldg(side.scales + scale_at[r] + u / 2);
+        const uint32_t byte = side.scales[scale_at[r] + u / 2];
         // 2^(byte - 127); bytes 0 and 255 (2^-127, NaN) as the format has them
         scale[j] = byte == 0 ? 0x1p-127f : __uint_as_float(byte == 255 ? 0x7FC00000u : byte << 23);
       } else {
         codes[j] = ld_stream(reinterpret_cast<const uint4*>(side.codes + where[j]) + u);
-        scale[j] = __ldg(reinterpret_cast<const float*>(side.scales + scale_at[r]) +
-                         a.head_units.quot(u));
+        scale[j] =
+            reinterpret_cast<const float*>(side.scales + scale_at[r])[a.head_units.quot(u)];
       }
     }
 #pragma unroll

@@ -19,22 +19,26 @@ constexpr int kWarp = 32;
 // ---------------------------------------------------------------------------
 // 128-bit global memory access
 // ---------------------------------------------------------------------------
+// Every load is coherent (never ld.global.nc): the kernel before this one in the
+// stream may write the data while this one is already resident (see pdl_enter),
+// and in-place calls overwrite it; the non-coherent path is only for what nobody
+// writes during a kernel's life.
+//
 // Read-once data (x, residual, q, k): no L1 allocation, and ask L2 to fetch the
-// whole 256-byte sector group.  Only used on data that no thread of the same
-// launch writes before reading it (each thread reads its own elements before it
-// overwrites them in place).
+// whole 256-byte sector group.  Not ordered against this launch's own writes: each
+// thread reads its own elements before it overwrites them in place.
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 
-// Data shared by all rows (weights, shift, scale): normal cached read-only path.
+// Data shared by all rows (weights, shift, scale): normal cached path.
 __device__ __forceinline__ uint4 ld_param(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -76,11 +80,13 @@ __device__ __forceinline__ void st_plain(void* p, uint4 v) {
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch.  Every kernel of the library is launched with
 // programmatic stream serialisation, so it may be scheduled while the kernel
-// before it in the stream is still finishing.  pdl_enter, the first statement
-// of every kernel, lets the next kernel in the stream be scheduled early
-// (griddepcontrol.launch_dependents) and then waits until the previous kernel
-// has completed and its writes are visible (griddepcontrol.wait) -- so no
-// global memory is read before that, whoever launched the previous kernel.
+// before it in the stream is still finishing.  pdl_enter lets the next kernel
+// in the stream be scheduled early (griddepcontrol.launch_dependents) and then
+// waits until the previous kernel has completed and its writes are visible
+// (griddepcontrol.wait).  Every kernel calls it before its first access to global
+// memory; only index arithmetic and copies of the arguments into shared memory
+// come before.  The loads behind it are coherent and, being volatile or behind
+// its memory clobber, are not moved in front of it.
 // Without a programmatic predecessor the wait returns at once.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_enter() {

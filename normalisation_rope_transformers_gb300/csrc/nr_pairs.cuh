@@ -9,7 +9,7 @@ namespace nr {
 // ld_stream and st_stream of 32 bytes (32-byte aligned).
 __device__ __forceinline__ void ld_stream32(const void* p, uint4& a, uint4& b) {
   asm volatile(
-      "ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      "ld.global.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
       : "l"(p));
 }

@@ -51,7 +51,7 @@ template <typename WT>
 __device__ __forceinline__ float load_w(const WT* w, int i);
 template <>
 __device__ __forceinline__ float load_w<float>(const float* w, int i) {
-  return __ldg(w + i);
+  return w[i];
 }
 template <>
 __device__ __forceinline__ float load_w<__nv_bfloat16>(const __nv_bfloat16* w, int i) {

@@ -56,7 +56,7 @@ struct FusedArgs {
   int rot_vec, interleaved, mrope;
 };
 
-__device__ __forceinline__ float weight_of(const float* w, int i) { return __ldg(w + i); }
+__device__ __forceinline__ float weight_of(const float* w, int i) { return w[i]; }
 __device__ __forceinline__ float weight_of(const __nv_bfloat16* w, int i) {
   return __bfloat162float(w[i]);
 }
@@ -199,10 +199,10 @@ __global__ void __launch_bounds__(kFusedThreads, kFusedPerSm)
   auto fetch = [&](const Cursor& u) {
     slot_of_token = -1;
     if (u.tok < a.tokens) {
-      slot_of_token = __ldg(a.slots + u.tok);
+      slot_of_token = a.slots[u.tok];
 #pragma unroll
       for (int ax = 0; ax < NPOS; ax++)
-        pos[ax] = (ax == 0 || a.mrope) ? __ldg(a.pos + ax * a.tokens + u.tok) : 0;
+        pos[ax] = (ax == 0 || a.mrope) ? a.pos[ax * a.tokens + u.tok] : 0;
     }
   };
   fetch(cur);

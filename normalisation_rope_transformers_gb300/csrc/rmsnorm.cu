@@ -100,7 +100,6 @@ __global__ void __launch_bounds__((PW && VPT <= 2) ? kDecodeMaxThreads : kRowMax
                                                            float hidden_f, float inv_hidden,
                                                            float eps, float w_add, int64_t rows,
                                                            int64_t prefetch_rows) {
-  pdl_enter();  // before any global read: the previous kernel may still run
   constexpr int N = Vec<T>::N;
   __shared__ float scratch[32];
   const int64_t row_off = static_cast<int64_t>(blockIdx.x) * nvec;  // in vectors
@@ -111,6 +110,9 @@ __global__ void __launch_bounds__((PW && VPT <= 2) ? kDecodeMaxThreads : kRowMax
   uint4 xv[VPT];
   uint4 rv[VPT];
   uint4 wpre[PW ? VPT : 1];
+  // Before any global read: the previous kernel may still run.  The addresses are
+  // formed before it ([8, 4096] bf16 cold: 1.80 us, 1.96 us with them behind it).
+  pdl_enter();
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const int vi = threadIdx.x + k * blockDim.x;
