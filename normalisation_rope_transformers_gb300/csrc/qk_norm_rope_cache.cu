@@ -20,7 +20,6 @@
 // stages and one barrier an item took 166 us (whole tokens) to 307 us (items
 // of a third): about 2 us an item whatever its rows, in the chain from the
 // barrier through the angles to the next barrier.
-#include <atomic>
 #include <type_traits>
 
 #include "quant.cuh"

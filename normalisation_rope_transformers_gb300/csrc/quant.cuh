@@ -44,9 +44,10 @@ __device__ __forceinline__ float clamp_scale(float a) {
 }
 
 // a / 448 correctly rounded, without a division: q = a * RN(1/448) corrected by
-// its remainder a - 448 q, which is exact.  (The outcome depends on a's 2^23
-// significands alone while nothing underflows; compared with the division for
-// every one of them.)
+// its remainder a - 448 q, which is exact (Markstein's method of dividing with a
+// fused multiply-add).  The outcome depends on a's 2^23 significands alone while
+// nothing underflows; a test compares every one of them with the division, at the
+// least, the largest and other binades of a.
 __device__ __forceinline__ float fp8_scale(float a) {
   constexpr float r = 1.0f / 448.0f;
   const float q = a * r;
@@ -95,7 +96,8 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&x)[N], float inv) {
   return c;
 }
 
-// n / d for 0 <= n < 2^31 by a multiplication (d >= 1): with s = ceil(log2 d)
+// n / d for 0 <= n < 2^31 by a multiplication (d >= 1), the method of Granlund and
+// Montgomery for divisions by an invariant integer: with s = ceil(log2 d)
 // and m = floor(2^(31 + s) / d) + 1, floor(n m / 2^(31 + s)) is exact for such n.
 struct FastDiv {
   uint32_t mul, shift, div;
