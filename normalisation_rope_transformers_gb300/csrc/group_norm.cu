@@ -223,10 +223,13 @@ __device__ __forceinline__ void gn_params(const void* p, int is_bf16, int channe
   }
 }
 
-// sigmoid(z).  Where the result is rounded to bf16: the hardware exponential
-// and reciprocal (each about 2^-22), two instructions of the special unit a
-// value; below z = -88 the exponential is infinite and the sigmoid zero, off by
-// less than 2^-126.  For f32 from t = e^-|z|, which never overflows.
+// sigmoid(z).  For bf16 tensors the hardware exponential and reciprocal, two
+// instructions of the special unit a value: within (1.3 |z| + 7) 2^-24 of itself
+// for z < 0 (a rounding of z log2(e), 2^-22 of the exponential, 2^-23 of the
+// reciprocal) and less above; below 2^-126 it is zero.  y and dx are rounded to
+// bf16 after it.  dw and db of f32 parameters are not: there the choice rests on x
+// and dy, whose own bf16 roundings (2^-9) moved every term of those sums by far
+// more.  For f32 tensors from t = e^-|z|, which never overflows.
 template <typename T>
 __device__ __forceinline__ F2 gn_sigmoid2(F2 z);
 template <>
