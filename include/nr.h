@@ -21,6 +21,11 @@
  *   nr_kv_cache_read                sequences of the cache read back
  *   nr_group_norm                   group norm, channels last, optional SiLU
  *   nr_group_norm_backward          its gradient
+ *   nr_rmsnorm_quant                RMSNorm (optional residual add) with e4m3 codes and
+ *                                   scales made from the data
+ *   nr_token_logprobs               log probabilities of given tokens, entropy and the
+ *                                   largest alternatives of rows of logits
+ *   nr_token_logprobs_backward      their gradient
  *
  * Conventions shared by every entry point
  *   - Pointers are DEVICE pointers (CUDA global memory) owned by the caller; the
@@ -125,6 +130,31 @@ nr_status nr_rmsnorm(void* out, const void* x, const void* w, void* residual, in
 nr_status nr_rmsnorm_quant_fp8(void* codes, void* out_bf16, const void* x, const void* w,
                                void* residual, int64_t rows, int64_t hidden, nr_dtype dtype,
                                float eps, int gemma, float scale, cudaStream_t stream);
+
+/*
+ * RMSNorm (optionally with the fused residual add) with FP8 e4m3 codes and scales
+ * made from the data.  n_j is nr_rmsnorm's normalised value in f32, not rounded to
+ * `dtype`; a is the largest |n_j| of a scale's extent (a NaN counts as nothing), taken
+ * as at least 2^-100 and at most the largest f32:
+ *   NR_SCALES_ROW    f32 [rows]:               scale = a / 448, code_j = e4m3(n_j * (448 / a))
+ *   NR_SCALES_GROUP  f32 [rows, hidden / 128]: the same for each 128 elements
+ *   NR_SCALES_MX     bytes [rows, hidden / 32]: s the least integer with a / 2^s <= 448,
+ *                    byte s + 127, code_j = e4m3(n_j / 2^s) (OCP MXFP8)
+ * Codes are rounded to nearest even; the value held is code * scale.
+ *
+ * codes     [rows, hidden] bytes.
+ * scales    as above; 4-byte aligned (ROW, GROUP).
+ * x, w, residual, rows, dtype, eps, gemma: as nr_rmsnorm.
+ * hidden    a multiple of 8 (bf16) or 4 (f32), of 128 for GROUP and of 32 for MX; at most
+ *           32768 (bf16) / 16384 (f32).
+ * No output may overlap an input or another output.
+ * Errors: as nr_rmsnorm.
+ */
+typedef enum nr_scale_layout { NR_SCALES_ROW = 0, NR_SCALES_GROUP = 1, NR_SCALES_MX = 2 } nr_scale_layout;
+
+nr_status nr_rmsnorm_quant(void* codes, void* scales, const void* x, const void* w,
+                           void* residual, int64_t rows, int64_t hidden, nr_dtype dtype,
+                           float eps, int gemma, nr_scale_layout layout, cudaStream_t stream);
 
 /*
  * Per-head RMSNorm of Q and K followed by NeoX rotary embedding, in one pass.
@@ -369,6 +399,51 @@ nr_status nr_group_norm_backward(void* dx, void* dw, void* db, const void* dy, c
  * and the size errors of nr_group_norm. */
 nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channels,
                                   int64_t groups, int backward, nr_dtype dtype, int64_t* bytes);
+
+/*
+ * Log probabilities of given tokens, entropy and the largest alternatives, over rows of
+ * logits.  With z = logits * inv_temperature, m the largest z of the row:
+ *     lse     = m + ln sum_j e^(z_j - m)
+ *     logprob = z_token - lse;  0 where the token is outside [0, vocab) (padding)
+ *     entropy = -sum_j p_j ln p_j,  p_j = e^(z_j - lse)
+ *     top_ids the `top` largest logits, largest first, equal ones by the lower index;
+ *     top_logprob theirs
+ * all in f32.  A logit of -inf has probability 0.  A row of -inf alone: lse and the log
+ * probabilities are -inf, the entropy 0.  A row that holds a NaN or +inf: NaN, and its
+ * top_ids may be -1.
+ *
+ * logprob, entropy, lse  [rows] f32.
+ * top_logprob, top_ids   [rows, top] f32 and int64; NULL with top = 0.
+ * logits                 [rows, vocab], `stride` elements between rows, dtype `dtype`;
+ *                        aligned to an element (rows need no 16 bytes).
+ * tokens                 [rows] int64 (8-byte aligned).
+ * vocab in [1, 2^31), stride >= vocab, top in [0, min(32, vocab)].
+ * inv_temperature        finite, > 0.
+ * Errors: as nr_rmsnorm.
+ */
+nr_status nr_token_logprobs(float* logprob, float* entropy, float* lse, float* top_logprob,
+                            int64_t* top_ids, const void* logits, const int64_t* tokens,
+                            int64_t rows, int64_t vocab, int64_t stride, int64_t top,
+                            float inv_temperature, nr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Gradient of nr_token_logprobs' logprob and entropy with respect to the logits:
+ *     dlogits_j = inv_temperature * (g ([j = token] - p_j) - h p_j (ln p_j + entropy))
+ * with g = dlogprob (0 for padding) and h = dentropy of the row.  A row of -inf alone has
+ * gradient 0.
+ *
+ * dlogits             [rows, vocab], `dlogits_stride` elements between rows, dtype `dtype`;
+ *                     may be logits itself (with its stride).
+ * dlogprob, dentropy  [rows] f32; either may be NULL (0).
+ * lse, entropy        as nr_token_logprobs wrote them for the same inv_temperature; entropy
+ *                     may be NULL when dentropy is.
+ * Other arguments and errors: as nr_token_logprobs.
+ */
+nr_status nr_token_logprobs_backward(void* dlogits, const float* dlogprob, const float* dentropy,
+                                     const void* logits, const int64_t* tokens, const float* lse,
+                                     const float* entropy, int64_t rows, int64_t vocab,
+                                     int64_t stride, int64_t dlogits_stride,
+                                     float inv_temperature, nr_dtype dtype, cudaStream_t stream);
 
 /*
  * LayerNorm (no affine) fused with adaLN modulation.

@@ -26,11 +26,18 @@ or ``__graft_entry__.build()``).
                        ..., q_out=None)
     group_norm(x, groups, w=None, b=None, eps=1e-5, activation=None, out=None, stats=False)
     group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=None)
+    rmsnorm_quant(x, w, residual=None, eps=1e-6, gemma=False, scales="row", codes=None,
+                  scales_out=None)
+    token_logprobs(logits, tokens, top=0, temperature=1.0)
+    token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy=None,
+                            temperature=1.0, dlogits=None)
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -109,6 +116,14 @@ lib.nr_group_norm_backward.restype = _int
 lib.nr_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, _int,
                                         ctypes.POINTER(_i64)]
 lib.nr_group_norm_workspace.restype = _int
+lib.nr_rmsnorm_quant.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _f32, _int, _int, _vp]
+lib.nr_rmsnorm_quant.restype = _int
+lib.nr_token_logprobs.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
+                                  _int, _vp]
+lib.nr_token_logprobs.restype = _int
+lib.nr_token_logprobs_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                           _i64, _f32, _int, _vp]
+lib.nr_token_logprobs_backward.restype = _int
 lib.nr_device_status.argtypes = [_vp]
 lib.nr_device_status.restype = _int
 lib.nr_test_wait_probe.argtypes = [_i64, _vp]
@@ -126,10 +141,14 @@ NR_CACHE_FP8 = 0
 NR_CACHE_MXFP4 = 1
 NR_ACT_NONE = 0
 NR_ACT_SILU = 1
+NR_SCALES_ROW = 0
+NR_SCALES_GROUP = 1
+NR_SCALES_MX = 2
 ENTRY_POINTS = ("nr_rmsnorm", "nr_rmsnorm_quant_fp8", "nr_qk_norm_rope", "nr_qk_norm_rope_ex", "nr_ln_modulate",
                 "nr_silu_and_mul", "nr_gelu_and_mul", "nr_gated_residual_ln_modulate",
                 "nr_kv_cache_write", "nr_qk_norm_rope_cache", "nr_kv_cache_read",
                 "nr_group_norm", "nr_group_norm_backward", "nr_group_norm_workspace",
+                "nr_rmsnorm_quant", "nr_token_logprobs", "nr_token_logprobs_backward",
                 "nr_device_status", "nr_test_wait_probe",
                 "nr_status_string", "nr_last_error_message", "nr_version")
 
@@ -692,6 +711,145 @@ def group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=N
     return dx, dw, db
 
 
+_SCALE_LAYOUTS = {"row": NR_SCALES_ROW, "group": NR_SCALES_GROUP, "mx": NR_SCALES_MX}
+
+
+def rmsnorm_quant(x, w, residual=None, eps=1e-6, gemma=False, scales="row", codes=None,
+                  scales_out=None):
+    """RMSNorm of x [rows, hidden] (with `residual`, first residual <- round(x + residual)
+    in place) into e4m3 codes with scales made from the data.  `scales` is "row" (float32
+    [rows]), "group" (float32 [rows, hidden / 128]) or "mx" (uint8 e8m0 bytes [rows,
+    hidden / 32], powers of two).  The value held is code * scale.  Returns (codes uint8,
+    scales); codes.view(torch.float8_e4m3fn) are the codes as numbers."""
+    eps, gemma = float(eps), bool(gemma)
+    if scales not in _SCALE_LAYOUTS:
+        raise ValueError("scales must be 'row', 'group' or 'mx', got %r" % (scales,))
+    key, known = _known("norm quant", (eps, gemma, scales), (x, w, residual, codes, scales_out))
+    if known is None:
+        _rows_2d(x, "x")
+        rows, hidden = x.shape
+        _expect(w, "w", x.dtype, (hidden,))
+        if residual is not None:
+            _expect(residual, "residual", x.dtype, x.shape)
+        extent = {"row": 0, "group": 128, "mx": 32}[scales]
+        if extent and hidden % extent:
+            raise ValueError("hidden = %d is not a multiple of %d" % (hidden, extent))
+        shape = (rows, hidden // extent) if extent else (rows,)
+        dtype = torch.uint8 if scales == "mx" else torch.float32
+        if codes is not None:
+            _expect(codes, "codes", torch.uint8, x.shape)
+        if scales_out is not None:
+            _expect(scales_out, "scales_out", dtype, shape)
+        _cuda(x, w, residual, codes, scales_out)
+        known = _remember(key, (shape, dtype, (rows, hidden, _dtype_code(x), eps, int(gemma),
+                                               _SCALE_LAYOUTS[scales]), x.device))
+    shape, dtype, sizes, device = known
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.uint8, device=device)
+    if scales_out is None:
+        scales_out = torch.empty(shape, dtype=dtype, device=device)
+    _launch(device.index, lib.nr_rmsnorm_quant, codes.data_ptr(), scales_out.data_ptr(),
+            x.data_ptr(), w.data_ptr(), None if residual is None else residual.data_ptr(), *sizes)
+    return codes, scales_out
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns: float32 [rows], and with top > 0 the alternatives'
+    float32 log probabilities and int64 ids [rows, top]."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+
+
+def _inv_temperature(temperature):
+    temperature = float(temperature)
+    if not (math.isfinite(temperature) and temperature > 0):
+        raise ValueError("temperature must be finite and > 0, got %r" % (temperature,))
+    return 1.0 / temperature
+
+
+def _logits_2d(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be [rows, vocab] with contiguous rows" % name)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("the rows of %s overlap" % name)
+    _dtype_code(t)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def token_logprobs(logits, tokens, top=0, temperature=1.0):
+    """Log softmax of logits [rows, vocab] (rows may be strided) / temperature at tokens
+    [rows] int64 (outside the vocabulary: padding, 0), the entropy of each row, its log sum
+    of exponentials, and the `top` largest alternatives (at most 32; equal logits by the
+    lower index).  Returns a TokenLogprobs.  No autograd graph is recorded: the gradient
+    is token_logprobs_backward."""
+    top, inv_t = int(top), _inv_temperature(temperature)
+    key, known = _known("logprobs", (top, inv_t), (logits, tokens))
+    if known is None:
+        stride = _logits_2d(logits, "logits")
+        rows, vocab = logits.shape
+        _expect(tokens, "tokens", torch.int64, (rows,))
+        if not 0 <= top <= min(32, vocab):
+            raise ValueError("top = %d must be in [0, min(32, vocab)]" % top)
+        _cuda(logits, tokens)
+        known = _remember(key, ((rows, vocab, stride, top, inv_t, _dtype_code(logits)),
+                                logits.device))
+    sizes, device = known
+    rows = sizes[0]
+    # tensors of their own: views of one cost the host more than allocations
+    logprob, entropy, lse = (torch.empty(rows, dtype=torch.float32, device=device)
+                             for _ in range(3))
+    top_logprob = top_ids = None
+    if top:
+        top_logprob = torch.empty((rows, top), dtype=torch.float32, device=device)
+        top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
+    _launch(device.index, lib.nr_token_logprobs, logprob.data_ptr(), entropy.data_ptr(),
+            lse.data_ptr(),
+            None if top_logprob is None else top_logprob.data_ptr(),
+            None if top_ids is None else top_ids.data_ptr(), logits.data_ptr(), tokens.data_ptr(),
+            *sizes)
+    return TokenLogprobs(logprob, entropy, lse, top_logprob, top_ids)
+
+
+def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy=None,
+                            temperature=1.0, dlogits=None):
+    """The gradient of token_logprobs with respect to the logits, for the gradients of its
+    logprob and entropy ([rows] float32, either may be None), its lse and (with dentropy)
+    entropy, and the same temperature.  dlogits may be logits (in place).  Returns
+    dlogits."""
+    inv_t = _inv_temperature(temperature)
+    key, known = _known("logprobs back", inv_t, (dlogprob, dentropy, logits, tokens, lse, entropy,
+                                                 dlogits))
+    if known is None:
+        stride = _logits_2d(logits, "logits")
+        rows, vocab = logits.shape
+        _expect(tokens, "tokens", torch.int64, (rows,))
+        _expect(lse, "lse", torch.float32, (rows,))
+        if dentropy is not None and entropy is None:
+            raise ValueError("dentropy needs the entropy that token_logprobs returned")
+        for t, name in ((dlogprob, "dlogprob"), (dentropy, "dentropy"), (entropy, "entropy")):
+            if t is not None:
+                _expect(t, name, torch.float32, (rows,))
+        out_stride = vocab
+        if dlogits is not None:
+            out_stride = _logits_2d(dlogits, "dlogits")
+            _expect(dlogits, "dlogits", logits.dtype, logits.shape, contiguous=False)
+        _cuda(logits, dlogprob, dentropy, tokens, lse, entropy, dlogits)
+        known = _remember(key, ((rows, vocab, stride, out_stride, inv_t, _dtype_code(logits)),
+                                logits.device))
+    sizes, device = known
+    if dlogits is None:
+        dlogits = torch.empty(sizes[:2], dtype=logits.dtype, device=device)
+    _launch(device.index, lib.nr_token_logprobs_backward, dlogits.data_ptr(),
+            *[None if t is None else t.data_ptr() for t in (dlogprob, dentropy, logits, tokens, lse,
+                                                            entropy)], *sizes)
+    return dlogits
+
+
 def ln_modulate(x, shift, scale, eps=1e-6, rows_per_sample=None, out=None):
     """LayerNorm (no affine) of x [rows, hidden] then * (1 + scale) + shift,
     with shift/scale [samples, hidden] (row r uses sample r // rows_per_sample).
@@ -773,6 +931,7 @@ def gelu_and_mul(x, out=None):
 __all__ = ["rmsnorm", "rmsnorm_quant_fp8", "qk_norm_rope", "qk_norm_rope_ex", "RopeConfig", "ln_modulate",
            "silu_and_mul", "gelu_and_mul", "device_status", "wait_probe",
            "gated_residual_ln_modulate", "kv_cache_write", "kv_cache_read", "qk_norm_rope_cache",
-           "group_norm", "group_norm_backward", "KvCache", "NrError", "lib",
+           "group_norm", "group_norm_backward", "rmsnorm_quant", "token_logprobs", "TokenLogprobs",
+           "token_logprobs_backward", "KvCache", "NrError", "lib",
            "LIB_PATH", "ENTRY_POINTS", "NR_F32", "NR_BF16", "NR_CACHE_FP8", "NR_CACHE_MXFP4",
-           "NR_ACT_NONE", "NR_ACT_SILU"]
+           "NR_ACT_NONE", "NR_ACT_SILU", "NR_SCALES_ROW", "NR_SCALES_GROUP", "NR_SCALES_MX"]

@@ -899,3 +899,145 @@ nr_status nr_gelu_and_mul(void* out, const void* x, int64_t rows, int64_t inter,
 }
 
 }  // extern "C"
+
+extern "C" {
+
+nr_status nr_rmsnorm_quant(void* codes, void* scales, const void* x, const void* w,
+                           void* residual, int64_t rows, int64_t hidden, nr_dtype dtype,
+                           float eps, int gemma, nr_scale_layout layout, cudaStream_t stream) {
+  CallRange range("nr_rmsnorm_quant");
+  const char* fn = "nr_rmsnorm_quant";
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (layout != NR_SCALES_ROW && layout != NR_SCALES_GROUP && layout != NR_SCALES_MX)
+    return fail(NR_ERR_VALUE, "%s: unknown scale layout %d", fn, (int)layout);
+  if (rows < 0 || hidden <= 0)
+    return fail(NR_ERR_SHAPE, "%s: need rows >= 0 and hidden > 0", fn);
+  if (!eps_ok(eps)) return fail(NR_ERR_VALUE, "%s: eps must be finite and >= 0", fn);
+  if (gemma != 0 && gemma != 1) return fail(NR_ERR_VALUE, "%s: gemma must be 0 or 1", fn);
+  const int64_t extent = layout == NR_SCALES_GROUP ? 128 : layout == NR_SCALES_MX ? 32 : 0;
+  const int64_t unit = extent ? extent : vec_elems(dtype);
+  if (hidden % unit != 0)
+    return fail(NR_ERR_UNSUPPORTED, "%s: hidden = %lld is not a multiple of %lld", fn,
+                (long long)hidden, (long long)unit);
+  if (hidden / vec_elems(dtype) > nr::kQuantMaxVectors)
+    return fail(NR_ERR_UNSUPPORTED, "%s: hidden = %lld is above %lld for this dtype", fn,
+                (long long)hidden, (long long)(nr::kQuantMaxVectors * vec_elems(dtype)));
+  if (rows > INT32_MAX) return fail(NR_ERR_SHAPE, "%s: rows too large", fn);
+  if (rows == 0) return ok();
+  if (!codes || !scales || !x || !w)
+    return fail(NR_ERR_NULL, "%s: codes, scales, x and w must be non-NULL", fn);
+  if (!aligned16(codes) || !aligned16(x) || !aligned16(w) || !aligned16(residual) ||
+      (layout != NR_SCALES_MX && misaligned(scales, 4)))
+    return fail(NR_ERR_ALIGN, "%s: pointers must be 16-byte aligned (f32 scales 4-byte)", fn);
+  const int64_t row_bytes = hidden * elem_size(dtype);
+  const int64_t per_row = layout == NR_SCALES_MX ? hidden / 32 : extent ? hidden / 128 * 4 : 4;
+  const Region rc = dense(codes, rows * hidden), rs = dense(scales, rows * per_row);
+  const Region rx = dense(x, rows * row_bytes), rw = dense(w, row_bytes);
+  const Region rr = dense(residual, residual ? rows * row_bytes : 0);
+  const Region ins[] = {rx, rw, rr};
+  if (any_overlap(ins, 3, rc) || any_overlap(ins, 3, rs) || overlap(rc, rs))
+    return fail(NR_ERR_ALIAS, "%s: an output overlaps an input or the other output", fn);
+  if (overlap(rr, rx) || overlap(rr, rw))
+    return fail(NR_ERR_ALIAS, "%s: residual overlaps x or w", fn);
+  return from_cuda(nr::launch_rmsnorm_quant(codes, scales, x, w, residual, rows, hidden,
+                                            dtype == NR_BF16, eps, gemma, (int)layout, stream),
+                   "nr_rmsnorm_quant launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of rows of logits; `stride` elements apart.
+nr_status check_logits(const char* fn, int64_t rows, int64_t vocab, int64_t stride, float inv_t,
+                       nr_dtype dtype) {
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (rows < 0 || vocab <= 0 || stride < vocab)
+    return fail(NR_ERR_SHAPE, "%s: need rows >= 0, vocab > 0 and stride >= vocab", fn);
+  if (vocab > INT32_MAX || rows > INT32_MAX || stride > INT64_MAX / 8 / (rows > 0 ? rows : 1))
+    return fail(NR_ERR_SHAPE, "%s: rows, vocab or stride too large", fn);
+  // blocks of one launch: at most eight a row forwards, one a 4096 elements backwards
+  const int64_t per_row = vocab / 4096 + 1;
+  if (rows > INT32_MAX / (per_row > 8 ? per_row : 8))
+    return fail(NR_ERR_SHAPE, "%s: too many rows for one launch", fn);
+  if (!(isfinite(inv_t) && inv_t > 0.0f))
+    return fail(NR_ERR_VALUE, "%s: inv_temperature must be finite and > 0", fn);
+  return NR_OK;
+}
+
+Region logit_rows(const void* p, int64_t rows, int64_t vocab, int64_t stride, nr_dtype dtype) {
+  return Region{reinterpret_cast<uintptr_t>(p), stride * elem_size(dtype), vocab * elem_size(dtype),
+                rows};
+}
+
+}  // namespace
+
+extern "C" {
+
+nr_status nr_token_logprobs(float* logprob, float* entropy, float* lse, float* top_logprob,
+                            int64_t* top_ids, const void* logits, const int64_t* tokens,
+                            int64_t rows, int64_t vocab, int64_t stride, int64_t top,
+                            float inv_temperature, nr_dtype dtype, cudaStream_t stream) {
+  CallRange range("nr_token_logprobs");
+  const char* fn = "nr_token_logprobs";
+  if (const nr_status s = check_logits(fn, rows, vocab, stride, inv_temperature, dtype)) return s;
+  if (top < 0 || top > nr::kLogprobMostTop || top > vocab)
+    return fail(NR_ERR_SHAPE, "%s: top = %lld must be in [0, min(%d, vocab)]", fn, (long long)top,
+                nr::kLogprobMostTop);
+  if (rows == 0) return ok();
+  if (!logprob || !entropy || !lse || !logits || !tokens || (top > 0 && (!top_logprob || !top_ids)))
+    return fail(NR_ERR_NULL, "%s: the outputs, logits and tokens must be non-NULL", fn);
+  if (misaligned(logits, elem_size(dtype)) || misaligned(tokens, 8) || misaligned(logprob, 4) ||
+      misaligned(entropy, 4) || misaligned(lse, 4) || misaligned(top_logprob, 4) ||
+      misaligned(top_ids, 8))
+    return fail(NR_ERR_ALIGN, "%s: pointers must be aligned to their elements", fn);
+  const Region ins[] = {logit_rows(logits, rows, vocab, stride, dtype), dense(tokens, rows * 8)};
+  const Region outs[] = {dense(logprob, rows * 4), dense(entropy, rows * 4), dense(lse, rows * 4),
+                         dense(top_logprob, top > 0 ? rows * top * 4 : 0),
+                         dense(top_ids, top > 0 ? rows * top * 8 : 0)};
+  for (int i = 0; i < 5; i++)
+    if (any_overlap(ins, 2, outs[i]) || any_overlap(outs, i, outs[i]))
+      return fail(NR_ERR_ALIAS, "%s: an output overlaps an input or another output", fn);
+  return from_cuda(nr::launch_token_logprobs(logprob, entropy, lse, top_logprob, top_ids, logits,
+                                             tokens, rows, vocab, stride, static_cast<int>(top),
+                                             inv_temperature, dtype == NR_BF16, stream),
+                   "nr_token_logprobs launch");
+}
+
+nr_status nr_token_logprobs_backward(void* dlogits, const float* dlogprob, const float* dentropy,
+                                     const void* logits, const int64_t* tokens, const float* lse,
+                                     const float* entropy, int64_t rows, int64_t vocab,
+                                     int64_t stride, int64_t dlogits_stride,
+                                     float inv_temperature, nr_dtype dtype, cudaStream_t stream) {
+  CallRange range("nr_token_logprobs_backward");
+  const char* fn = "nr_token_logprobs_backward";
+  if (const nr_status s = check_logits(fn, rows, vocab, stride, inv_temperature, dtype)) return s;
+  if (const nr_status s = check_logits(fn, rows, vocab, dlogits_stride, inv_temperature, dtype))
+    return s;
+  if (rows == 0) return ok();
+  if (!dlogits || !logits || !tokens || !lse || (dentropy && !entropy))
+    return fail(NR_ERR_NULL, "%s: dlogits, logits, tokens, lse (and entropy with dentropy) must be "
+                             "non-NULL", fn);
+  const int es = elem_size(dtype);
+  if (misaligned(dlogits, es) || misaligned(logits, es) || misaligned(tokens, 8) ||
+      misaligned(lse, 4) || misaligned(entropy, 4) || misaligned(dlogprob, 4) ||
+      misaligned(dentropy, 4))
+    return fail(NR_ERR_ALIGN, "%s: pointers must be aligned to their elements", fn);
+  const Region out = logit_rows(dlogits, rows, vocab, dlogits_stride, dtype);
+  const Region in = logit_rows(logits, rows, vocab, stride, dtype);
+  const Region rest[] = {dense(tokens, rows * 8), dense(lse, rows * 4),
+                         dense(entropy, entropy ? rows * 4 : 0),
+                         dense(dlogprob, dlogprob ? rows * 4 : 0),
+                         dense(dentropy, dentropy ? rows * 4 : 0)};
+  const bool in_place = dlogits == logits && (dlogits_stride == stride || rows == 1);
+  if ((!in_place && overlap(out, in)) || any_overlap(rest, 5, out))
+    return fail(NR_ERR_ALIAS, "%s: dlogits overlaps an input (only dlogits == logits is allowed)",
+                fn);
+  return from_cuda(nr::launch_token_logprobs_backward(dlogits, dlogprob, dentropy, logits, tokens,
+                                                      lse, entropy, rows, vocab, stride,
+                                                      dlogits_stride, inv_temperature,
+                                                      dtype == NR_BF16, stream),
+                   "nr_token_logprobs_backward launch");
+}
+
+}  // extern "C"

@@ -187,6 +187,24 @@ cudaError_t launch_group_norm(const GroupNormArgs& args, int is_bf16, cudaStream
 cudaError_t launch_group_norm_backward(const GroupNormArgs& args, int is_bf16,
                                        cudaStream_t stream);
 
+// RMSNorm with an e4m3 output and scales from the data; mode as nr_scale_format.
+cudaError_t launch_rmsnorm_quant(void* codes, void* scales, const void* x, const void* w,
+                                 void* residual, int64_t rows, int64_t hidden, int is_bf16,
+                                 float eps, int gemma, int mode, cudaStream_t stream);
+
+// Log probabilities of given tokens; top = 0: no alternatives.
+constexpr int kLogprobMostTop = 32;
+cudaError_t launch_token_logprobs(float* logprob, float* entropy, float* lse, float* top_logprob,
+                                  int64_t* top_ids, const void* logits, const int64_t* tokens,
+                                  int64_t rows, int64_t vocab, int64_t stride, int top,
+                                  float inv_t, int is_bf16, cudaStream_t stream);
+cudaError_t launch_token_logprobs_backward(void* dlogits, const float* dlogprob,
+                                           const float* dentropy, const void* logits,
+                                           const int64_t* tokens, const float* lse,
+                                           const float* entropy, int64_t rows, int64_t vocab,
+                                           int64_t stride, int64_t out_stride, float inv_t,
+                                           int is_bf16, cudaStream_t stream);
+
 // Device status word: bits set by kernels whose bounded waits ran out.
 constexpr unsigned kStatusBitQkBulkWait = 1u;
 constexpr unsigned kStatusBitProbeWait = 2u;
