@@ -23,6 +23,8 @@
  *   nr_group_norm_backward          its gradient
  *   nr_rmsnorm_quant                RMSNorm (optional residual add) with e4m3 codes and
  *                                   scales made from the data
+ *   nr_cache_attention              attention of one token, a chain or a tree of drafted
+ *                                   tokens over sequences of the cache
  *   nr_token_logprobs               log probabilities of given tokens, entropy and the
  *                                   largest alternatives of rows of logits
  *   nr_token_logprobs_backward      their gradient
@@ -343,6 +345,51 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
                            const int32_t* block_table, int64_t table_width,
                            const int32_t* cu_seqlens, int64_t seqs, int64_t rows, nr_dtype dtype,
                            cudaStream_t stream);
+
+/*
+ * Attention of each sequence's newest tokens over everything the cache holds for it.
+ * Sequence s has L = seq_lens[s] tokens in the cache; its queries are rows cu_q[s] ..
+ * cu_q[s + 1] - 1 of q, and these T tokens are the last T of the L (their K and V are written
+ * before this call, by nr_kv_cache_write or nr_qk_norm_rope_cache).  Query t of s sees position
+ * p < L - T always, and position L - T + j, its own or another new token,
+ *     without a tree: when j <= t (one token, or a chain);
+ *     with one:       when bit j % 32 of tree[cu_q[s] + t][j / 32] is set (a tree of drafted
+ *                     tokens: each token's ancestors and itself).
+ * With query head i reading K/V head i / (q_heads / heads), over the positions it sees:
+ *     score_p = scale * sum_d q_d k_pd;  lse = ln sum_p e^(score_p)
+ *     out     = round(sum_p e^(score_p - lse) v_p)
+ * A query that sees nothing gets zeros, and lse = -inf.  Positions whose block is past the
+ * table or outside [0, blocks) are seen by nobody.  What K, V and scales hold at positions that
+ * a query does not see (NaN, infinities) does not touch it.
+ *
+ * out          [tokens, q_heads, head_dim] contiguous, dtype `dtype`.
+ * lse          [tokens, q_heads] f32, or NULL.
+ * q            [tokens, q_heads, head_dim], q_tok_stride elements between tokens (a multiple of
+ *              16 bytes), dtype `dtype`.
+ * block_table  [seqs, table_width] int32, as nr_kv_cache_read.
+ * seq_lens     [seqs] int32, at most 2^30 each.
+ * cu_q         [seqs + 1] int32, not decreasing; NULL: one query a sequence (tokens == seqs).
+ *              Rows outside [cu_q[0], cu_q[seqs]) are left as they were.
+ * tree         [tokens, tree_words] int32; NULL with tree_words = 0.  Words past a sequence's T
+ *              tokens are ignored; new tokens past the words are not seen.
+ * All tables are device memory.  q_heads is a multiple of the cache's heads; head_dim is 64, 128
+ * or 256; tokens * q_heads < 2^31; scale is finite.
+ * workspace    as nr_group_norm, of at least nr_cache_attention_workspace bytes.
+ * Sums are formed in a fixed order (the same inputs give the same bits).  Scores, weights and sums
+ * are f32; weights are rounded to f16 for the product with V (bf16 tensors), or held in 22 bits
+ * (f32 tensors).  MXFP4 elements below 2^-37 of their head row's largest scale count as zero.
+ * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
+ */
+nr_status nr_cache_attention(void* out, float* lse, const void* q, const nr_kv_cache* cache,
+                             const int32_t* block_table, int64_t table_width,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t seqs,
+                             int64_t tokens, int64_t q_heads, int64_t q_tok_stride,
+                             const int32_t* tree, int64_t tree_words, float scale, nr_dtype dtype,
+                             void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of nr_cache_attention, whatever the other sizes, into *bytes.  Errors:
+ * NR_ERR_NULL, NR_ERR_UNSUPPORTED. */
+nr_status nr_cache_attention_workspace(int64_t head_dim, int64_t* bytes);
 
 typedef enum nr_activation { NR_ACT_NONE = 0, NR_ACT_SILU = 1 } nr_activation;
 

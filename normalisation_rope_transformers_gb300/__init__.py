@@ -28,6 +28,8 @@ or ``__graft_entry__.build()``).
     group_norm_backward(dy, x, mean, rstd, w=None, b=None, activation=None, dx=None)
     rmsnorm_quant(x, w, residual=None, eps=1e-6, gemma=False, scales="row", codes=None,
                   scales_out=None)
+    cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q=None,
+                    tree=None, scale=None, out=None, return_lse=False)
     token_logprobs(logits, tokens, top=0, temperature=1.0)
     token_logprobs_backward(dlogprob, dentropy, logits, tokens, lse, entropy=None,
                             temperature=1.0, dlogits=None)
@@ -118,6 +120,11 @@ lib.nr_group_norm_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, _int,
 lib.nr_group_norm_workspace.restype = _int
 lib.nr_rmsnorm_quant.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _f32, _int, _int, _vp]
 lib.nr_rmsnorm_quant.restype = _int
+lib.nr_cache_attention.argtypes = [_vp, _vp, _vp, ctypes.POINTER(KvCache), _vp, _i64, _vp, _vp, _i64,
+                                   _i64, _i64, _i64, _vp, _i64, _f32, _int, _vp, _i64, _vp]
+lib.nr_cache_attention.restype = _int
+lib.nr_cache_attention_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
+lib.nr_cache_attention_workspace.restype = _int
 lib.nr_token_logprobs.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
                                   _int, _vp]
 lib.nr_token_logprobs.restype = _int
@@ -148,6 +155,7 @@ ENTRY_POINTS = ("nr_rmsnorm", "nr_rmsnorm_quant_fp8", "nr_qk_norm_rope", "nr_qk_
                 "nr_silu_and_mul", "nr_gelu_and_mul", "nr_gated_residual_ln_modulate",
                 "nr_kv_cache_write", "nr_qk_norm_rope_cache", "nr_kv_cache_read",
                 "nr_group_norm", "nr_group_norm_backward", "nr_group_norm_workspace",
+                "nr_cache_attention", "nr_cache_attention_workspace",
                 "nr_rmsnorm_quant", "nr_token_logprobs", "nr_token_logprobs_backward",
                 "nr_device_status", "nr_test_wait_probe",
                 "nr_status_string", "nr_last_error_message", "nr_version")
@@ -600,6 +608,73 @@ def kv_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, r
     return k_out, v_out
 
 
+def cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q=None,
+                    tree=None, scale=None, out=None, return_lse=False):
+    """Attention of each sequence's newest tokens over what the cache (as kv_cache_write's)
+    holds for it.  q is [tokens, q_heads, head_dim], token-strided, its heads a multiple of the
+    cache's; seq_lens [seqs] int32 counts a sequence's tokens in the cache, the newest among
+    them; cu_q [seqs + 1] int32 says which rows of q belong to which sequence (None: one
+    each).  A query sees every earlier token, itself, and of its sequence's other new
+    tokens those in front of it, or with `tree` [tokens, words] int32 those whose bit is set
+    (bit j % 32 of word j / 32 for the j-th new token; a token's own bit included).  `scale`
+    is 1 / sqrt(head_dim) if not given.  A query that sees nothing gets zeros.  Returns out
+    [tokens, q_heads, head_dim], or (out, lse) with the float32 [tokens, q_heads] log sums of
+    exponentials."""
+    if scale is not None:
+        scale = float(scale)
+    return_lse = bool(return_lse)
+    key, known = _known("attention", (scale, return_lse),
+                        (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, tree,
+                         out))
+    if known is None:
+        layout = _cache_layout(k_cache, v_cache, k_scale, v_scale)
+        _heads_3d(q, "q")
+        tokens, heads, dim = q.shape
+        if dim != layout[3]:
+            raise ValueError("q must have the cache's head_dim %d, got %s"
+                             % (layout[3], tuple(q.shape)))
+        if heads < 1 or heads % layout[2]:
+            raise ValueError("%d query heads are no multiple of the cache's %d"
+                             % (heads, layout[2]))
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a [seqs, blocks] tensor")
+        seqs = block_table.shape[0]
+        _expect(block_table, "block_table", torch.int32, block_table.shape)
+        _expect(seq_lens, "seq_lens", torch.int32, (seqs,))
+        if cu_q is not None:
+            _expect(cu_q, "cu_q", torch.int32, (seqs + 1,))
+        elif tokens != seqs:
+            raise ValueError("without cu_q there is one query a sequence: %d tokens, %d sequences"
+                             % (tokens, seqs))
+        words = 0
+        if tree is not None:
+            if not isinstance(tree, torch.Tensor) or tree.dim() != 2 or tree.shape[1] < 1:
+                raise ValueError("tree must be a [tokens, words] tensor")
+            words = tree.shape[1]
+            _expect(tree, "tree", torch.int32, (tokens, words))
+        if out is not None:
+            _expect(out, "out", q.dtype, q.shape)
+        _cuda(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, tree, out)
+        need = ctypes.c_int64()
+        _check(lib.nr_cache_attention_workspace(dim, ctypes.byref(need)))
+        known = _remember(key, (layout, block_table.shape[1],
+                                (seqs, tokens, heads, _tok_stride(q)), words,
+                                dim ** -0.5 if scale is None else scale, _dtype_code(q),
+                                need.value, q.device))
+    layout, width, sizes, words, scale, code, need, device = known
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if return_lse else None
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _launch(device.index, lib.nr_cache_attention, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), q.data_ptr(),
+            _kv_cache(layout, k_cache, v_cache, k_scale, v_scale), block_table.data_ptr(), width,
+            seq_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(), *sizes,
+            None if tree is None else tree.data_ptr(), words, scale, code, workspace.data_ptr(),
+            need)
+    return (out, lse) if return_lse else out
+
+
 def _activation(name):
     if name is None or name == "none":
         return NR_ACT_NONE
@@ -931,7 +1006,8 @@ def gelu_and_mul(x, out=None):
 __all__ = ["rmsnorm", "rmsnorm_quant_fp8", "qk_norm_rope", "qk_norm_rope_ex", "RopeConfig", "ln_modulate",
            "silu_and_mul", "gelu_and_mul", "device_status", "wait_probe",
            "gated_residual_ln_modulate", "kv_cache_write", "kv_cache_read", "qk_norm_rope_cache",
-           "group_norm", "group_norm_backward", "rmsnorm_quant", "token_logprobs", "TokenLogprobs",
+           "group_norm", "group_norm_backward", "rmsnorm_quant", "cache_attention",
+           "token_logprobs", "TokenLogprobs",
            "token_logprobs_backward", "KvCache", "NrError", "lib",
            "LIB_PATH", "ENTRY_POINTS", "NR_F32", "NR_BF16", "NR_CACHE_FP8", "NR_CACHE_MXFP4",
            "NR_ACT_NONE", "NR_ACT_SILU", "NR_SCALES_ROW", "NR_SCALES_GROUP", "NR_SCALES_MX"]

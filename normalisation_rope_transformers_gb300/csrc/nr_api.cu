@@ -1041,3 +1041,82 @@ nr_status nr_token_logprobs_backward(void* dlogits, const float* dlogprob, const
 }
 
 }  // extern "C"
+
+extern "C" {
+
+nr_status nr_cache_attention_workspace(int64_t head_dim, int64_t* bytes) {
+  const char* fn = "nr_cache_attention_workspace";
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(NR_ERR_UNSUPPORTED, "%s: head_dim %lld is not 64, 128 or 256", fn,
+                (long long)head_dim);
+  if (bytes == nullptr) return fail(NR_ERR_NULL, "%s: bytes must be non-NULL", fn);
+  *bytes = nr::cache_attention_workspace(head_dim);
+  return ok();
+}
+
+nr_status nr_cache_attention(void* out, float* lse, const void* q, const nr_kv_cache* cache,
+                             const int32_t* block_table, int64_t table_width,
+                             const int32_t* seq_lens, const int32_t* cu_q, int64_t seqs,
+                             int64_t tokens, int64_t q_heads, int64_t q_tok_stride,
+                             const int32_t* tree, int64_t tree_words, float scale, nr_dtype dtype,
+                             void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  CallRange range("nr_cache_attention");
+  const char* fn = "nr_cache_attention";
+  if (!valid_dtype(dtype)) return fail(NR_ERR_DTYPE, "%s: unknown dtype %d", fn, (int)dtype);
+  if (seqs < 0 || tokens < 0 || table_width < 0 || tree_words < 0 || q_heads < 1)
+    return fail(NR_ERR_SHAPE, "%s: need seqs, tokens, table_width, tree_words >= 0, q_heads >= 1",
+                fn);
+  const bool empty = tokens == 0 || seqs == 0;
+  nr::KvCacheArgs args;
+  if (const nr_status s = check_cache(fn, cache, !empty, &args)) return s;
+  const int64_t dim = cache->head_dim, row = q_heads * dim;
+  if (dim != 64 && dim != 128 && dim != 256)
+    return fail(NR_ERR_UNSUPPORTED, "%s: head_dim %lld is not 64, 128 or 256", fn, (long long)dim);
+  if (q_heads > 65536 || q_heads % cache->heads != 0)
+    return fail(NR_ERR_SHAPE, "%s: %lld query heads are no multiple of %lld K/V heads (or too many)",
+                fn, (long long)q_heads, (long long)cache->heads);
+  if (seqs >= INT32_MAX || table_width > INT32_MAX || tree_words > INT32_MAX / 32 ||
+      tokens > INT32_MAX / q_heads)
+    return fail(NR_ERR_SHAPE, "%s: seqs, table_width, tree_words or tokens * q_heads too large", fn);
+  if (q_tok_stride < row || q_tok_stride > INT64_MAX / 8 / (tokens > 0 ? tokens : 1))
+    return fail(NR_ERR_SHAPE, "%s: token stride smaller than q_heads * head_dim, or too large", fn);
+  if (!cu_q && tokens != seqs)
+    return fail(NR_ERR_SHAPE, "%s: without cu_q there is one query a sequence (%lld, %lld)", fn,
+                (long long)tokens, (long long)seqs);
+  if (!isfinite(scale)) return fail(NR_ERR_VALUE, "%s: scale must be finite", fn);
+  if (empty) return ok();
+  if ((tree != nullptr) != (tree_words > 0))
+    return fail(NR_ERR_NULL, "%s: tree is given exactly when tree_words > 0", fn);
+  if (!out || !q || !seq_lens || (!block_table && table_width > 0) || !workspace)
+    return fail(NR_ERR_NULL, "%s: out, q, block_table, seq_lens and workspace must be non-NULL", fn);
+  const int es = elem_size(dtype);
+  if ((q_tok_stride * es) % 16 != 0)
+    return fail(NR_ERR_ALIGN, "%s: the token stride must be a multiple of 16 bytes", fn);
+  if (!aligned16(out) || !aligned16(q) || !aligned16(workspace) || misaligned(lse, 4) ||
+      misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(cu_q, 4) ||
+      misaligned(tree, 4))
+    return fail(NR_ERR_ALIGN, "%s: out, q and workspace must be 16-byte aligned, the rest 4-byte",
+                fn);
+  const int64_t need = nr::cache_attention_workspace(dim);
+  if (workspace_bytes < need)
+    return fail(NR_ERR_SHAPE, "%s: the workspace has %lld bytes, %lld are needed", fn,
+                (long long)workspace_bytes, (long long)need);
+  const Region ro = dense(out, tokens * row * es), rl = dense(lse, lse ? tokens * q_heads * 4 : 0);
+  const Region ws = dense(workspace, workspace_bytes);
+  const Region ins[] = {
+      Region{reinterpret_cast<uintptr_t>(q), q_tok_stride * es, row * es, tokens},
+      dense(block_table, seqs * table_width * 4), dense(seq_lens, seqs * 4),
+      dense(cu_q, cu_q ? (seqs + 1) * 4 : 0), dense(tree, tokens * tree_words * 4)};
+  const CacheRegions held(*cache);
+  if (any_overlap(ins, 5, ro) || any_overlap(ins, 5, rl) || any_overlap(ins, 5, ws) ||
+      overlap(ro, rl) || overlap(ro, ws) || overlap(rl, ws) || held.overlaps(ro) ||
+      held.overlaps(rl) || held.overlaps(ws))
+    return fail(NR_ERR_ALIAS, "%s: an output or the workspace overlaps another tensor", fn);
+  const nr::CacheAttentionArgs p = {out,      lse,  q,      block_table, seq_lens,
+                                    cu_q,     tree, table_width, seqs,   tokens,
+                                    q_heads,  q_tok_stride, tree_words,  scale, workspace};
+  return from_cuda(nr::launch_cache_attention(args, p, dtype == NR_BF16, stream),
+                   "nr_cache_attention launch");
+}
+
+}  // extern "C"

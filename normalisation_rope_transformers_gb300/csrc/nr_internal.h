@@ -192,6 +192,23 @@ cudaError_t launch_rmsnorm_quant(void* codes, void* scales, const void* x, const
                                  void* residual, int64_t rows, int64_t hidden, int is_bf16,
                                  float eps, int gemma, int mode, cudaStream_t stream);
 
+// Attention over a cache; pointers as nr_cache_attention's.
+struct CacheAttentionArgs {
+  void* out;
+  float* lse;
+  const void* q;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* tree;
+  int64_t table_width, seqs, tokens, q_heads, q_stride, tree_words;
+  float scale;
+  void* workspace;
+};
+int64_t cache_attention_workspace(int64_t head_dim);  // bytes
+cudaError_t launch_cache_attention(const KvCacheArgs& cache, const CacheAttentionArgs& args,
+                                   int is_bf16, cudaStream_t stream);
+
 // Log probabilities of given tokens; top = 0: no alternatives.
 constexpr int kLogprobMostTop = 32;
 cudaError_t launch_token_logprobs(float* logprob, float* entropy, float* lse, float* top_logprob,
