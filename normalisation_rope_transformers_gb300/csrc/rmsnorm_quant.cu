@@ -124,7 +124,30 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
     }
   }
   block_sum_max(sum, top, scratch);
-  const float inv = rstd_refined(row_mean_of(sum, a.hidden, a.inv_hidden), a.eps);
+  float inv;
+  {
+    const float ms = row_mean_of(sum, a.hidden, a.inv_hidden);
+    if (ms + a.eps >= 0x1p-80f && ms <= 0x1p120f) {
+      inv = rstd_refined(ms, a.eps);
+    } else {  // squares near the ends of f32's range: of scaled values (the same for the block)
+      const float f = ms < 1.0f ? 0x1p60f : 0x1p-80f;
+      float none = 0.0f;
+      sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < VPT; k++) {
+        const int i = threadIdx.x + k * blockDim.x;
+        if (i < a.nvec) {
+          float v[N];
+          Vec<T>::unpack(xv[k], v);
+#pragma unroll
+          for (int e = 0; e < N; e++) sum = fmaf(v[e] * f, v[e] * f, sum);
+        }
+      }
+      block_sum_max(sum, none, scratch2);
+      inv = rstd_refined(row_mean_of(sum, a.hidden, a.inv_hidden), a.eps * f * f) * f;
+      __syncthreads();  // scratch2 may be used again
+    }
+  }
   // n = (v inv) w, or (row scales) v w with inv in the factor.  The latter loses
   // nothing while v w stays far from the ends of f32's range; a row that does not
   // (a NaN among them) takes its maximum from n.
