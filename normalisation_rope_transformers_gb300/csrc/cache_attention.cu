@@ -49,7 +49,12 @@ struct Words {
     if constexpr (N >= 16) {
 #pragma unroll
       for (int i = 0; i < N / 16; i++) {
-        const uint4 v = in ? ld_stream(p + i * step) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        // no wider prefetch into L2: the neighbouring head's codes are another block's
+        if (in)
+          asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "l"(p + i * step));
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     } else if constexpr (N == 8) {
@@ -669,7 +674,10 @@ int64_t attn_need() {
   return (shares * 16 + 127) / 128 * 128 + 2 * shares * kAttnRows * (DIM + 2) * 4;
 }
 
-// The opt-in to more than 48 KB of shared memory, once a kernel and device.
+// The opt-in to more than 48 KB of shared memory, once a kernel and device.  Both kernels ask
+// for the largest share of the SM's memory: an SM that the join ran on with a small one has no
+// room for all blocks of the next call, which then runs in two waves ([400009 tokens] calls back to back
+// took 428 us, calls apart 272 us).
 template <typename Kernel>
 cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
   int device = 0;
@@ -679,6 +687,9 @@ cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
   if (done[device].load(std::memory_order_relaxed)) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess) done[device].store(1, std::memory_order_relaxed);
   return e;
 }
@@ -687,8 +698,9 @@ template <typename T, bool FP4, int DIM>
 cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM>);
   constexpr unsigned shares = kSms * attn_blocks<DIM>;
-  static std::atomic<int> done[64];
+  static std::atomic<int> done[64], done_join[64];
   cudaError_t e = allow_shared(cache_attention_kernel<T, FP4, DIM>, shared, done);
+  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, DIM>, 0, done_join);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
