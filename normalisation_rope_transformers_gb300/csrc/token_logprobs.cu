@@ -11,9 +11,13 @@
 //
 // Alternatives: every element has a key of its own, value first, then the lowest
 // index.  The k-th largest of the threads' maxima of the first chunk is a lower bound
-// of the k-th largest element; what exceeds the bound is appended to a list in shared
-// memory, from which one warp takes the k largest at the end.  A list that fills up is
-// cut to its k largest, which raises the bound, so any order of values ends.
+// of the k-th largest element; the vectors whose maxima reach it are noted in a list in
+// shared memory.  At the end one warp raises the bound to the k-th largest of the noted
+// maxima, reads the vectors that reach that again and orders their elements.  (Noting the
+// elements themselves costs 30 us at [4093, 151551] with k = 5, 110 us with k = 20.)  Where
+// the list does not hold them (rising rows, many equal values) the whole row is read again,
+// with a list that is cut to its k largest when it fills up, which raises the bound: any order
+// of values ends.
 //
 // Gradient: dz = p (-g - h (ln p + H)) + g [j = token], p = e^(z - lse), g and h the
 // gradients of logprob and entropy H: one read and one write of the logits.
@@ -30,7 +34,9 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;                       // vectors a thread and chunk
 constexpr int kChunk = kThreads * kUnroll;       // vectors
-constexpr int kList = 1024;                      // candidates
+constexpr int kList = 1000;                      // noted vectors, or candidates (below 1024)
+constexpr int kFew = 64;                         // vectors read again
+constexpr int kCandidates = 256;                 // elements of theirs
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -114,26 +120,46 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Largest element of the vectors (a NaN counts as nothing).
-__device__ __forceinline__ float top_of(const uint4 (&v)[kUnroll], __nv_bfloat16) {
-  uint32_t m = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
-#pragma unroll
-  for (int j = 1; j < kUnroll; j++)
-    m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w)));
+// Largest element of a vector (a NaN counts as nothing).
+template <typename T>
+__device__ __forceinline__ float top_of(const uint4& v);
+template <>
+__device__ __forceinline__ float top_of<__nv_bfloat16>(const uint4& v) {
+  const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
   return fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), -kInf);
 }
-__device__ __forceinline__ float top_of(const uint4 (&v)[kUnroll], float) {
-  float m = -kInf;
-#pragma unroll
-  for (int j = 0; j < kUnroll; j++)
-    m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y))),
-              fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w)));
-  return m;
+template <>
+__device__ __forceinline__ float top_of<float>(const uint4& v) {
+  return fmaxf(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))),
+               -kInf);
+}
+
+// The largest T, zero below bit LOW, that at least k of a warp's values reach (0 if there are
+// fewer): two bits at a time, three counts of at most 1023 in one word.  each(f) calls f with
+// each value of the lane.
+template <int LOW, typename Each>
+__device__ __forceinline__ uint32_t kth_bound(const Each& each, int k, uint32_t from = 0,
+                                              int high = 30) {
+  uint32_t bound = from;
+#pragma unroll 1
+  for (int bit = high; bit >= LOW; bit -= 2) {
+    uint32_t n = 0;
+    each([&](uint32_t v) {
+      n += (v >= (bound | 1u << bit) ? 1u : 0u) + (v >= (bound | 2u << bit) ? 1u << 10 : 0u) +
+           (v >= (bound | 3u << bit) ? 1u << 20 : 0u);
+    });
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    const uint32_t need = static_cast<uint32_t>(k);
+    bound |= (n >> 20 >= need ? 3u : (n >> 10 & 1023u) >= need ? 2u : (n & 1023u) >= need ? 1u : 0u)
+             << bit;
+  }
+  return bound;
 }
 
 // The k largest of `n` keys in shared memory, by one warp, in order, into `best`
-// (zeros where there are fewer).  The keys are lost.  No key is there twice.
-__device__ __forceinline__ void take_largest(uint64_t* keys, int n, int k, uint64_t* best) {
+// (zeros where there are fewer), one after the other.  The keys are lost.
+__device__ __noinline__ void take_one_by_one(uint64_t* keys, int n, int k, uint64_t* best) {
   const int lane = threadIdx.x % kWarp;
   uint64_t mine = 0;
   int at = -1;
@@ -157,16 +183,167 @@ __device__ __forceinline__ void take_largest(uint64_t* keys, int n, int k, uint6
   }
 }
 
+// The same where at most 32 keys reach the k-th largest value (its neighbours in the order
+// included): a bound by bits of the value, and places by counting.  No key is there twice.
+__device__ __forceinline__ void take_largest(uint64_t* keys, int n, int k, uint64_t* best) {
+  const int lane = threadIdx.x % kWarp;
+  auto each = [&](auto&& f) {
+    for (int i = lane; i < n; i += kWarp) f(static_cast<uint32_t>(keys[i] >> 32));
+  };
+  auto reach = [&](uint32_t bound) {
+    uint32_t c = 0;
+    each([&](uint32_t v) { c += v >= bound; });
+    return __reduce_add_sync(0xFFFFFFFFu, c);
+  };
+  uint32_t bound = 0;
+  if (n > kWarp) {
+    bound = kth_bound<16>(each, k);
+    if (reach(bound) > kWarp) {
+      bound = kth_bound<0>(each, k, bound, 14);
+      if (reach(bound) > kWarp) {  // equal values
+        take_one_by_one(keys, n, k, best);
+        return;
+      }
+    }
+  }
+  int have = 0;
+  for (int base = 0; base < n; base += kWarp) {
+    const uint64_t key = base + lane < n ? keys[base + lane] : 0;
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, key != 0 && static_cast<uint32_t>(key >> 32) >= bound);
+    const int at = have + __popc(in & ((1u << lane) - 1u));
+    if (in >> lane & 1u) best[at] = key;
+    have += __popc(in);
+  }
+  __syncwarp();
+  const uint64_t mine = lane < have ? best[lane] : 0;
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < kWarp; i++) rank += __shfl_sync(0xFFFFFFFFu, mine, i) > mine;
+  __syncwarp();
+  best[lane] = 0;
+  __syncwarp();
+  if (mine != 0 && rank < k) best[rank] = mine;
+  __syncwarp();
+}
+
 // What a block shares; the other blocks of its cluster are read by the first.
 struct Shared {
   uint64_t list[kList];
+  uint64_t candidates[kCandidates];
+  uint32_t few[kFew];
   uint64_t best[kLogprobMostTop];
   uint64_t bound;
   uint32_t maxima[kThreads];
   Stats stats[kThreads / kWarp];
   Stats total;
   int count;
+  int lost;  // something had no room
 };
+
+// A thread's element outside the vectors.
+struct Extra {
+  float x;
+  uint32_t at;
+};
+
+// The largest elements from the noted vectors and the extra elements, by one warp.  Sets
+// sh.lost where they have no room.
+template <typename T>
+__device__ __forceinline__ void read_noted(Shared& sh, const uint4* body, uint32_t head,
+                                           const Extra& extra, int top) {
+  constexpr int N = Vec<T>::N;
+  const int lane = threadIdx.x % kWarp;
+  const int n = sh.count;
+  const uint32_t bound = kth_bound<16>(
+      [&](auto&& f) {
+        for (int i = lane; i < n; i += kWarp) f(static_cast<uint32_t>(sh.list[i] >> 32));
+      },
+      top);
+  const unsigned before = (1u << lane) - 1u;
+  int few = 0;
+  for (int base = 0; base < n; base += kWarp) {
+    const uint64_t note = base + lane < n ? sh.list[base + lane] : 0;
+    const bool in = note != 0 && static_cast<uint32_t>(note >> 32) >= bound;
+    const unsigned all = __ballot_sync(0xFFFFFFFFu, in);
+    const int at = few + __popc(all & before);
+    if (in && at < kFew) sh.few[at] = static_cast<uint32_t>(note);
+    few += __popc(all);
+  }
+  __syncwarp();
+  int have = 0;
+  auto offer = [&](uint64_t key) {  // by the whole warp; 0: nothing
+    const bool in = key != 0 && static_cast<uint32_t>(key >> 32) >= bound;
+    const unsigned all = __ballot_sync(0xFFFFFFFFu, in);
+    const int at = have + __popc(all & before);
+    if (in && at < kCandidates) sh.candidates[at] = key;
+    have += __popc(all);
+  };
+  for (int base = 0; base < min(few, kFew); base += kWarp) {
+    const bool in = base + lane < min(few, kFew);
+    const uint32_t v = in ? sh.few[base + lane] : 0;
+    float u[N];
+    Vec<T>::unpack(in ? ld_param(body + v) : make_uint4(0u, 0u, 0u, 0u), u);
+#pragma unroll
+    for (int i = 0; i < N; i++) offer(in && u[i] == u[i] ? key_of(u[i], head + v * N + i) : 0);
+  }
+  offer(extra.at != 0xFFFFFFFFu && extra.x == extra.x ? key_of(extra.x, extra.at) : 0);
+  __syncwarp();
+  if (few > kFew || have > kCandidates) {
+    if (lane == 0) sh.lost = 1;
+  } else {
+    take_largest(sh.candidates, have, top, sh.best);
+  }
+}
+
+// The candidates of the vectors [v0, v1) and of the extra elements once more, into a list that
+// is cut to its `top` largest whenever it is full.  All threads of the block.
+template <typename T>
+__device__ __noinline__ void collect_again(Shared& sh, const uint4* body, uint32_t head, uint32_t v0,
+                                           uint32_t v1, Extra extra, uint64_t bound, int top) {
+  constexpr int N = Vec<T>::N;
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (t == 0) sh.count = 0;
+  __syncthreads();
+  for (uint32_t base = v0; base < v1 + kThreads; base += kThreads) {
+    // one vector a thread; past the last ones, the extra elements
+    uint64_t key[N];
+    const uint32_t v = base + t;
+    float u[N];
+    if (v < v1) Vec<T>::unpack(ld_param(body + v), u);
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      key[i] = v < v1 && u[i] == u[i] ? key_of(u[i], head + v * N + i) : 0;
+    if (base >= v1) key[0] = extra.at != 0xFFFFFFFFu && extra.x == extra.x ? key_of(extra.x, extra.at) : 0;
+    bool left = true;
+    for (;;) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < N; i++) n += left && key[i] > bound;
+      bool kept = true;
+      if (n > 0) {
+        int at = atomicAdd(&sh.count, n);
+        kept = at + n <= kList;
+        if (kept) {
+#pragma unroll
+          for (int i = 0; i < N; i++)
+            if (key[i] > bound) sh.list[at++] = key[i];
+        } else {
+          for (int i = at; i < kList && i < at + n; i++) sh.list[i] = 0;
+        }
+      }
+      if (kept) left = false;
+      if (!__syncthreads_or(!kept)) break;
+      if (t < kWarp) {
+        take_largest(sh.list, kList, top, sh.best);
+        for (int i = t; i < top; i += kWarp) sh.list[i] = sh.best[i];
+        if (t == 0) sh.count = top, sh.bound = sh.best[top - 1];
+      }
+      __syncthreads();
+      bound = sh.bound;
+    }
+  }
+}
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(const LogprobArgs a) {
@@ -182,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(c
   const uint32_t v0 = min(rank * per, part.vecs), v1 = min(v0 + per, part.vecs);
   const float c = kLog2e * a.inv_t;
   if (TOP) {
-    if (t == 0) sh.count = 0, sh.bound = 0;
+    if (t == 0) sh.count = 0, sh.lost = 0;
     __syncthreads();
   }
   pdl_enter();  // before any global read: the previous kernel may still run
@@ -216,39 +393,15 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(c
   Stats s{-kInf, 0.0f, 0.0f};
   uint64_t bound = 0;      // keys above it are candidates
   float bound_v = -kInf;   // its value
-  // Offers candidates: count(bound) of this thread's, emit(bound, place) writes them.
-  auto offer = [&](float top, auto&& count, auto&& emit) {
-    int n = top >= bound_v ? count(bound) : 0;
-    for (;;) {
-      bool kept = true;
-      if (n > 0) {
-        const int at = atomicAdd(&sh.count, n);
-        kept = at + n <= kList;
-        if (kept)
-          emit(bound, at);
-        else
-          for (int i = at; i < kList && i < at + n; i++) sh.list[i] = 0;
-      }
-      if (!__syncthreads_or(!kept)) break;
-      if (t < kWarp) {
-        take_largest(sh.list, kList, a.top, sh.best);
-        for (int i = t; i < a.top; i += kWarp) sh.list[i] = sh.best[i];
-        if (t == 0) sh.count = a.top, sh.bound = sh.best[a.top - 1];
-      }
-      __syncthreads();
-      bound = sh.bound;
-      bound_v = bound ? value_of(static_cast<uint32_t>(bound >> 32)) : -kInf;
-      n = kept ? 0 : count(bound);
-    }
-  };
-
   bool first = true;
   for (uint32_t base = v0; base < v1; base += kChunk) {
     uint4 raw[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; j++) raw[j] = next[j];
     if (base + kChunk < v1) load(base + kChunk);
-    const float top = top_of(raw, T{});
+    float tops[kUnroll], top = -kInf;
+#pragma unroll
+    for (int j = 0; j < kUnroll; j++) tops[j] = top_of<T>(raw[j]), top = fmaxf(top, tops[j]);
     if (top > s.m) {
       const float d = fmaxf(s.m - top, -1e30f), f = exp2_fast(d * c);
       s.e = fmaf(s.l, d, s.e) * f;
@@ -285,66 +438,43 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(c
     s.e += lo + hi;
     if (TOP) {
       if (first) {
-        // the k-th largest of the threads' maxima
+        // the k-th largest of the threads' maxima, its leading bits
         first = false;
         sh.maxima[t] = ordered(top);
         __syncthreads();
-        if (t < kWarp) {
-          uint32_t have[kThreads / kWarp];
+        uint32_t have[kThreads / kWarp];
 #pragma unroll
-          for (int i = 0; i < kThreads / kWarp; i++) have[i] = sh.maxima[i * kWarp + t];
-          uint32_t kth = 0;
-          for (int r = 0; r < a.top; r++) {
-            uint32_t best = 0;
+        for (int i = 0; i < kThreads / kWarp; i++) have[i] = sh.maxima[i * kWarp + t % kWarp];
+        const uint32_t kth = kth_bound<16>(
+            [&](auto&& f) {
 #pragma unroll
-            for (int i = 0; i < kThreads / kWarp; i++) best = max(best, have[i]);
-            kth = __reduce_max_sync(0xFFFFFFFFu, best);
-            const bool winner = t == __ffs(__ballot_sync(0xFFFFFFFFu, best == kth)) - 1;
-            bool gone = !winner;
-#pragma unroll
-            for (int i = 0; i < kThreads / kWarp; i++)
-              if (!gone && have[i] == kth) have[i] = 0, gone = true;
-          }
-          if (t == 0) sh.bound = static_cast<uint64_t>(kth) << 32;
+              for (int i = 0; i < kThreads / kWarp; i++) f(have[i]);
+            },
+            a.top);
+        if (kth > ordered(-kInf)) {
+          bound = static_cast<uint64_t>(kth) << 32;
+          bound_v = value_of(kth);
         }
-        __syncthreads();
-        bound = sh.bound;
-        bound_v = bound ? value_of(static_cast<uint32_t>(bound >> 32)) : -kInf;
       }
-      auto each = [&](auto&& f) {
+      if (top >= bound_v) {
 #pragma unroll
         for (int j = 0; j < kUnroll; j++) {
           const uint32_t v = base + t + j * kThreads;
-          if (v >= v1) continue;
-          float u[N];
-          Vec<T>::unpack(raw[j], u);
-#pragma unroll
-          for (int i = 0; i < N; i++)
-            if (u[i] >= bound_v) f(key_of(u[i], part.head + v * N + i));
+          if (v >= v1 || tops[j] < bound_v) continue;
+          // (nothing more is worth noting once one had no room)
+          if (*static_cast<volatile int*>(&sh.lost)) continue;
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kList)
+            sh.list[at] = static_cast<uint64_t>(ordered(tops[j])) << 32 | v;
+          else
+            sh.lost = 1;
         }
-      };
-      offer(
-          top,
-          [&](uint64_t b) {
-            int n = 0;
-            each([&](uint64_t k) { n += k > b; });
-            return n;
-          },
-          [&](uint64_t b, int at) {
-            each([&](uint64_t k) {
-              if (k > b) sh.list[at++] = k;
-            });
-          });
+      }
     }
   }
   if (rank == 0 && (part.head | part.tail)) {
     if (extra_at < a.vocab) s = join(s, Stats{extra, extra == -kInf ? 0.0f : 1.0f, 0.0f}, c);
     if (!(extra < kInf)) s.l = extra - extra;  // a NaN or +inf: no probabilities
-    if (TOP) {
-      const uint64_t k = extra_at < a.vocab && extra == extra ? key_of(extra, extra_at) : 0;
-      offer(k ? extra : -kInf, [&](uint64_t b) { return k > b ? 1 : 0; },
-            [&](uint64_t, int at) { sh.list[at] = k; });
-    }
   }
 
   // the block's statistics, in a fixed order
@@ -356,10 +486,17 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(c
   }
   if (t % kWarp == 0) sh.stats[t / kWarp] = s;
   __syncthreads();
+  if (TOP) {
+    if (t < kWarp && !sh.lost)
+      read_noted<T>(sh, body, part.head, Extra{extra, extra_at}, a.top);
+    __syncthreads();
+    if (sh.lost)
+      collect_again<T>(sh, body, part.head, v0, v1, Extra{extra, extra_at}, bound, a.top);
+  }
   if (t < kWarp) {
     s = sh.stats[0];
     for (int i = 1; i < kThreads / kWarp; i++) s = join(s, sh.stats[i], c);
-    if (TOP) take_largest(sh.list, min(sh.count, kList), a.top, sh.best);
+    if (TOP && sh.lost) take_largest(sh.list, min(sh.count, kList), a.top, sh.best);
     if (t == 0) sh.total = s;
   }
   if (ranks > 1) {
