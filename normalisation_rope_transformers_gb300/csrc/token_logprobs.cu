@@ -346,7 +346,7 @@ __device__ __noinline__ void collect_again(Shared& sh, const uint4* body, uint32
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const LogprobArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ Shared sh;
   const int t = threadIdx.x;
