@@ -3,7 +3,7 @@
 //
 // An item is a block of up to R query rows of one sequence and K/V head (row t * group + i
 // is query token t, the i-th of the head's query heads); its work is counted in tiles of
-// kAttnTile positions.  All items' tiles, in order of (sequence, head, row block, tile),
+// TILE positions.  All items' tiles, in order of (sequence, head, row block, tile),
 // are cut into equal shares, one a block: lengths are known on the device alone, and long
 // sequences are split while short ones share a block.  A block meets at most one item that
 // began before its share and one that ends behind it; their partial results go to the
@@ -14,7 +14,6 @@
 
 namespace nr {
 
-constexpr int kAttnTile = 64;  // positions
 constexpr int kAttnMostPositions = 1 << 30;
 constexpr float kAttnLog2e = 1.4426950408889634f;
 constexpr float kAttnLn2 = 0.6931471805599453f;
@@ -46,6 +45,7 @@ struct AttnArgs {
 
 // One sequence's queries and lengths, clamped to what is there: the tables are data that the
 // host does not see.
+template <int TILE>
 struct AttnSeq {
   int first;     // its first query token
   int queries;   // T
@@ -64,14 +64,14 @@ struct AttnSeq {
     context = length - queries;
     const int64_t reach = a.width * a.geo.block_size;
     const int n = reach < length ? static_cast<int>(reach) : length;
-    tiles = max(1, (n + kAttnTile - 1) / kAttnTile);  // an item without positions writes zeros
+    tiles = max(1, (n + TILE - 1) / TILE);  // an item without positions writes zeros
   }
 };
 
 // R rows an item: row blocks of a sequence.
 template <int R>
-__device__ __forceinline__ int64_t row_blocks(const AttnArgs& a, const AttnSeq& s) {
-  return (static_cast<int64_t>(s.queries) * a.group.div + R - 1) / R;
+__device__ __forceinline__ int64_t row_blocks(const AttnArgs& a, int queries) {
+  return (static_cast<int64_t>(queries) * a.group.div + R - 1) / R;
 }
 
 // Where in the order of all tiles each thread's sequences begin; shared by the block.
@@ -81,7 +81,7 @@ struct AttnPlan {
   int64_t warp[THREADS / kWarp];
 };
 
-template <int R, int THREADS>
+template <int R, int TILE, int THREADS>
 __device__ __forceinline__ void make_plan(const AttnArgs& a, AttnPlan<THREADS>& plan) {
   const int t = threadIdx.x, lane = t % kWarp;
   const int per = (a.seqs + THREADS - 1) / THREADS;
@@ -89,8 +89,8 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, AttnPlan<THREADS>& 
   for (int i = 0; i < per; i++) {
     const int64_t s = static_cast<int64_t>(t) * per + i;
     if (s >= a.seqs) break;
-    const AttnSeq q(a, static_cast<int>(s));
-    n += row_blocks<R>(a, q) * a.heads * q.tiles;
+    const AttnSeq<TILE> q(a, static_cast<int>(s));
+    n += row_blocks<R>(a, q.queries) * a.heads * q.tiles;
   }
 #pragma unroll
   for (int d = 1; d < kWarp; d <<= 1) {
@@ -115,7 +115,7 @@ struct AttnItem {
   int seq, head, rb, tile;
 };
 
-template <int R, int THREADS>
+template <int R, int TILE, int THREADS>
 __device__ __forceinline__ AttnItem locate(const AttnArgs& a, const AttnPlan<THREADS>& plan,
                                            int64_t unit) {
   int lo = 0, hi = THREADS;  // at[lo] <= unit < at[hi]
@@ -128,8 +128,8 @@ __device__ __forceinline__ AttnItem locate(const AttnArgs& a, const AttnPlan<THR
   int s = lo * per;
   int64_t left = unit - plan.at[lo];
   for (;; s++) {
-    const AttnSeq q(a, s);
-    const int64_t rbs = row_blocks<R>(a, q), n = rbs * a.heads * q.tiles;
+    const AttnSeq<TILE> q(a, s);
+    const int64_t rbs = row_blocks<R>(a, q.queries), n = rbs * a.heads * q.tiles;
     if (left < n) {
       const int64_t item = left / q.tiles;
       const int h = static_cast<int>(item / rbs);
@@ -140,6 +140,18 @@ __device__ __forceinline__ AttnItem locate(const AttnArgs& a, const AttnPlan<THR
   }
 }
 
+// The item behind `it` in the order (there is one).
+template <int R, int TILE>
+__device__ __forceinline__ void next_item(const AttnArgs& a, AttnItem& it, int queries) {
+  it.tile = 0;
+  if (++it.rb < row_blocks<R>(a, queries)) return;
+  it.rb = 0;
+  if (++it.head < a.heads) return;
+  it.head = 0;
+  do it.seq++;
+  while (AttnSeq<TILE>(a, it.seq).queries == 0);
+}
+
 __device__ __forceinline__ float attn_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -147,7 +159,8 @@ __device__ __forceinline__ float attn_exp2(float x) {
 }
 
 // Whether query token t (row `token` of q) of a sequence sees position p < length.
-__device__ __forceinline__ bool attn_sees(const AttnArgs& a, const AttnSeq& s, int t, int p) {
+template <int TILE>
+__device__ __forceinline__ bool attn_sees(const AttnArgs& a, const AttnSeq<TILE>& s, int t, int p) {
   const int j = p - s.context;
   if (j < 0) return true;
   if (a.tree == nullptr) return j <= t;
@@ -186,5 +199,125 @@ __device__ __forceinline__ float2 floats_of_half2(uint32_t h) {
       : "r"(h));
   return v;
 }
+
+constexpr int kScaleUp = 13;  // MXFP4 values are held times 2^13
+
+// The scale bytes of one token and head: f16 multipliers relative to the largest (a NaN scale
+// stays a NaN), times 2^kScaleUp; the largest as f32 without that factor.
+template <int G>
+__device__ __forceinline__ float mx_multipliers(uint64_t bytes, uint16_t (&m)[G]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < G; i++) {
+    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
+    if (b != 255u) top = max(top, b);
+  }
+#pragma unroll
+  for (int i = 0; i < G; i++) {
+    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
+    const int e = static_cast<int>(b) - static_cast<int>(top) + kScaleUp;  // 2^e
+    m[i] = static_cast<uint16_t>(b == 255u ? 0x7E00
+                                 : e >= -14 ? (e + 15) << 10
+                                 : e >= -24 ? 1 << (e + 24)
+                                            : 0);
+  }
+  // 2^(top - 127 - kScaleUp); below 2^-126: nothing that f32 scores would see
+  const int e = static_cast<int>(top) - kScaleUp;
+  return e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
+}
+
+// The power of two at or above a finite scale, between 2^-100 and 2^127; 0 for others.
+__device__ __forceinline__ float scale_reference(float s) {
+  if (!(s > 0.0f && s <= kScaleCeil)) return 0.0f;
+  const uint32_t up = (__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u;
+  return __uint_as_float(min(max(up, 27u << 23), 254u << 23));
+}
+// Its reciprocal, of 0: 0.
+__device__ __forceinline__ float power_reciprocal(float p) {
+  return p == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(p));
+}
+
+template <typename T>
+__device__ __forceinline__ T narrow(float x) {
+  return static_cast<T>(x);
+}
+
+namespace {
+
+// Joins the parts of the items that more than one share worked on: block (i, y) the item that
+// begins in share i, rows y, y + gridDim.y, ...
+template <typename T, int R, int DIM>
+__global__ void __launch_bounds__(DIM / 4) cache_attention_join_kernel(const AttnArgs a) {
+  pdl_enter();
+  const int4 join = a.joins[blockIdx.x];
+  if (join.w == 0) return;
+  const AttnSeq<1> seq(a, join.x);
+  const int rows =
+      min(seq.queries * static_cast<int>(a.group.div) - join.z * R, R);
+  constexpr int64_t kPart = R * (DIM + 2);
+  const float* first = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + 1) * kPart;
+  const float* rest = first + kPart;  // share i + 1's first part, and every second one behind it
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * 2 * kPart; };
+    float top = -__builtin_huge_valf();
+    for (int i = 0; i < join.w; i++) top = fmaxf(top, part(i)[R * DIM + 2 * r]);
+    float sum = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < join.w; i++) {
+      const float m = part(i)[R * DIM + 2 * r], l = part(i)[R * DIM + 2 * r + 1];
+      if (l == 0.0f) continue;
+      const float f = attn_exp2(m - top);
+      const float4 y = *reinterpret_cast<const float4*>(part(i) + r * DIM + 4 * threadIdx.x);
+      sum = fmaf(l, f, sum);
+      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y);
+      x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+    }
+    const int row = join.z * R + r;
+    const int tok = a.group.quot(row), i_head = row - tok * a.group.div;
+    const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
+                         join.y * a.group.div + i_head;
+    const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+    T* out = static_cast<T*>(a.out) + head * DIM + 4 * threadIdx.x;
+    out[0] = narrow<T>(x.x * inv);
+    out[1] = narrow<T>(x.y * inv);
+    out[2] = narrow<T>(x.z * inv);
+    out[3] = narrow<T>(x.w * inv);
+    if (threadIdx.x == 0 && a.lse != nullptr)
+      a.lse[head] = sum != 0.0f ? (top + log2f(sum)) * kAttnLn2 : -__builtin_huge_valf();
+  }
+}
+
+// Shared memory of a kernel, once a device: the opt-in to more than 48 KB, and the largest share
+// of the SM's memory.  Without the latter an SM that the join ran on with a small share has no room
+// for all blocks of the next call, which then runs in two waves (400009 tokens, calls back to back:
+// 428 us, calls apart 272 us).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (done[device].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done[device].store(1, std::memory_order_relaxed);
+  return e;
+}
+
+// Room for the joins of `shares` shares of R rows: 16 bytes a share, then two parts each.
+constexpr int64_t attn_joins_bytes(int64_t shares) { return (shares * 16 + 127) / 128 * 128; }
+constexpr int64_t attn_bytes(int64_t shares, int64_t rows, int64_t dim) {
+  return attn_joins_bytes(shares) + 2 * shares * rows * (dim + 2) * 4;
+}
+
+}  // namespace
+
+// Many rows an item, bf16 tensors, heads of 64 or 128 (cache_attention_rows.cu).
+int64_t attn_rows_bytes(int64_t head_dim);
+cudaError_t launch_attn_rows(const AttnArgs& a, bool fp4, int64_t head_dim, void* workspace,
+                             cudaStream_t stream);
 
 }  // namespace nr

@@ -31,7 +31,7 @@ constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
 constexpr int kAttnRows = 16;
 constexpr int kStep = 16;          // positions a warp handles at a time
-constexpr int kScaleUp = 13;       // MXFP4 values are held times 2^13
+constexpr int kAttnTile = kStep * kAttnWarps;  // positions of a block's step
 constexpr float kWeightUp = 16384.0f;  // weights are held times 2^14
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -91,41 +91,6 @@ struct Layout {
   }
 };
 
-// The scale bytes of one token and head: f16 multipliers relative to the largest (a NaN scale
-// stays a NaN), times 2^kScaleUp; the largest as f32 without that factor.
-template <int G>
-__device__ __forceinline__ float mx_multipliers(uint64_t bytes, uint16_t (&m)[G]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < G; i++) {
-    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
-    if (b != 255u) top = max(top, b);
-  }
-#pragma unroll
-  for (int i = 0; i < G; i++) {
-    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
-    const int e = static_cast<int>(b) - static_cast<int>(top) + kScaleUp;  // 2^e
-    m[i] = static_cast<uint16_t>(b == 255u ? 0x7E00
-                                 : e >= -14 ? (e + 15) << 10
-                                 : e >= -24 ? 1 << (e + 24)
-                                            : 0);
-  }
-  // 2^(top - 127 - kScaleUp); below 2^-126: nothing that f32 scores would see
-  const int e = static_cast<int>(top) - kScaleUp;
-  return e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
-}
-
-// The power of two at or above a finite scale, between 2^-100 and 2^127; 0 for others.
-__device__ __forceinline__ float scale_reference(float s) {
-  if (!(s > 0.0f && s <= kScaleCeil)) return 0.0f;
-  const uint32_t up = (__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u;
-  return __uint_as_float(min(max(up, 27u << 23), 254u << 23));
-}
-// Its reciprocal, of 0: 0.
-__device__ __forceinline__ float power_reciprocal(float p) {
-  return p == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(p));
-}
-
 template <typename T, bool FP4, int DIM>
 struct AttnShared {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
@@ -143,11 +108,6 @@ struct AttnShared {
   AttnPlan<kAttnThreads> plan;
 };
 
-template <typename T>
-__device__ __forceinline__ T narrow(float x) {
-  return static_cast<T>(x);
-}
-
 template <typename T, bool FP4, int DIM>
 __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
     cache_attention_kernel(const AttnArgs a) {
@@ -157,17 +117,17 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
   auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM>*>(smem_raw);
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp, g = lane / 4, c = lane % 4;
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<kAttnRows>(a, sh.plan);
+  make_plan<kAttnRows, kAttnTile>(a, sh.plan);
   const int64_t total = sh.plan.at[kAttnThreads];
   const int64_t share = share_size(total, gridDim.x);
   int64_t unit = blockIdx.x * share;
   const int64_t end = min(unit + share, total);
   if (t == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (unit >= end) return;
-  AttnItem it = locate<kAttnRows>(a, sh.plan, unit);
+  AttnItem it = locate<kAttnRows, kAttnTile>(a, sh.plan, unit);
 
   while (unit < end) {
-    const AttnSeq seq(a, it.seq);
+    const AttnSeq<kAttnTile> seq(a, it.seq);
     const int rows_left = seq.queries * static_cast<int>(a.group.div) - it.rb * kAttnRows;
     const int rows = min(rows_left, kAttnRows);
     const int steps = static_cast<int>(min(static_cast<int64_t>(seq.tiles - it.tile), end - unit));
@@ -613,85 +573,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
 
     unit += steps;
     if (unit >= end) break;
-    it.tile = 0;
-    if (++it.rb == row_blocks<kAttnRows>(a, seq)) {
-      it.rb = 0;
-      if (++it.head == a.heads) {
-        it.head = 0;
-        do it.seq++;
-        while (AttnSeq(a, it.seq).queries == 0);
-      }
-    }
+    next_item<kAttnRows, kAttnTile>(a, it, seq.queries);
   }
-}
-
-// Joins the parts of the items that more than one share worked on: block (i, y) the item that
-// begins in share i, rows y, y + gridDim.y, ...
-template <typename T, int DIM>
-__global__ void __launch_bounds__(DIM / 4) cache_attention_join_kernel(const AttnArgs a) {
-  pdl_enter();
-  const int4 join = a.joins[blockIdx.x];
-  if (join.w == 0) return;
-  const AttnSeq seq(a, join.x);
-  const int rows =
-      min(seq.queries * static_cast<int>(a.group.div) - join.z * kAttnRows, kAttnRows);
-  constexpr int64_t kPart = kAttnRows * (DIM + 2);
-  const float* first = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + 1) * kPart;
-  const float* rest = first + kPart;  // share i + 1's first part, and every second one behind it
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * 2 * kPart; };
-    float top = -__builtin_huge_valf();
-    for (int i = 0; i < join.w; i++) top = fmaxf(top, part(i)[kAttnRows * DIM + 2 * r]);
-    float sum = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < join.w; i++) {
-      const float m = part(i)[kAttnRows * DIM + 2 * r], l = part(i)[kAttnRows * DIM + 2 * r + 1];
-      if (l == 0.0f) continue;
-      const float f = attn_exp2(m - top);
-      const float4 y = *reinterpret_cast<const float4*>(part(i) + r * DIM + 4 * threadIdx.x);
-      sum = fmaf(l, f, sum);
-      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y);
-      x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-    }
-    const int row = join.z * kAttnRows + r;
-    const int tok = a.group.quot(row), i_head = row - tok * a.group.div;
-    const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
-                         join.y * a.group.div + i_head;
-    const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-    T* out = static_cast<T*>(a.out) + head * DIM + 4 * threadIdx.x;
-    out[0] = narrow<T>(x.x * inv);
-    out[1] = narrow<T>(x.y * inv);
-    out[2] = narrow<T>(x.z * inv);
-    out[3] = narrow<T>(x.w * inv);
-    if (threadIdx.x == 0 && a.lse != nullptr)
-      a.lse[head] = sum != 0.0f ? (top + log2f(sum)) * kAttnLn2 : -__builtin_huge_valf();
-  }
-}
-
-template <int DIM>
-int64_t attn_need() {
-  constexpr int64_t shares = kSms * attn_blocks<DIM>;
-  return (shares * 16 + 127) / 128 * 128 + 2 * shares * kAttnRows * (DIM + 2) * 4;
-}
-
-// The opt-in to more than 48 KB of shared memory, once a kernel and device.  Both kernels ask
-// for the largest share of the SM's memory: an SM that the join ran on with a small one has no
-// room for all blocks of the next call, which then runs in two waves ([400009 tokens] calls back to back
-// took 428 us, calls apart 272 us).
-template <typename Kernel>
-cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
-  if (done[device].load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(bytes));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) done[device].store(1, std::memory_order_relaxed);
-  return e;
 }
 
 template <typename T, bool FP4, int DIM>
@@ -700,16 +583,16 @@ cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr unsigned shares = kSms * attn_blocks<DIM>;
   static std::atomic<int> done[64], done_join[64];
   cudaError_t e = allow_shared(cache_attention_kernel<T, FP4, DIM>, shared, done);
-  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, DIM>, 0, done_join);
+  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, kAttnRows, DIM>, 0, done_join);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
-                                       (shares * 16 + 127) / 128 * 128);
+                                       attn_joins_bytes(shares));
   e = launch_pdl(cache_attention_kernel<T, FP4, DIM>, dim3(shares), dim3(kAttnThreads), shared, s,
                  a);
   if (e != cudaSuccess) return e;
   const unsigned y = a.group.div < 4 ? 4 : 8;
-  return launch_pdl(cache_attention_join_kernel<T, DIM>, dim3(shares, y), dim3(DIM / 4), 0, s, a);
+  return launch_pdl(cache_attention_join_kernel<T, kAttnRows, DIM>, dim3(shares, y), dim3(DIM / 4), 0, s, a);
 }
 
 template <typename T, bool FP4>
@@ -751,12 +634,17 @@ AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
 }  // namespace
 
 int64_t cache_attention_workspace(int64_t head_dim) {
-  return head_dim == 64 ? attn_need<64>() : head_dim == 128 ? attn_need<128>() : attn_need<256>();
+  const int64_t shares = kSms * (head_dim == 256 ? attn_blocks<256> : attn_blocks<128>);
+  const int64_t few = attn_bytes(shares, kAttnRows, head_dim), many = attn_rows_bytes(head_dim);
+  return few > many ? few : many;
 }
 
 cudaError_t launch_cache_attention(const KvCacheArgs& c, const CacheAttentionArgs& p, int is_bf16,
                                    cudaStream_t stream) {
   const AttnArgs a = attn_args(c, p);
+  // More than 16 rows an item on average: the kernel whose tile of products has 128.
+  if (is_bf16 && c.head_dim <= 128 && p.tokens * (p.q_heads / c.heads) > kAttnRows * p.seqs)
+    return launch_attn_rows(a, c.fp4, c.head_dim, p.workspace, stream);
   if (is_bf16)
     return c.fp4 ? attn_dim<__nv_bfloat16, true>(c.head_dim, a, p.workspace, stream)
                  : attn_dim<__nv_bfloat16, false>(c.head_dim, a, p.workspace, stream);

@@ -225,6 +225,7 @@ cudaError_t launch_token_logprobs_backward(void* dlogits, const float* dlogprob,
 // Device status word: bits set by kernels whose bounded waits ran out.
 constexpr unsigned kStatusBitQkBulkWait = 1u;
 constexpr unsigned kStatusBitProbeWait = 2u;
+constexpr unsigned kStatusBitAttnWait = 4u;
 
 // Device address of the current device's status word (status.cu), looked up
 // once per device.  Kernels that bound a wait take it as an argument.
