@@ -3,9 +3,10 @@
 //
 // An item is a block of up to R query rows of one sequence and K/V head (row t * group + i
 // is query token t, the i-th of the head's query heads); its work is counted in tiles of
-// TILE positions.  All items' tiles, in order of (sequence, head, row block, tile),
+// TILE positions, behind COST units for what an item costs besides them (its queries, the start
+// of its loads, its result).  All items' units, in order of (sequence, head, row block, tile),
 // are cut into equal shares, one a block: lengths are known on the device alone, and long
-// sequences are split while short ones share a block.  A block meets at most one item that
+// sequences are split while short ones share a block.  A tile belongs to the share that its unit is in.  A block meets at most one item that
 // began before its share and one that ends behind it; their partial results go to the
 // workspace and a second kernel joins them, in the order of the shares.
 #pragma once
@@ -81,7 +82,7 @@ struct AttnPlan {
   int64_t warp[THREADS / kWarp];
 };
 
-template <int R, int TILE, int THREADS>
+template <int R, int TILE, int COST, int THREADS>
 __device__ __forceinline__ void make_plan(const AttnArgs& a, AttnPlan<THREADS>& plan) {
   const int t = threadIdx.x, lane = t % kWarp;
   const int per = (a.seqs + THREADS - 1) / THREADS;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs& a, AttnPlan<THREADS>& 
     const int64_t s = static_cast<int64_t>(t) * per + i;
     if (s >= a.seqs) break;
     const AttnSeq<TILE> q(a, static_cast<int>(s));
-    n += row_blocks<R>(a, q.queries) * a.heads * q.tiles;
+    n += row_blocks<R>(a, q.queries) * a.heads * (q.tiles + COST);
   }
 #pragma unroll
   for (int d = 1; d < kWarp; d <<= 1) {
@@ -115,9 +116,10 @@ struct AttnItem {
   int seq, head, rb, tile;
 };
 
-template <int R, int TILE, int THREADS>
+// The first tile at or behind `unit` (moved on to that tile's).
+template <int R, int TILE, int COST, int THREADS>
 __device__ __forceinline__ AttnItem locate(const AttnArgs& a, const AttnPlan<THREADS>& plan,
-                                           int64_t unit) {
+                                           int64_t& unit) {
   int lo = 0, hi = THREADS;  // at[lo] <= unit < at[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -129,18 +131,19 @@ __device__ __forceinline__ AttnItem locate(const AttnArgs& a, const AttnPlan<THR
   int64_t left = unit - plan.at[lo];
   for (;; s++) {
     const AttnSeq<TILE> q(a, s);
-    const int64_t rbs = row_blocks<R>(a, q.queries), n = rbs * a.heads * q.tiles;
+    const int64_t rbs = row_blocks<R>(a, q.queries), each = q.tiles + COST, n = rbs * a.heads * each;
     if (left < n) {
-      const int64_t item = left / q.tiles;
+      const int64_t item = left / each;
       const int h = static_cast<int>(item / rbs);
-      return AttnItem{s, h, static_cast<int>(item - h * rbs),
-                      static_cast<int>(left - item * q.tiles)};
+      const int off = static_cast<int>(left - item * each) - COST;
+      if (off < 0) unit -= off;
+      return AttnItem{s, h, static_cast<int>(item - h * rbs), off < 0 ? 0 : off};
     }
     left -= n;
   }
 }
 
-// The item behind `it` in the order (there is one).
+// The first tile of the item behind `it` in the order (there is one).
 template <int R, int TILE>
 __device__ __forceinline__ void next_item(const AttnArgs& a, AttnItem& it, int queries) {
   it.tile = 0;
@@ -244,47 +247,68 @@ __device__ __forceinline__ T narrow(float x) {
 
 namespace {
 
-// Joins the parts of the items that more than one share worked on: block (i, y) the item that
-// begins in share i, rows y, y + gridDim.y, ...
+// Joins the parts of the items that more than one share worked on: block (i, y) rows
+// kJoinRows y + threadIdx.y of the item that begins in share i, four dimensions a thread.
+constexpr int kJoinRows = 4;
 template <typename T, int R, int DIM>
-__global__ void __launch_bounds__(DIM / 4) cache_attention_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(DIM / 4 * kJoinRows) cache_attention_join_kernel(const AttnArgs a) {
   pdl_enter();
   const int4 join = a.joins[blockIdx.x];
   if (join.w == 0) return;
   const AttnSeq<1> seq(a, join.x);
-  const int rows =
-      min(seq.queries * static_cast<int>(a.group.div) - join.z * R, R);
+  const int r = blockIdx.y * kJoinRows + threadIdx.y;
+  const int row = join.z * R + r;
+  if (row >= seq.queries * static_cast<int>(a.group.div)) return;
   constexpr int64_t kPart = R * (DIM + 2);
   const float* first = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + 1) * kPart;
   const float* rest = first + kPart;  // share i + 1's first part, and every second one behind it
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * 2 * kPart; };
-    float top = -__builtin_huge_valf();
-    for (int i = 0; i < join.w; i++) top = fmaxf(top, part(i)[R * DIM + 2 * r]);
-    float sum = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < join.w; i++) {
-      const float m = part(i)[R * DIM + 2 * r], l = part(i)[R * DIM + 2 * r + 1];
-      if (l == 0.0f) continue;
-      const float f = attn_exp2(m - top);
-      const float4 y = *reinterpret_cast<const float4*>(part(i) + r * DIM + 4 * threadIdx.x);
-      sum = fmaf(l, f, sum);
-      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y);
-      x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+  auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * 2 * kPart; };
+  // Some parts' sums and values at a time, on their way together.
+  constexpr int kAtOnce = 8;
+  float top = -__builtin_huge_valf(), sum = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int base = 0; base < join.w; base += kAtOnce) {
+    float2 ml[kAtOnce];
+    float4 y[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; i++) {
+      const bool in = base + i < join.w;
+      const float* p = part(in ? base + i : 0);
+      ml[i] = in ? *reinterpret_cast<const float2*>(p + R * DIM + 2 * r)
+                 : make_float2(-__builtin_huge_valf(), 0.0f);
+      y[i] = in ? *reinterpret_cast<const float4*>(p + r * DIM + 4 * threadIdx.x)
+                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    const int row = join.z * R + r;
-    const int tok = a.group.quot(row), i_head = row - tok * a.group.div;
-    const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
-                         join.y * a.group.div + i_head;
-    const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-    T* out = static_cast<T*>(a.out) + head * DIM + 4 * threadIdx.x;
-    out[0] = narrow<T>(x.x * inv);
-    out[1] = narrow<T>(x.y * inv);
-    out[2] = narrow<T>(x.z * inv);
-    out[3] = narrow<T>(x.w * inv);
-    if (threadIdx.x == 0 && a.lse != nullptr)
-      a.lse[head] = sum != 0.0f ? (top + log2f(sum)) * kAttnLn2 : -__builtin_huge_valf();
+    float to = top;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; i++) to = fmaxf(to, ml[i].x);
+    if (top != -__builtin_huge_valf()) {
+      const float f = attn_exp2(top - to);
+      sum *= f;
+      x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+    }
+    top = to;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; i++) {
+      if (ml[i].y == 0.0f) continue;
+      const float f = attn_exp2(ml[i].x - top);
+      sum = fmaf(ml[i].y, f, sum);
+      x.x = fmaf(y[i].x, f, x.x), x.y = fmaf(y[i].y, f, x.y);
+      x.z = fmaf(y[i].z, f, x.z), x.w = fmaf(y[i].w, f, x.w);
+    }
   }
+  const int tok = a.group.quot(row), i_head = row - tok * a.group.div;
+  const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
+                       join.y * a.group.div + i_head;
+  const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+  T* out = static_cast<T*>(a.out) + head * DIM + 4 * threadIdx.x;
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+  else
+    *reinterpret_cast<float4*>(out) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  if (threadIdx.x == 0 && a.lse != nullptr)
+    a.lse[head] = sum != 0.0f ? (top + log2f(sum)) * kAttnLn2 : -__builtin_huge_valf();
 }
 
 // Shared memory of a kernel, once a device: the opt-in to more than 48 KB, and the largest share

@@ -32,6 +32,7 @@ constexpr int kAttnWarps = kAttnThreads / kWarp;
 constexpr int kAttnRows = 16;
 constexpr int kStep = 16;          // positions a warp handles at a time
 constexpr int kAttnTile = kStep * kAttnWarps;  // positions of a block's step
+constexpr int kItemCost = 3;  // tiles that an item costs besides its own
 constexpr float kWeightUp = 16384.0f;  // weights are held times 2^14
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -117,14 +118,14 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
   auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM>*>(smem_raw);
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp, g = lane / 4, c = lane % 4;
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<kAttnRows, kAttnTile>(a, sh.plan);
+  make_plan<kAttnRows, kAttnTile, kItemCost>(a, sh.plan);
   const int64_t total = sh.plan.at[kAttnThreads];
   const int64_t share = share_size(total, gridDim.x);
   int64_t unit = blockIdx.x * share;
   const int64_t end = min(unit + share, total);
   if (t == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (unit >= end) return;
-  AttnItem it = locate<kAttnRows, kAttnTile>(a, sh.plan, unit);
+  AttnItem it = locate<kAttnRows, kAttnTile, kItemCost>(a, sh.plan, unit);
 
   while (unit < end) {
     const AttnSeq<kAttnTile> seq(a, it.seq);
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
     }
     __syncthreads();  // the shared memory is written anew
 
-    unit += steps;
+    unit += steps + kItemCost;
     if (unit >= end) break;
     next_item<kAttnRows, kAttnTile>(a, it, seq.queries);
   }
@@ -591,8 +592,8 @@ cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   e = launch_pdl(cache_attention_kernel<T, FP4, DIM>, dim3(shares), dim3(kAttnThreads), shared, s,
                  a);
   if (e != cudaSuccess) return e;
-  const unsigned y = a.group.div < 4 ? 4 : 8;
-  return launch_pdl(cache_attention_join_kernel<T, kAttnRows, DIM>, dim3(shares, y), dim3(DIM / 4), 0, s, a);
+  return launch_pdl(cache_attention_join_kernel<T, kAttnRows, DIM>,
+                    dim3(shares, kAttnRows / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
 }
 
 template <typename T, bool FP4>

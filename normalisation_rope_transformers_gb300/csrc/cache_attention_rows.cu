@@ -28,6 +28,7 @@ constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kRowsThreads = (kMmaWarp + 1) * kWarp;
 constexpr int kRowsShares = 152;   // one block an SM
 constexpr int kPer = kPos / kLoadWarps;  // positions a loading warp
+constexpr int kItemCost = 8;       // tiles that an item costs besides its own
 constexpr int kMeta = 4;           // tiles whose scales are kept
 constexpr int kItems = 8;          // items whose row scales are kept
 constexpr float kHeadroom = 8.0f;  // a score may exceed the reference by 2^8
@@ -152,6 +153,160 @@ struct RowsShared {
   AttnPlan<kRowsThreads> plan;
 };
 
+// A loading lane's codes of some positions: position n * kAtOnce + lane / kLanes of the warp's, 16
+// bytes of its head from 16 * (lane % kLanes) on.
+template <bool FP4, int DIM>
+struct RowsLane {
+  static constexpr int kLanes = (FP4 ? DIM / 2 : DIM) / 16;  // of a position
+  static constexpr int kAtOnce = kWarp / kLanes;             // positions an instruction
+  static constexpr int kLoads = kPer / kAtOnce;
+  static constexpr int kChunks = FP4 ? 4 : 2;                // of 16 bytes that 16 bytes of codes widen to
+  uint4 x[kLoads];
+
+  __device__ __forceinline__ void load(const unsigned char* codes, const int64_t* at, int lane) {
+#pragma unroll
+    for (int n = 0; n < kLoads; n++) {
+      const int64_t from = at[n * kAtOnce + lane / kLanes];
+      x[n] = make_uint4(0u, 0u, 0u, 0u);
+      if (from >= 0)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[n].x), "=r"(x[n].y), "=r"(x[n].z), "=r"(x[n].w)
+                     : "l"(codes + from));
+    }
+  }
+
+  // Widened into a tile, from its row row0 on.  TIDY: halves that are NaN become 0; bit n of the
+  // result: the n-th position had one.
+  template <bool TIDY>
+  __device__ __forceinline__ uint32_t store(unsigned char* dst, const uint16_t* mult, int row0,
+                                            int lane) const {
+    using Sh = RowsShared<FP4, DIM>;
+    const int lr = lane / kLanes, lc = lane % kLanes;
+    uint32_t found = 0;
+#pragma unroll
+    for (int n = 0; n < kLoads; n++) {
+      const int pos = n * kAtOnce + lr, row = row0 + pos;
+      const uint32_t word[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      uint4 half[kChunks];
+      if constexpr (!FP4) {
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          half[e] = make_uint4(half2_of_e4m3(word[2 * e]), half2_of_e4m3(word[2 * e] >> 16),
+                               half2_of_e4m3(word[2 * e + 1]), half2_of_e4m3(word[2 * e + 1] >> 16));
+      } else {
+        const uint32_t f = mult[pos * Sh::kGroups + lc] * 0x10001u;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          uint32_t h[4];
+          half2_of_e2m1(word[e], h);
+          half[e] =
+              make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f), mul_half2(h[3], f));
+        }
+      }
+      if (TIDY) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < kChunks; e++)
+          any |= tidy(half[e].x) | tidy(half[e].y) | tidy(half[e].z) | tidy(half[e].w);
+        if (any) found |= 1u << n;
+      }
+      // Chunk c of 16 bytes of a row lies at c ^ (row % 8) of its block of 128 bytes.  The order in
+      // which the lanes of a row write theirs keeps eight neighbouring lanes in different banks.
+      const int turn = FP4 ? (DIM == 128 ? (lc >> 1) | (row & 1) << 1 : (row >> 1 & 1) | (row & 1) << 1)
+                           : (DIM == 128 ? lc >> 2 : 0);
+#pragma unroll
+      for (int s = 0; s < kChunks; s++) {
+        const int e = s ^ turn, c = lc * kChunks + e;
+        uint4 h = half[0];
+#pragma unroll
+        for (int o = 1; o < kChunks; o++)
+          if (e == o) h = half[o];
+        *reinterpret_cast<uint4*>(dst + c / 8 * Sh::kBlockBytes + row * 128 + ((c % 8) ^ (row & 7)) * 16) = h;
+      }
+    }
+    return found;
+  }
+
+  __device__ __forceinline__ static uint32_t tidy(uint32_t& h) {
+    const uint32_t nan = ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) |
+                         ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
+    h &= ~nan;
+    return nan;
+  }
+};
+
+// One thread's row of a tile of scores: the largest score before the row's own factor, over the
+// positions whose bits are set (ALL: every one).
+template <bool ALL>
+__device__ __forceinline__ float rows_largest(unsigned s_at, const float* ks, const uint32_t (&see)[4]) {
+  float mx = kNone;
+  uint32_t x[32];
+#pragma unroll 1
+  for (int j = 0; j < 4; j++) {
+    tmem_load(s_at + 32 * j, x);
+    tmem_loaded(x);
+    const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * j);
+    const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const float4 k = k4[e];
+      float u[4];
+      split(mul2(f2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), f2(k.x, k.y)), u[0], u[1]);
+      split(mul2(f2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), f2(k.z, k.w)), u[2],
+            u[3]);
+      if (!ALL) {
+#pragma unroll
+        for (int h = 0; h < 4; h++)
+          if (!(bits >> (4 * e + h) & 1u)) u[h] = kNone;
+      }
+      mx = fmaxf(mx, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+    }
+  }
+  return mx;
+}
+
+// Its weights e^(score - m), summed; times V's scales and `up` as f16 over the scores.
+template <bool ALL>
+__device__ __forceinline__ float rows_weigh(unsigned s_at, const float* ks, const float* vs,
+                                            const uint32_t (&see)[4], float rs, float neg, float up) {
+  const F2 rs2 = f2(rs, rs), neg2 = f2(neg, neg), up2 = f2(up, up);
+  F2 l2 = f2(0.0f, 0.0f);
+  uint32_t x[32];
+#pragma unroll 1
+  for (int j = 0; j < 4; j++) {
+    tmem_load(s_at + 32 * j, x);
+    tmem_loaded(x);
+    const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * j);
+    const float4* v4 = reinterpret_cast<const float4*>(vs + 32 * j);
+    const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) {
+      const float4 k = k4[e / 2], v = v4[e / 2];
+      const F2 kk = e % 2 ? f2(k.z, k.w) : f2(k.x, k.y);
+      const F2 vv = e % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
+      float u[2];
+      split(fma2(mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk), rs2, neg2), u[0],
+            u[1]);
+      u[0] = attn_exp2(u[0]);
+      u[1] = attn_exp2(u[1]);
+      const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
+      if (!s0) u[0] = 0.0f;
+      if (!s1) u[1] = 0.0f;
+      const F2 weight = f2(u[0], u[1]);
+      l2 = add2(l2, weight);
+      split(mul2(mul2(weight, vv), up2), u[0], u[1]);
+      if (!s0) u[0] = 0.0f;  // whatever its scale
+      if (!s1) u[1] = 0.0f;
+      p[e] = half2_of(u[0], u[1]);
+    }
+    tmem_store16(s_at + 16 * j, p);
+  }
+  float lo, hi;
+  split(l2, lo, hi);
+  return lo + hi;
+}
+
 // Waits for the phase; once a wait has run out, no further one waits: every role runs through its
 // loop, the outputs are not valid, and the status word says so.
 struct Waiter {
@@ -213,7 +368,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&sh.tmem), kCols);
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<kRows, kPos>(a, sh.plan);  // (its barriers make the above visible)
+  make_plan<kRows, kPos, kItemCost>(a, sh.plan);  // (its barriers make the above visible)
   tc_before();
   __syncthreads();
   tc_after();
@@ -227,7 +382,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const Waiter wait{&sh.dead, status};
 
   if (w.unit < w.end) {
-    w.it = locate<kRows, kPos>(a, sh.plan, w.unit);
+    w.it = locate<kRows, kPos, kItemCost>(a, sh.plan, w.unit);
     int64_t tile = 0;  // of this block, over all its items
     int item = 0;
     while (w.unit < w.end) {
@@ -299,30 +454,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             vt = fmaxf(vt, vref);
             __syncwarp();
             // the largest score
-            float mx = kNone;
-            uint32_t x[32];
-#pragma unroll 1
-            for (int j = 0; j < 4; j++) {
-              tmem_load(s_at + 32 * j, x);
-              tmem_loaded(x);
-              const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * j);
-              const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
-#pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const float4 k = k4[e];
-                float u[4];
-                split(mul2(f2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), f2(k.x, k.y)),
-                      u[0], u[1]);
-                split(mul2(f2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), f2(k.z, k.w)),
-                      u[2], u[3]);
-                if (!clean) {
-#pragma unroll
-                  for (int h = 0; h < 4; h++)
-                    if (!(bits >> (4 * e + h) & 1u)) u[h] = kNone;
-                }
-                mx = fmaxf(mx, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
-              }
-            }
+            float mx = clean ? rows_largest<true>(s_at, ks, see) : rows_largest<false>(s_at, ks, see);
             if (mx > kNone) mx *= rs;
             // the reference moves, and the row of O with it
             const bool need = mx > (m == kNone ? kNone : m + kHeadroom) || vt > vref;
@@ -341,6 +473,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 wait(smem_addr(&sh.o_full[b ^ 1]), ((g - 1) >> 1) & 1);
                 __syncwarp();
                 tc_after();
+                uint32_t x[32];
 #pragma unroll 1
                 for (int j = 0; j < DIM / 32; j++) {
                   tmem_load(mine + 2 * kPos + 32 * j, x);
@@ -354,45 +487,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             const float neg = m == kNone ? 0.0f : -m;
             const float up = kHeldUp * power_reciprocal(vref);
-            const F2 rs2 = f2(rs, rs), neg2 = f2(neg, neg), up2 = f2(up, up);
-            F2 l2 = f2(0.0f, 0.0f);
-#pragma unroll 1
-            for (int j = 0; j < 4; j++) {
-              tmem_load(s_at + 32 * j, x);
-              tmem_loaded(x);
-              const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * j);
-              const float4* v4 = reinterpret_cast<const float4*>(vs + 32 * j);
-              const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 16; e++) {
-                const float4 k = k4[e / 2], v = v4[e / 2];
-                const F2 kk = e % 2 ? f2(k.z, k.w) : f2(k.x, k.y);
-                const F2 vv = e % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
-                float u[2];
-                split(fma2(mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk), rs2,
-                           neg2),
-                      u[0], u[1]);
-                u[0] = attn_exp2(u[0]);
-                u[1] = attn_exp2(u[1]);
-                if (!clean) {
-                  if (!(bits >> (2 * e) & 1u)) u[0] = 0.0f;
-                  if (!(bits >> (2 * e + 1) & 1u)) u[1] = 0.0f;
-                }
-                const F2 weight = f2(u[0], u[1]);
-                l2 = add2(l2, weight);
-                split(mul2(mul2(weight, vv), up2), u[0], u[1]);
-                if (!clean) {  // whatever its scale
-                  if (!(bits >> (2 * e) & 1u)) u[0] = 0.0f;
-                  if (!(bits >> (2 * e + 1) & 1u)) u[1] = 0.0f;
-                }
-                p[e] = half2_of(u[0], u[1]);
-              }
-              tmem_store16(s_at + 16 * j, p);
-            }
-            float lo, hi;
-            split(l2, lo, hi);
-            l += lo + hi;
+            l += clean ? rows_weigh<true>(s_at, ks, vs, see, rs, neg, up)
+                       : rows_weigh<false>(s_at, ks, vs, see, rs, neg, up);
             tmem_stored();
           }
           tc_before();
@@ -483,13 +579,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ loading
         const int lw = warp - kSoftWarps;
-        constexpr int kLanes = kCodeRow / 16;            // of a position
-        constexpr int kAtOnce = kWarp / kLanes;          // positions an instruction
-        constexpr int kLoads = kPer / kAtOnce;
-        constexpr int kChunks = FP4 ? 4 : 2;             // of 16 bytes that a lane's codes widen to
-        const int lr = lane / kLanes, lc = lane % kLanes;
-        const unsigned char* kc = a.side[0].codes + w.it.head * kCodeRow + 16 * lc;
-        const unsigned char* vc = a.side[1].codes + w.it.head * kCodeRow + 16 * lc;
+        RowsLane<FP4, DIM> k, v;
+        const int64_t from = w.it.head * kCodeRow + 16 * (lane % k.kLanes);
+        const unsigned char* kc = a.side[0].codes + from;
+        const unsigned char* vc = a.side[1].codes + from;
         const int base0 = w.it.tile * kPos + lw * kPer;
         auto lookup = [&](int i) {
           const int p = base0 + i * kPos + lane;
@@ -534,79 +627,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
           sh.at[lw][i & 1][lane] = at;
         };
-        auto load = [&](const unsigned char* codes, int i, uint4 (&x)[kLoads]) {
-#pragma unroll
-          for (int n = 0; n < kLoads; n++) {
-            const int64_t at = sh.at[lw][i & 1][n * kAtOnce + lr];
-            x[n] = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= 0)
-              asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[n].x), "=r"(x[n].y), "=r"(x[n].z), "=r"(x[n].w)
-                           : "l"(codes + at));
-          }
-        };
-        // widened into a tile; `clean_up`: halves that are NaN become 0, and the positions are noted
-        auto store = [&](unsigned char* dst, const uint4 (&x)[kLoads], const uint16_t* mult, bool clean_up,
-                         int p0) {
-#pragma unroll
-          for (int n = 0; n < kLoads; n++) {
-            const int pos = n * kAtOnce + lr, row = lw * kPer + pos;
-            const uint32_t word[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-            uint4 half[kChunks];
-            if constexpr (!FP4) {
-#pragma unroll
-              for (int e = 0; e < 2; e++)
-                half[e] = make_uint4(half2_of_e4m3(word[2 * e]), half2_of_e4m3(word[2 * e] >> 16),
-                                     half2_of_e4m3(word[2 * e + 1]), half2_of_e4m3(word[2 * e + 1] >> 16));
-            } else {
-              const uint32_t f = mult[pos * Sh::kGroups + lc] * 0x10001u;
-#pragma unroll
-              for (int e = 0; e < 4; e++) {
-                uint32_t h[4];
-                half2_of_e2m1(word[e], h);
-                half[e] = make_uint4(mul_half2(h[0], f), mul_half2(h[1], f), mul_half2(h[2], f),
-                                     mul_half2(h[3], f));
-              }
-            }
-            if (clean_up) {
-              uint32_t any = 0;
-              auto fix = [&](uint32_t& h) {
-                const uint32_t nan = ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) |
-                                     ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
-                any |= nan;
-                h &= ~nan;
-              };
-#pragma unroll
-              for (int e = 0; e < kChunks; e++) fix(half[e].x), fix(half[e].y), fix(half[e].z), fix(half[e].w);
-              if (any) {
-                atomicMin(&sh.nan_lo[item % kItems], p0 + pos);
-                atomicMax(&sh.nan_hi[item % kItems], p0 + pos);
-              }
-            }
-            // Chunk c of 16 bytes of a row lies at c ^ (row % 8) of its block of 128 bytes.  The order in
-            // which the lanes of a row write theirs keeps eight neighbouring lanes in different banks.
-            const int turn = FP4 ? (DIM == 128 ? (lc >> 1) | (row & 1) << 1 : (row >> 1) & 1 | (row & 1) << 1)
-                                 : (DIM == 128 ? lc >> 2 : 0);
-#pragma unroll
-            for (int s = 0; s < kChunks; s++) {
-              const int e = s ^ turn, c = lc * kChunks + e;
-              uint4 h = half[0];
-#pragma unroll
-              for (int o = 1; o < kChunks; o++)
-                if (e == o) h = half[o];
-              *reinterpret_cast<uint4*>(dst + c / 8 * Sh::kBlockBytes + row * 128 +
-                                        ((c % 8) ^ (row & 7)) * 16) = h;
-            }
-          }
-        };
-
         int blk = lookup(0);
         place(0, blk);
         blk = lookup(1);
         __syncwarp();
-        uint4 kx[kLoads], vx[kLoads];
-        load(kc, 0, kx);
-        load(vc, 0, vx);
+        k.load(kc, sh.at[lw][0], lane);
+        v.load(vc, sh.at[lw][0], lane);
 
         // Q: two threads a row
         if (item > 0) wait(smem_addr(&sh.q_empty), (item - 1) & 1);
@@ -687,14 +713,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             __syncwarp();
           }
           if (g >= 2) wait(smem_addr(&sh.k_empty[b]), ((g >> 1) - 1) & 1);
-          store(sh.k[b], kx, &sh.km[lw][i & 1][0][0], false, p0);
-          if (more) load(kc, i + 1, kx);
+          k.template store<false>(sh.k[b], &sh.km[lw][i & 1][0][0], lw * kPer, lane);
+          if (more) k.load(kc, sh.at[lw][(i + 1) & 1], lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[b]));
           if (g >= 2) wait(smem_addr(&sh.v_empty[b]), ((g >> 1) - 1) & 1);
-          store(sh.v[b], vx, &sh.vm[lw][i & 1][0][0], !clean, p0);
-          if (more) load(vc, i + 1, vx);
+          if (clean) {
+            v.template store<false>(sh.v[b], &sh.vm[lw][i & 1][0][0], lw * kPer, lane);
+          } else {
+            uint32_t found = v.template store<true>(sh.v[b], &sh.vm[lw][i & 1][0][0], lw * kPer, lane);
+            for (; found != 0; found &= found - 1) {
+              const int pos = p0 + (__ffs(found) - 1) * v.kAtOnce + lane / v.kLanes;
+              atomicMin(&sh.nan_lo[item % kItems], pos);
+              atomicMax(&sh.nan_hi[item % kItems], pos);
+            }
+          }
+          if (more) v.load(vc, sh.at[lw][(i + 1) & 1], lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[b]));
@@ -738,7 +773,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
 
-      w.unit += steps;
+      w.unit += steps + kItemCost;
       tile += steps;
       item++;
       if (w.unit < w.end) next_item<kRows, kPos>(a, w.it, seq.queries);
@@ -774,8 +809,8 @@ cudaError_t rows_go(AttnArgs a, void* workspace, cudaStream_t s) {
   e = launch_pdl(cache_attention_rows_kernel<FP4, DIM>, dim3(kRowsShares), dim3(kRowsThreads), shared, s,
                  a, status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>, dim3(kRowsShares, 32),
-                    dim3(DIM / 4), 0, s, a);
+  return launch_pdl(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>,
+                    dim3(kRowsShares, kRows / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
 }
 
 }  // namespace
