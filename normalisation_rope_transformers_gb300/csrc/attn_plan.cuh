@@ -311,12 +311,12 @@ __global__ void __launch_bounds__(DIM / 4 * kJoinRows) cache_attention_join_kern
     a.lse[head] = sum != 0.0f ? (top + log2f(sum)) * kAttnLn2 : -__builtin_huge_valf();
 }
 
-// Shared memory of a kernel, once a device: the opt-in to more than 48 KB, and the largest share
-// of the SM's memory.  Without the latter an SM that the join ran on with a small share has no room
-// for all blocks of the next call, which then runs in two waves (400009 tokens, calls back to back:
-// 428 us, calls apart 272 us).
+// Shared memory of a kernel, once a device: the opt-in to more than 48 KB, and how much of the SM's
+// memory is to be shared memory, in percent.  Both kernels of a call ask for the same: an SM that
+// the join ran on with a small share has no room for all blocks of the next call, which then runs in
+// two waves (400009 tokens, calls back to back: 428 us, calls apart 272 us).
 template <typename Kernel>
-cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
+cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done, int percent = 100) {
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
@@ -326,7 +326,7 @@ cudaError_t allow_shared(Kernel kernel, size_t bytes, std::atomic<int>* done) {
                            static_cast<int>(bytes));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
+                             percent);
   if (e == cudaSuccess) done[device].store(1, std::memory_order_relaxed);
   return e;
 }

@@ -796,12 +796,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 template <bool FP4, int DIM>
 cudaError_t rows_go(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr size_t shared = sizeof(RowsShared<FP4, DIM>) + 1024;
+  constexpr int percent = 86;  // 196 of 228 KB: the rest is L1, for what the registers do not hold
+  static_assert(shared <= 195 * 1024, "one block an SM");
   static std::atomic<int> done[64], done_join[64];
   unsigned* status = nullptr;
   cudaError_t e = status_word(&status);
-  if (e == cudaSuccess) e = allow_shared(cache_attention_rows_kernel<FP4, DIM>, shared, done);
+  if (e == cudaSuccess) e = allow_shared(cache_attention_rows_kernel<FP4, DIM>, shared, done, percent);
   if (e == cudaSuccess)
-    e = allow_shared(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>, 0, done_join);
+    e = allow_shared(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>, 0, done_join, percent);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
