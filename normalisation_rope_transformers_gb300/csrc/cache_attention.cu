@@ -23,13 +23,12 @@ namespace nr {
 namespace {
 
 // A share for each block that fits at once on 152 SMs (any number is right).
-template <int DIM>
-constexpr int attn_blocks = DIM == 256 ? 2 : 3;
+template <int DIM, int ROWS>
+constexpr int attn_blocks = DIM == 256 ? 2 : ROWS == 8 ? 4 : 3;
 constexpr int kSms = 152;
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
-constexpr int kAttnRows = 16;
 constexpr int kStep = 16;          // positions a warp handles at a time
 constexpr int kAttnTile = kStep * kAttnWarps;  // positions of a block's step
 constexpr int kItemCost = 3;  // tiles that an item costs besides its own
@@ -40,6 +39,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// The fragment of an 8 x 8 matrix of halves turned into the fragment of its transpose.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // N bytes (4, 8 or a multiple of 16) from global memory, or zeros.
@@ -92,45 +98,47 @@ struct Layout {
   }
 };
 
-template <typename T, bool FP4, int DIM>
+template <typename T, bool FP4, int DIM, int ROWS>
 struct AttnShared {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
   using L = Layout<FP4, DIM>;
-  uint4 q[SPLIT][L::kStepsK][kWarp];       // fragments
-  float row_scale[kAttnRows];
-  int64_t at[kAttnWarps][2][kStep];        // code offsets, -1: no such position
+  // fragments: 16 rows are the first operand, 8 rows the second
+  using Fragment = typename std::conditional<ROWS == 16, uint4, uint2>::type;
+  Fragment q[SPLIT][L::kStepsK][kWarp];
+  alignas(16) float row_scale[ROWS];
+  alignas(16) int64_t at[kAttnWarps][2][kStep];        // code offsets, -1: no such position
   float ks[kAttnWarps][kStep];             // scales of K, of V
   float vs[kAttnWarps][kStep];
   uint16_t km[kAttnWarps][kStep][FP4 ? L::kGroups : 1];
   uint16_t vm[kAttnWarps][kStep][FP4 ? L::kGroups : 1];
-  float m[kAttnWarps][kAttnRows], l[kAttnWarps][kAttnRows];
-  float top[kAttnRows], sum[kAttnRows];
-  float o[kAttnWarps][kAttnRows][DIM + 4];
+  float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];
+  float top[ROWS], sum[ROWS];
+  alignas(16) float o[kAttnWarps][ROWS][DIM + 4];
   AttnPlan<kAttnThreads> plan;
 };
 
-template <typename T, bool FP4, int DIM>
-__global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
+template <typename T, bool FP4, int DIM, int ROWS>
+__global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
     cache_attention_kernel(const AttnArgs a) {
   using L = Layout<FP4, DIM>;
   constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM>*>(smem_raw);
+  auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM, ROWS>*>(smem_raw);
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp, g = lane / 4, c = lane % 4;
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<kAttnRows, kAttnTile, kItemCost>(a, sh.plan);
+  make_plan<ROWS, kAttnTile, kItemCost>(a, sh.plan);
   const int64_t total = sh.plan.at[kAttnThreads];
   const int64_t share = share_size(total, gridDim.x);
   int64_t unit = blockIdx.x * share;
   const int64_t end = min(unit + share, total);
   if (t == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (unit >= end) return;
-  AttnItem it = locate<kAttnRows, kAttnTile, kItemCost>(a, sh.plan, unit);
+  AttnItem it = locate<ROWS, kAttnTile, kItemCost>(a, sh.plan, unit);
 
   while (unit < end) {
     const AttnSeq<kAttnTile> seq(a, it.seq);
-    const int rows_left = seq.queries * static_cast<int>(a.group.div) - it.rb * kAttnRows;
-    const int rows = min(rows_left, kAttnRows);
+    const int rows_left = seq.queries * static_cast<int>(a.group.div) - it.rb * ROWS;
+    const int rows = min(rows_left, ROWS);
     const int steps = static_cast<int>(min(static_cast<int64_t>(seq.tiles - it.tile), end - unit));
 
     // Q's rows as fragments: eight threads a row, each DIM / 8 elements
@@ -138,7 +146,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       const int r = t / 8, part = t % 8;
       constexpr int N = DIM / 8;
       float x[N], top = 0.0f;
-      const int row = it.rb * kAttnRows + r;
+      const int row = it.rb * ROWS + r;
       const int tok = a.group.quot(row), head = it.head * a.group.div + (row - tok * a.group.div);
       const T* p = static_cast<const T*>(a.q) + (seq.first + tok) * a.q_stride +
                    static_cast<int64_t>(head) * DIM + part * N;
@@ -153,14 +161,16 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       // times 2^(14 - e) for top in [2^e, 2^(e + 1)) (rows below 2^-100: 2^114)
       const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127;
       const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-      if (part == 0)
+      if (part == 0 && r < ROWS)
         sh.row_scale[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 #pragma unroll
       for (int i = 0; i < N; i++) {
         const int d = part * N + i;
         constexpr int P = L::kPieceK;
         const int k = d / (4 * P) * (P / 4) + d % P / 4, lc = d % (4 * P) / P, sub = d % 4;
-        const int at = ((r % 8) * 4 + lc) * 8 + ((sub / 2) * 2 + r / 8) * 2 + sub % 2;  // halves
+        const int at = ROWS == 16 ? ((r % 8) * 4 + lc) * 8 + ((sub / 2) * 2 + r / 8) * 2 + sub % 2
+                                  : (r * 4 + lc) * 4 + sub;  // halves
+        if (r >= ROWS) continue;
         const float v = x[i] * up;
         const __half hi = __float2half_rn(v);
         reinterpret_cast<__half*>(sh.q[0][k])[at] = hi;
@@ -169,13 +179,17 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       }
     }
     __syncthreads();
-    const float rs0 = sh.row_scale[g], rs1 = sh.row_scale[g + 8];
-    const int row0 = it.rb * kAttnRows + g;
-    const int tok0 = a.group.quot(row0), tok1 = a.group.quot(row0 + 8);
+    // A lane's two rows: with 16 they are rows of the scores' fragment (positions its columns),
+    // with 8 its columns (positions its rows): half the products, and half of O.
+    const int r0 = ROWS == 16 ? g : 2 * c, r1 = ROWS == 16 ? g + 8 : 2 * c + 1;
+    const float rs0 = sh.row_scale[r0], rs1 = sh.row_scale[r1];
+    const int row0 = it.rb * ROWS + r0, row1 = it.rb * ROWS + r1;
+    const int tok0 = a.group.quot(row0), tok1 = a.group.quot(row1);
 
-    float o[L::kTilesV][4];
+    constexpr int kTilesO = L::kTilesV * ROWS / 16;
+    float o[kTilesO][4];
 #pragma unroll
-    for (int j = 0; j < L::kTilesV; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    for (int j = 0; j < kTilesO; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m0 = -__builtin_huge_valf(), m1 = m0, l0 = 0.0f, l1 = 0.0f;
     // A row's weights are held relative to the largest V scale that it has met, as a power of two
     // (so that a step's result does not depend on it but where weights leave f16's range).
@@ -185,13 +199,17 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
     const unsigned char* kc = a.side[0].codes + it.head * L::kCodeRow;
     const unsigned char* vc = a.side[1].codes + it.head * L::kCodeRow;
     const int base0 = it.tile * kAttnTile + warp * kStep;
-    auto lookup = [&](int i) {  // the block of position `lane` of step i, or -1
+    // What the table says for position `lane` of step i, or -1.  (It is looked at a step later: a
+    // comparison here would wait for it.)
+    const int32_t* table = a.table + it.seq * a.width;
+    auto lookup = [&](int i) {
       const int p = base0 + i * kAttnTile + lane;
-      if (lane >= kStep || i >= steps || p >= seq.length) return -1;
-      const int64_t page = a.page.quot(p);
-      if (page >= a.width) return -1;
-      const int b = a.table[it.seq * a.width + page];
-      return b >= 0 && b < a.blocks ? b : -1;
+      int b = -1;
+      if (lane < kStep && i < steps && p < seq.length) {
+        const uint32_t page = a.page.quot(p);
+        if (page < a.width) b = table[page];
+      }
+      return b;
     };
     float ks = 0.0f, vs = 0.0f;        // FP8 scales of this lane's position
     uint64_t kb = 0, vb = 0;           // MXFP4 scale bytes
@@ -203,8 +221,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
         int64_t at = -1;
         ks = vs = 0.0f;
         kb = vb = 0;
-        if (block >= 0) {
-          const int64_t in = p - static_cast<int64_t>(a.page.quot(p)) * a.page.div;
+        if (block >= 0 && block < a.blocks) {
+          const uint32_t in = p - a.page.quot(p) * a.page.div;
           at = block * a.geo.code_block_stride + in * a.geo.code_row;
           const int64_t sc = block * a.geo.scale_block_stride + in * a.geo.scale_row;
           if constexpr (!FP4) {
@@ -231,7 +249,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
         }
         sh.at[warp][i & 1][lane] = at;
       }
-      return __all_sync(0xFFFFFFFFu, lane >= kStep || (block >= 0 && p < seq.context));
+      return __all_sync(0xFFFFFFFFu,
+                        lane >= kStep || (block >= 0 && block < a.blocks && p < seq.context));
     };
     Words<L::kBytesK> k[2];
     Words<L::kBytesV> v[4];
@@ -280,68 +299,92 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       }
       __syncwarp();
 
-      float s[2][4];
+      // Scores: s[n][e], element e of position fragment n (16 rows: n-th eight positions; 8 rows: one
+      // fragment of all 16).
+      constexpr int kN = ROWS / 8;
+      float s[kN][4];
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int n = 0; n < kN; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
-        for (int q = 0; q < L::kStepsK; q++) {
-          uint32_t b0, b1;
+      for (int q = 0; q < L::kStepsK; q++) {
+        uint32_t h[2][2];  // of position 8 n + g: dimensions k_dim, + 1 and + 2, + 3
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
           if constexpr (!FP4) {
-            b0 = half2_of_e4m3(k[n].w[q]);
-            b1 = half2_of_e4m3(k[n].w[q] >> 16);
+            h[n][0] = half2_of_e4m3(k[n].w[q]);
+            h[n][1] = half2_of_e4m3(k[n].w[q] >> 16);
           } else {
-            uint32_t h[4];
-            half2_of_e2m1(k[n].w[q / 2], h);
+            uint32_t w[4];
+            half2_of_e2m1(k[n].w[q / 2], w);
             const uint32_t f = sh.km[warp][8 * n + g][L::k_dim(0, q) / 32 +
                                                      (L::kPieceK == 32 ? c : c / 2)] *
                                0x10001u;
-            b0 = mul_half2(h[q % 2 * 2], f);
-            b1 = mul_half2(h[q % 2 * 2 + 1], f);
+            h[n][0] = mul_half2(w[q % 2 * 2], f);
+            h[n][1] = mul_half2(w[q % 2 * 2 + 1], f);
           }
-          mma_f16(s[n], sh.q[0][q][lane], b0, b1);
-          if (SPLIT == 2) mma_f16(s[n], sh.q[SPLIT - 1][q][lane], b0, b1);
+        }
+#pragma unroll
+        for (int part = 0; part < SPLIT; part++) {
+          const auto x = sh.q[part][q][lane];
+          if constexpr (ROWS == 16) {
+            mma_f16(s[0], x, h[0][0], h[0][1]);
+            mma_f16(s[1], x, h[1][0], h[1][1]);
+          } else {
+            mma_f16(s[0], make_uint4(h[0][0], h[1][0], h[0][1], h[1][1]), x.x, x.y);
+          }
         }
       }
       if (more) load_k(i + 1);
 
-      // scores in units of log2
+      // In units of log2.  Element e of fragment n: row r0 or r1, position at(n, e).
+      auto at = [&](int n, int e) { return ROWS == 16 ? 8 * n + 2 * c + e % 2 : g + 8 * (e / 2); };
+      auto second = [](int e) { return ROWS == 16 ? e >= 2 : e % 2 == 1; };  // of r1
       float mx0 = m0, mx1 = m1;
-      float2 sv[2];
+      float sv[kN][2];  // V's scales of the lane's positions
+      {
+        float sk[kN][2];
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        const float2 sk = *reinterpret_cast<const float2*>(&sh.ks[warp][8 * n + 2 * c]);
-        sv[n] = *reinterpret_cast<const float2*>(&sh.vs[warp][8 * n + 2 * c]);
-        s[n][0] *= sk.x * rs0;
-        s[n][1] *= sk.y * rs0;
-        s[n][2] *= sk.x * rs1;
-        s[n][3] *= sk.y * rs1;
+        for (int n = 0; n < kN; n++) {
+          if (ROWS == 16) {
+            const float2 x = *reinterpret_cast<const float2*>(&sh.ks[warp][8 * n + 2 * c]);
+            const float2 y = *reinterpret_cast<const float2*>(&sh.vs[warp][8 * n + 2 * c]);
+            sk[n][0] = x.x, sk[n][1] = x.y, sv[n][0] = y.x, sv[n][1] = y.y;
+          } else {
+            sk[n][0] = sh.ks[warp][g], sk[n][1] = sh.ks[warp][g + 8];
+            sv[n][0] = sh.vs[warp][g], sv[n][1] = sh.vs[warp][g + 8];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            s[n][e] *= sk[n][ROWS == 16 ? e % 2 : e / 2] * (second(e) ? rs1 : rs0);
+        }
       }
       uint32_t hidden = 0;  // bit 4 n + e: not seen
       if (!was_clean) {
+        const int rows_end = it.rb * ROWS + rows;
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < kN; n++)
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const int p = base0 + i * kAttnTile + 8 * n + 2 * c + e;
-            const bool there = sh.at[warp][i & 1][8 * n + 2 * c + e] >= 0;
-            if (!(there && row0 < it.rb * kAttnRows + rows && attn_sees(a, seq, tok0, p))) {
+          for (int e = 0; e < 4; e++) {
+            const int p = base0 + i * kAttnTile + at(n, e);
+            const bool there = sh.at[warp][i & 1][at(n, e)] >= 0;
+            if (!(there && (second(e) ? row1 : row0) < rows_end &&
+                  attn_sees(a, seq, second(e) ? tok1 : tok0, p))) {
               hidden |= 1u << (4 * n + e);
               s[n][e] = -__builtin_huge_valf();
-            }
-            if (!(there && row0 + 8 < it.rb * kAttnRows + rows && attn_sees(a, seq, tok1, p))) {
-              hidden |= 1u << (4 * n + 2 + e);
-              s[n][2 + e] = -__builtin_huge_valf();
             }
           }
       }
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
-        mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
-      }
+      for (int n = 0; n < kN; n++)
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
+        for (int e = 0; e < 4; e++) {
+          if (second(e)) mx1 = fmaxf(mx1, s[n][e]);
+          else mx0 = fmaxf(mx0, s[n][e]);
+        }
+      // the lanes that share a row
+      constexpr int kFirst = ROWS == 16 ? 1 : 4, kLast = ROWS == 16 ? 2 : 16;
+#pragma unroll
+      for (int d = kFirst; d <= kLast; d <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
       }
@@ -352,15 +395,16 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       } else {
         vt0 = vt1 = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-          const float x = scale_reference(sv[n].x), y = scale_reference(sv[n].y);
-          if (!(hidden >> (4 * n) & 1u)) vt0 = fmaxf(vt0, x);
-          if (!(hidden >> (4 * n + 1) & 1u)) vt0 = fmaxf(vt0, y);
-          if (!(hidden >> (4 * n + 2) & 1u)) vt1 = fmaxf(vt1, x);
-          if (!(hidden >> (4 * n + 3) & 1u)) vt1 = fmaxf(vt1, y);
-        }
+        for (int n = 0; n < kN; n++)
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
+          for (int e = 0; e < 4; e++) {
+            if (hidden >> (4 * n + e) & 1u) continue;
+            const float x = scale_reference(sv[n][ROWS == 16 ? e % 2 : e / 2]);
+            if (second(e)) vt1 = fmaxf(vt1, x);
+            else vt0 = fmaxf(vt0, x);
+          }
+#pragma unroll
+        for (int d = kFirst; d <= kLast; d <<= 1) {
           vt0 = fmaxf(vt0, __shfl_xor_sync(0xFFFFFFFFu, vt0, d));
           vt1 = fmaxf(vt1, __shfl_xor_sync(0xFFFFFFFFu, vt1, d));
         }
@@ -376,12 +420,9 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
         f0 *= vref0 * power_reciprocal(vt0);
         f1 *= vref1 * power_reciprocal(vt1);
 #pragma unroll
-        for (int j = 0; j < L::kTilesV; j++) {
-          o[j][0] *= f0;
-          o[j][1] *= f0;
-          o[j][2] *= f1;
-          o[j][3] *= f1;
-        }
+        for (int j = 0; j < kTilesO; j++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) o[j][e] *= second(e) ? f1 : f0;
         m0 = mx0;
         m1 = mx1;
         vref0 = vt0;
@@ -389,44 +430,60 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       }
       const float winv0 = kWeightUp * power_reciprocal(vref0);
       const float winv1 = kWeightUp * power_reciprocal(vref1);
-      float w[2][4];
+      float w[kN][4];
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-#pragma unroll
-        for (int e = 0; e < 4; e++) w[n][e] = attn_exp2(s[n][e] - (e < 2 ? use0 : use1));
-        l0 += w[n][0] + w[n][1];
-        l1 += w[n][2] + w[n][3];
-        w[n][0] *= sv[n].x * winv0;
-        w[n][1] *= sv[n].y * winv0;
-        w[n][2] *= sv[n].x * winv1;
-        w[n][3] *= sv[n].y * winv1;
-        if (!was_clean) {
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (hidden >> (4 * n + e) & 1u) w[n][e] = 0.0f;  // whatever its scale
-        }
-      }
-      uint4 p[SPLIT];
-      p[0] = make_uint4(half2_of(w[0][0], w[0][1]), half2_of(w[0][2], w[0][3]),
-                        half2_of(w[1][0], w[1][1]), half2_of(w[1][2], w[1][3]));
-      if (SPLIT == 2) {
-        const uint32_t hi[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
-        uint32_t lo[4];
+      for (int n = 0; n < kN; n++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float2 f = floats_of_half2(hi[e]);
-          lo[e] = half2_of(w[e / 2][e % 2 * 2] - f.x, w[e / 2][e % 2 * 2 + 1] - f.y);
+          w[n][e] = attn_exp2(s[n][e] - (second(e) ? use1 : use0));
+          if (second(e)) l1 += w[n][e];
+          else l0 += w[n][e];
+          w[n][e] *= sv[n][ROWS == 16 ? e % 2 : e / 2] * (second(e) ? winv1 : winv0);
+          if (!was_clean && (hidden >> (4 * n + e) & 1u)) w[n][e] = 0.0f;  // whatever its scale
         }
-        p[SPLIT - 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      // As fragments of the second product: 16 rows its first operand as they are, 8 rows its second,
+      // turned around.  p[part][0 .. 3] or [0 .. 1].
+      uint32_t p[SPLIT][2 * kN];
+#pragma unroll
+      for (int n = 0; n < kN; n++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const float x = w[n][2 * h], y = w[n][2 * h + 1];
+          p[0][2 * n + h] = half2_of(x, y);
+          if (SPLIT == 2) {
+            const float2 f = floats_of_half2(p[0][2 * n + h]);
+            p[SPLIT - 1][2 * n + h] = half2_of(x - f.x, y - f.y);
+          }
+        }
+      uint32_t seen[2 * kN];  // ones where a weight may be
+#pragma unroll
+      for (int n = 0; n < 2 * kN; n++)
+        seen[n] = (hidden >> (2 * n) & 1u ? 0u : 0x3C00u) | (hidden >> (2 * n + 1) & 1u ? 0u : 0x3C000000u);
+      if constexpr (ROWS == 8) {
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+#pragma unroll
+          for (int part = 0; part < SPLIT; part++) p[part][n] = transposed(p[part][n]);
+          if (!was_clean) seen[n] = transposed(seen[n]);
+        }
       }
 
-      // the second product: pairs of positions of one dimension
-      const uint4 seen =
-          make_uint4((hidden & 1 ? 0u : 0x3C00u) | (hidden & 2 ? 0u : 0x3C000000u),
-                     (hidden & 4 ? 0u : 0x3C00u) | (hidden & 8 ? 0u : 0x3C000000u),
-                     (hidden & 16 ? 0u : 0x3C00u) | (hidden & 32 ? 0u : 0x3C000000u),
-                     (hidden & 64 ? 0u : 0x3C00u) | (hidden & 128 ? 0u : 0x3C000000u));
-      auto product = [&](int j, uint32_t b0, uint32_t b1) {
+      // The second product, for output tiles j and j + 1: x and y pairs of positions (2 c, 2 c + 1; 8
+      // further) of each one's dimension.
+      auto product = [&](int j, uint32_t x0, uint32_t y0, uint32_t x1, uint32_t y1) {
+        auto both = [&](float (&d)[4], float (&d2)[4], const uint32_t (&f)[2 * kN], uint32_t x0, uint32_t y0,
+                        uint32_t x1, uint32_t y1) {
+          if constexpr (ROWS == 16) {
+            const uint4 rows16 = make_uint4(f[0], f[1], f[2 * kN - 2], f[2 * kN - 1]);
+            mma_f16(d, rows16, x0, y0);
+            mma_f16(d2, rows16, x1, y1);
+          } else {
+            mma_f16(d, make_uint4(x0, x1, y0, y1), f[0], f[1]);
+          }
+        };
+        constexpr int kPer = ROWS == 16 ? 1 : 2;  // output tiles a fragment
+        float(&d)[4] = o[j / kPer];
+        float(&d2)[4] = o[(j + 1) / kPer];
         if (!was_clean) {
           // A NaN of V reaches those who see its position and nobody else: it leaves the
           // product (0 * NaN is a NaN), and is counted.
@@ -434,19 +491,21 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
             return ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) |
                    ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
           };
-          const uint32_t n0 = nan_halves(b0), n1 = nan_halves(b1);
-          if (__any_sync(0xFFFFFFFFu, (n0 | n1) != 0)) {
-            float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(count, seen, n0 & 0x3C003C00u, n1 & 0x3C003C00u);
-            b0 &= ~n0;
-            b1 &= ~n1;
+          const uint32_t a0 = nan_halves(x0), b0 = nan_halves(y0), a1 = nan_halves(x1), b1 = nan_halves(y1);
+          if (__any_sync(0xFFFFFFFFu, (a0 | b0 | a1 | b1) != 0)) {
+            float n0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, n1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            constexpr uint32_t one = 0x3C003C00u;
+            both(n0, n1, seen, a0 & one, b0 & one, a1 & one, b1 & one);
+            x0 &= ~a0, y0 &= ~b0, x1 &= ~a1, y1 &= ~b1;
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-              if (count[e] > 0.0f) o[j][e] = __uint_as_float(0x7FC00000u);
+            for (int e = 0; e < 4; e++) {
+              if (n0[e] > 0.0f) d[e] = __uint_as_float(0x7FC00000u);
+              if (ROWS == 16 && n1[e] > 0.0f) d2[e] = __uint_as_float(0x7FC00000u);
+            }
           }
         }
-        mma_f16(o[j], p[0], b0, b1);
-        if (SPLIT == 2) mma_f16(o[j], p[SPLIT - 1], b0, b1);
+#pragma unroll
+        for (int part = 0; part < SPLIT; part++) both(d, d2, p[part], x0, y0, x1, y1);
       };
       if constexpr (!FP4) {
 #pragma unroll
@@ -455,8 +514,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
           for (int h = 0; h < 2; h++) {
             const uint32_t x = __byte_perm(v[0].w[q], v[1].w[q], h ? 0x7362 : 0x5140);
             const uint32_t y = __byte_perm(v[2].w[q], v[3].w[q], h ? 0x7362 : 0x5140);
-            product(4 * q + 2 * h, half2_of_e4m3(x), half2_of_e4m3(y));
-            product(4 * q + 2 * h + 1, half2_of_e4m3(x >> 16), half2_of_e4m3(y >> 16));
+            product(4 * q + 2 * h, half2_of_e4m3(x), half2_of_e4m3(y), half2_of_e4m3(x >> 16),
+                    half2_of_e4m3(y >> 16));
           }
         }
       } else {
@@ -467,22 +526,21 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
         const uint32_t f1 = f[(8 + 2 * c) * G] | static_cast<uint32_t>(f[(9 + 2 * c) * G]) << 16;
 #pragma unroll
         for (int q = 0; q < L::kTilesV / 8; q++) {
-          uint32_t x[4], y[4];
           auto even = [](uint32_t lo, uint32_t hi) {
             return (lo & 0x0F0F0F0Fu) | (hi & 0x0F0F0F0Fu) << 4;
           };
           auto odd = [](uint32_t lo, uint32_t hi) {
             return (lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
           };
-          half2_of_e2m1(even(v[0].w[q], v[1].w[q]), x);
-          half2_of_e2m1(even(v[2].w[q], v[3].w[q]), y);
-#pragma unroll
-          for (int h = 0; h < 4; h++) product(8 * q + 2 * h, mul_half2(x[h], f0), mul_half2(y[h], f1));
-          half2_of_e2m1(odd(v[0].w[q], v[1].w[q]), x);
-          half2_of_e2m1(odd(v[2].w[q], v[3].w[q]), y);
+          uint32_t x0[4], y0[4], x1[4], y1[4];
+          half2_of_e2m1(even(v[0].w[q], v[1].w[q]), x0);
+          half2_of_e2m1(even(v[2].w[q], v[3].w[q]), y0);
+          half2_of_e2m1(odd(v[0].w[q], v[1].w[q]), x1);
+          half2_of_e2m1(odd(v[2].w[q], v[3].w[q]), y1);
 #pragma unroll
           for (int h = 0; h < 4; h++)
-            product(8 * q + 2 * h + 1, mul_half2(x[h], f0), mul_half2(y[h], f1));
+            product(8 * q + 2 * h, mul_half2(x0[h], f0), mul_half2(y0[h], f1), mul_half2(x1[h], f0),
+                    mul_half2(y1[h], f1));
         }
       }
       if (more) load_v(i + 1);
@@ -490,36 +548,37 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
     }
 
     // --- the warps' results joined, in order
+    constexpr int kFirst = ROWS == 16 ? 1 : 4, kLast = ROWS == 16 ? 2 : 16;
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
+    for (int d = kFirst; d <= kLast; d <<= 1) {
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
     }
-    if (c == 0) {
-      sh.m[warp][g] = m0;
-      sh.m[warp][g + 8] = m1;
-      sh.l[warp][g] = l0;
-      sh.l[warp][g + 8] = l1;
+    if ((ROWS == 16 ? c : g) == 0) {
+      sh.m[warp][r0] = m0;
+      sh.m[warp][r1] = m1;
+      sh.l[warp][r0] = l0;
+      sh.l[warp][r1] = l1;
     }
     __syncthreads();
-    float top0 = sh.m[0][g], top1 = sh.m[0][g + 8];
+    float top0 = sh.m[0][r0], top1 = sh.m[0][r1];
 #pragma unroll
     for (int w = 1; w < kAttnWarps; w++) {
-      top0 = fmaxf(top0, sh.m[w][g]);
-      top1 = fmaxf(top1, sh.m[w][g + 8]);
+      top0 = fmaxf(top0, sh.m[w][r0]);
+      top1 = fmaxf(top1, sh.m[w][r1]);
     }
     const float f0 = m0 == -__builtin_huge_valf() ? 0.0f : attn_exp2(m0 - top0);
     const float f1 = m1 == -__builtin_huge_valf() ? 0.0f : attn_exp2(m1 - top1);
     const float back0 = vref0 * (1.0f / kWeightUp), back1 = vref1 * (1.0f / kWeightUp);
 #pragma unroll
-    for (int j = 0; j < L::kTilesV; j++) {
-      const int d0 = L::v_dim(2 * c, j), d1 = L::v_dim(2 * c + 1, j);
-      sh.o[warp][g][d0] = o[j][0] * back0 * f0;
-      sh.o[warp][g][d1] = o[j][1] * back0 * f0;
-      sh.o[warp][g + 8][d0] = o[j][2] * back1 * f1;
-      sh.o[warp][g + 8][d1] = o[j][3] * back1 * f1;
-    }
-    if (t < kAttnRows) {
+    for (int j = 0; j < kTilesO; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const bool two = ROWS == 16 ? e >= 2 : e % 2 == 1;
+        const int d = ROWS == 16 ? L::v_dim(2 * c + e % 2, j) : L::v_dim(g, 2 * j + e / 2);
+        sh.o[warp][two ? r1 : r0][d] = o[j][e] * (two ? back1 : back0) * (two ? f1 : f0);
+      }
+    if (t < ROWS) {
       float top = sh.m[0][t], sum = 0.0f;
 #pragma unroll
       for (int w = 1; w < kAttnWarps; w++) top = fmaxf(top, sh.m[w][t]);
@@ -532,7 +591,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
     __syncthreads();
     const bool from_start = it.tile == 0, to_end = it.tile + steps == seq.tiles;
     float* part = a.partial +
-                  (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * kAttnRows * (DIM + 2);
+                  (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * ROWS * (DIM + 2);
     for (int i = t; i < rows * (DIM / 4); i += kAttnThreads) {
       const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
       float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][d]);
@@ -543,7 +602,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       }
       const float sum = sh.sum[r];
       if (from_start && to_end) {
-        const int row = it.rb * kAttnRows + r;
+        const int row = it.rb * ROWS + r;
         const int tok = a.group.quot(row), i_head = row - tok * a.group.div;
         const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
                              it.head * a.group.div + i_head;
@@ -559,8 +618,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
       } else {
         *reinterpret_cast<float4*>(part + r * DIM + d) = x;
         if (d == 0) {
-          part[kAttnRows * DIM + 2 * r] = sh.top[r];
-          part[kAttnRows * DIM + 2 * r + 1] = sum;
+          part[ROWS * DIM + 2 * r] = sh.top[r];
+          part[ROWS * DIM + 2 * r + 1] = sum;
         }
       }
     }
@@ -574,33 +633,38 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM>)
 
     unit += steps + kItemCost;
     if (unit >= end) break;
-    next_item<kAttnRows, kAttnTile>(a, it, seq.queries);
+    next_item<ROWS, kAttnTile>(a, it, seq.queries);
   }
 }
 
-template <typename T, bool FP4, int DIM>
+template <typename T, bool FP4, int DIM, int ROWS>
 cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
-  constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM>);
-  constexpr unsigned shares = kSms * attn_blocks<DIM>;
+  constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM, ROWS>);
+  constexpr unsigned shares = kSms * attn_blocks<DIM, ROWS>;
   static std::atomic<int> done[64], done_join[64];
-  cudaError_t e = allow_shared(cache_attention_kernel<T, FP4, DIM>, shared, done);
-  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, kAttnRows, DIM>, 0, done_join);
+  cudaError_t e = allow_shared(cache_attention_kernel<T, FP4, DIM, ROWS>, shared, done);
+  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, ROWS, DIM>, 0, done_join);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                        attn_joins_bytes(shares));
-  e = launch_pdl(cache_attention_kernel<T, FP4, DIM>, dim3(shares), dim3(kAttnThreads), shared, s,
-                 a);
+  e = launch_pdl(cache_attention_kernel<T, FP4, DIM, ROWS>, dim3(shares), dim3(kAttnThreads), shared,
+                 s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attention_join_kernel<T, kAttnRows, DIM>,
-                    dim3(shares, kAttnRows / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
+  return launch_pdl(cache_attention_join_kernel<T, ROWS, DIM>, dim3(shares, ROWS / kJoinRows),
+                    dim3(DIM / 4, kJoinRows), 0, s, a);
+}
+
+template <typename T, bool FP4, int ROWS>
+cudaError_t attn_dim(int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
+  if (dim == 64) return attn_go<T, FP4, 64, ROWS>(a, ws, s);
+  if (dim == 128) return attn_go<T, FP4, 128, ROWS>(a, ws, s);
+  return attn_go<T, FP4, 256, ROWS>(a, ws, s);
 }
 
 template <typename T, bool FP4>
-cudaError_t attn_dim(int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
-  if (dim == 64) return attn_go<T, FP4, 64>(a, ws, s);
-  if (dim == 128) return attn_go<T, FP4, 128>(a, ws, s);
-  return attn_go<T, FP4, 256>(a, ws, s);
+cudaError_t attn_rows(int64_t average, int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
+  return average <= 8 ? attn_dim<T, FP4, 8>(dim, a, ws, s) : attn_dim<T, FP4, 16>(dim, a, ws, s);
 }
 
 AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
@@ -635,22 +699,28 @@ AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
 }  // namespace
 
 int64_t cache_attention_workspace(int64_t head_dim) {
-  const int64_t shares = kSms * (head_dim == 256 ? attn_blocks<256> : attn_blocks<128>);
-  const int64_t few = attn_bytes(shares, kAttnRows, head_dim), many = attn_rows_bytes(head_dim);
+  const bool wide = head_dim == 256;
+  const int64_t rows8 =
+      attn_bytes(kSms * (wide ? attn_blocks<256, 8> : attn_blocks<128, 8>), 8, head_dim);
+  const int64_t rows16 =
+      attn_bytes(kSms * (wide ? attn_blocks<256, 16> : attn_blocks<128, 16>), 16, head_dim);
+  const int64_t many = attn_rows_bytes(head_dim), few = rows8 > rows16 ? rows8 : rows16;
   return few > many ? few : many;
 }
 
 cudaError_t launch_cache_attention(const KvCacheArgs& c, const CacheAttentionArgs& p, int is_bf16,
                                    cudaStream_t stream) {
   const AttnArgs a = attn_args(c, p);
-  // More than 16 rows an item on average: the kernel whose tile of products has 128.
-  if (is_bf16 && c.head_dim <= 128 && p.tokens * (p.q_heads / c.heads) > kAttnRows * p.seqs)
+  // Query rows an item on average (what each sequence has is known on the device alone).  More than
+  // 16: the kernel whose tile of products has 128.  Up to 8: the form with half the products.
+  const int64_t average = (p.tokens * (p.q_heads / c.heads) + p.seqs - 1) / p.seqs;
+  if (is_bf16 && c.head_dim <= 128 && average > 16)
     return launch_attn_rows(a, c.fp4, c.head_dim, p.workspace, stream);
   if (is_bf16)
-    return c.fp4 ? attn_dim<__nv_bfloat16, true>(c.head_dim, a, p.workspace, stream)
-                 : attn_dim<__nv_bfloat16, false>(c.head_dim, a, p.workspace, stream);
-  return c.fp4 ? attn_dim<float, true>(c.head_dim, a, p.workspace, stream)
-               : attn_dim<float, false>(c.head_dim, a, p.workspace, stream);
+    return c.fp4 ? attn_rows<__nv_bfloat16, true>(average, c.head_dim, a, p.workspace, stream)
+                 : attn_rows<__nv_bfloat16, false>(average, c.head_dim, a, p.workspace, stream);
+  return c.fp4 ? attn_rows<float, true>(average, c.head_dim, a, p.workspace, stream)
+               : attn_rows<float, false>(average, c.head_dim, a, p.workspace, stream);
 }
 
 }  // namespace nr
