@@ -22,17 +22,21 @@
 namespace nr {
 namespace {
 
+// NT: tiles of eight query rows an item has.  A warp's step is 16 SUB positions: 32 where a lane's
+// codes of them fit in the registers beside O.  (One token, heads of 128 in FP8, 400009 positions in
+// 48 sequences: 16 at a time XXX us, 32 YYY us.)
+template <bool FP4, int DIM, int NT>
+constexpr int kSub = DIM == 256 || (NT == 3 && DIM == 128 && !FP4) ? 1 : 2;
 // A share for each block that fits at once on 152 SMs (any number is right).
-template <int DIM, int ROWS>
-constexpr int attn_blocks = DIM == 256 ? 2 : ROWS == 8 ? 4 : 3;
+template <int DIM, int NT>
+constexpr int attn_blocks = DIM == 256 || NT > 1 ? 2 : 3;
 constexpr int kSms = 152;
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
-constexpr int kStep = 16;          // positions a warp handles at a time
-constexpr int kAttnTile = kStep * kAttnWarps;  // positions of a block's step
-constexpr int kItemCost = 3;  // tiles that an item costs besides its own
-constexpr float kWeightUp = 16384.0f;  // weights are held times 2^14
+constexpr int kItemCost = 192;  // positions that an item costs besides its own
+constexpr float kSlack = 4.0f;  // a row's reference is behind its maximum by up to 2^4,
+constexpr float kWeightUp = 2048.0f;  // weights are held times 2^11
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -98,102 +102,49 @@ struct Layout {
   }
 };
 
-template <typename T, bool FP4, int DIM, int ROWS>
+template <typename T, bool FP4, int DIM, int NT, int STEP>
 struct AttnShared {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
   using L = Layout<FP4, DIM>;
-  // fragments: 16 rows are the first operand, 8 rows the second
-  using Fragment = typename std::conditional<ROWS == 16, uint4, uint2>::type;
-  Fragment q[SPLIT][L::kStepsK][kWarp];
+  static constexpr int ROWS = 8 * NT;
+  uint2 q[SPLIT][NT][L::kStepsK][kWarp];  // fragments
   alignas(16) float row_scale[ROWS];
-  alignas(16) int64_t at[kAttnWarps][2][kStep];        // code offsets, -1: no such position
-  float ks[kAttnWarps][kStep];             // scales of K, of V
-  float vs[kAttnWarps][kStep];
-  uint16_t km[kAttnWarps][kStep][FP4 ? L::kGroups : 1];
-  uint16_t vm[kAttnWarps][kStep][FP4 ? L::kGroups : 1];
+  alignas(16) int64_t at[kAttnWarps][2][STEP];        // code offsets, -1: no such position
+  float ks[kAttnWarps][STEP];             // scales of K, of V
+  float vs[kAttnWarps][STEP];
+  uint16_t km[kAttnWarps][STEP][FP4 ? L::kGroups : 1];
+  uint16_t vm[kAttnWarps][STEP][FP4 ? L::kGroups : 1];
   float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];
   float top[ROWS], sum[ROWS];
   alignas(16) float o[kAttnWarps][ROWS][DIM + 4];
   AttnPlan<kAttnThreads> plan;
 };
 
-template <typename T, bool FP4, int DIM, int ROWS>
-__global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
+template <typename T, bool FP4, int DIM, int NT>
+__global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
     cache_attention_kernel(const AttnArgs a) {
   using L = Layout<FP4, DIM>;
-  constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+  constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1, SUB = kSub<FP4, DIM, NT>, ROWS = 8 * NT;
+  constexpr int kStep = 16 * SUB, kAttnTile = kStep * kAttnWarps;
+  constexpr int kCost = kItemCost / kAttnTile;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM, ROWS>*>(smem_raw);
+  auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM, NT, kStep>*>(smem_raw);
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp, g = lane / 4, c = lane % 4;
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<ROWS, kAttnTile, kItemCost>(a, sh.plan);
+  make_plan<ROWS, kAttnTile, kCost>(a, sh.plan);
   const int64_t total = sh.plan.at[kAttnThreads];
   const int64_t share = share_size(total, gridDim.x);
   int64_t unit = blockIdx.x * share;
   const int64_t end = min(unit + share, total);
   if (t == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (unit >= end) return;
-  AttnItem it = locate<ROWS, kAttnTile, kItemCost>(a, sh.plan, unit);
+  AttnItem it = locate<ROWS, kAttnTile, kCost>(a, sh.plan, unit);
 
   while (unit < end) {
     const AttnSeq<kAttnTile> seq(a, it.seq);
     const int rows_left = seq.queries * static_cast<int>(a.group.div) - it.rb * ROWS;
     const int rows = min(rows_left, ROWS);
     const int steps = static_cast<int>(min(static_cast<int64_t>(seq.tiles - it.tile), end - unit));
-
-    // Q's rows as fragments: eight threads a row, each DIM / 8 elements
-    {
-      const int r = t / 8, part = t % 8;
-      constexpr int N = DIM / 8;
-      float x[N], top = 0.0f;
-      const int row = it.rb * ROWS + r;
-      const int tok = a.group.quot(row), head = it.head * a.group.div + (row - tok * a.group.div);
-      const T* p = static_cast<const T*>(a.q) + (seq.first + tok) * a.q_stride +
-                   static_cast<int64_t>(head) * DIM + part * N;
-#pragma unroll
-      for (int i = 0; i < N / Vec<T>::N; i++) {
-        float v[Vec<T>::N];
-        Vec<T>::unpack(r < rows ? ld_param(p + i * Vec<T>::N) : make_uint4(0u, 0u, 0u, 0u), v);
-#pragma unroll
-        for (int e = 0; e < Vec<T>::N; e++) x[i * Vec<T>::N + e] = v[e];
-      }
-      top = group_max<8>(max_abs(x));
-      // times 2^(14 - e) for top in [2^e, 2^(e + 1)) (rows below 2^-100: 2^114)
-      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127;
-      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-      if (part == 0 && r < ROWS)
-        sh.row_scale[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
-#pragma unroll
-      for (int i = 0; i < N; i++) {
-        const int d = part * N + i;
-        constexpr int P = L::kPieceK;
-        const int k = d / (4 * P) * (P / 4) + d % P / 4, lc = d % (4 * P) / P, sub = d % 4;
-        const int at = ROWS == 16 ? ((r % 8) * 4 + lc) * 8 + ((sub / 2) * 2 + r / 8) * 2 + sub % 2
-                                  : (r * 4 + lc) * 4 + sub;  // halves
-        if (r >= ROWS) continue;
-        const float v = x[i] * up;
-        const __half hi = __float2half_rn(v);
-        reinterpret_cast<__half*>(sh.q[0][k])[at] = hi;
-        if (SPLIT == 2)
-          reinterpret_cast<__half*>(sh.q[SPLIT - 1][k])[at] = __float2half_rn(v - __half2float(hi));
-      }
-    }
-    __syncthreads();
-    // A lane's two rows: with 16 they are rows of the scores' fragment (positions its columns),
-    // with 8 its columns (positions its rows): half the products, and half of O.
-    const int r0 = ROWS == 16 ? g : 2 * c, r1 = ROWS == 16 ? g + 8 : 2 * c + 1;
-    const float rs0 = sh.row_scale[r0], rs1 = sh.row_scale[r1];
-    const int row0 = it.rb * ROWS + r0, row1 = it.rb * ROWS + r1;
-    const int tok0 = a.group.quot(row0), tok1 = a.group.quot(row1);
-
-    constexpr int kTilesO = L::kTilesV * ROWS / 16;
-    float o[kTilesO][4];
-#pragma unroll
-    for (int j = 0; j < kTilesO; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    float m0 = -__builtin_huge_valf(), m1 = m0, l0 = 0.0f, l1 = 0.0f;
-    // A row's weights are held relative to the largest V scale that it has met, as a power of two
-    // (so that a step's result does not depend on it but where weights leave f16's range).
-    float vref0 = 0.0f, vref1 = 0.0f;
 
     // --- the pipeline's stages
     const unsigned char* kc = a.side[0].codes + it.head * L::kCodeRow;
@@ -252,45 +203,118 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
       return __all_sync(0xFFFFFFFFu,
                         lane >= kStep || (block >= 0 && block < a.blocks && p < seq.context));
     };
-    Words<L::kBytesK> k[2];
-    Words<L::kBytesV> v[4];
+    Words<L::kBytesK> k[SUB][2];
+    Words<L::kBytesV> v[SUB][4];
     auto load_k = [&](int i) {
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
+      for (int n = 0; n < 2 * SUB; n++) {
         const int64_t at = sh.at[warp][i & 1][8 * n + g];
         constexpr int bytes = L::kPieceK * (FP4 ? 1 : 2) / 2;  // of a vector
-        k[n].load(kc + at + bytes * c, 4 * bytes, at >= 0);
+        k[n / 2][n % 2].load(kc + at + bytes * c, 4 * bytes, at >= 0);
       }
     };
     auto load_v = [&](int i) {
 #pragma unroll
-      for (int n = 0; n < 4; n++) {
+      for (int n = 0; n < 4 * SUB; n++) {
         const int64_t at = sh.at[warp][i & 1][(n / 2) * 8 + 2 * c + n % 2];
         constexpr int bytes = L::kPieceV * (FP4 ? 1 : 2) / 2;
-        v[n].load(vc + at + bytes * g, 8 * bytes, at >= 0);
+        v[n / 4][n % 4].load(vc + at + bytes * g, 8 * bytes, at >= 0);
       }
     };
 
     int block = lookup(0);
+    const int after = lookup(1);
+    // Q's rows, eight threads a row, each DIM / 8 elements: on their way
+    constexpr int kPasses = (NT + 1) / 2, N = DIM / 8;
+    uint4 qx[kPasses][N / Vec<T>::N];
+    const int eighth = t % 8;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; pass++) {
+      const int r = 16 * pass + t / 8;
+      const int row = it.rb * ROWS + (r < rows ? r : 0);
+      const int tok = a.group.quot(row), head = it.head * a.group.div + (row - tok * a.group.div);
+      const T* p = static_cast<const T*>(a.q) + (seq.first + tok) * a.q_stride +
+                   static_cast<int64_t>(head) * DIM + eighth * N;
+#pragma unroll
+      for (int i = 0; i < N / Vec<T>::N; i++)
+        qx[pass][i] = r < rows ? ld_param(p + i * Vec<T>::N) : make_uint4(0u, 0u, 0u, 0u);
+    }
     bool clean = place(0, block);
-    block = lookup(1);
+    block = after;
     __syncwarp();
     load_k(0);
     load_v(0);
+    // as fragments
+#pragma unroll
+    for (int pass = 0; pass < kPasses; pass++) {
+      const int r = 16 * pass + t / 8;
+      float x[N], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N / Vec<T>::N; i++) {
+        float v[Vec<T>::N];
+        Vec<T>::unpack(qx[pass][i], v);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; e++) x[i * Vec<T>::N + e] = v[e];
+      }
+      top = group_max<8>(max_abs(x));
+      // times 2^(14 - e) for top in [2^e, 2^(e + 1)) (rows below 2^-100: 2^114)
+      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 254) - 127;
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      if (r < ROWS) {
+        if (eighth == 0)
+          sh.row_scale[r] =
+              a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          const int d = eighth * N + i;
+          constexpr int P = L::kPieceK;
+          const int k = d / (4 * P) * (P / 4) + d % P / 4, lc = d % (4 * P) / P;
+          const int at = (r % 8 * 4 + lc) * 4 + d % 4;  // halves
+          const float v = x[i] * up;
+          const __half hi = __float2half_rn(v);
+          reinterpret_cast<__half*>(sh.q[0][r / 8][k])[at] = hi;
+          if (SPLIT == 2)
+            reinterpret_cast<__half*>(sh.q[SPLIT - 1][r / 8][k])[at] =
+                __float2half_rn(v - __half2float(hi));
+        }
+      }
+    }
+    __syncthreads();
+
+    // A lane's rows: 8 n + 2 c + e, e 0 or 1.  Positions are the rows of a fragment of scores, query
+    // rows its columns: of 16 positions a lane has g and g + 8.
+    float rs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) rs[n][e] = sh.row_scale[8 * n + 2 * c + e];
+    constexpr int kTilesO = DIM / 16;
+    float o[NT][kTilesO][4];
+    float m[NT][2], l[NT][2];
+    // A row's weights are held relative to the largest V scale that it has met, as a power of two
+    // (so that a step's result does not depend on it but where weights leave f16's range).
+    float vref[NT][2], vref_low = 0.0f;  // (the smallest of any row)
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int j = 0; j < kTilesO; j++) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; e++) m[n][e] = -__builtin_huge_valf(), l[n][e] = vref[n][e] = 0.0f;
+    }
 
     for (int i = 0; i < steps; i++) {
       // scales of this step to shared memory, the next one's on their way
       if (FP4 && lane < kStep) {
-        uint16_t m[L::kGroups];
-        ks = mx_multipliers(kb, m);
+        uint16_t mul[L::kGroups];
+        ks = mx_multipliers(kb, mul);
 #pragma unroll
-        for (int e = 0; e < L::kGroups; e++) sh.km[warp][lane][FP4 ? e : 0] = m[e];
-        vs = mx_multipliers(vb, m);
+        for (int e = 0; e < L::kGroups; e++) sh.km[warp][lane][FP4 ? e : 0] = mul[e];
+        vs = mx_multipliers(vb, mul);
 #pragma unroll
-        for (int e = 0; e < L::kGroups; e++) sh.vm[warp][lane][FP4 ? e : 0] = m[e];
+        for (int e = 0; e < L::kGroups; e++) sh.vm[warp][lane][FP4 ? e : 0] = mul[e];
       }
       if (lane < kStep) sh.ks[warp][lane] = ks, sh.vs[warp][lane] = vs;
-      const float vs_now = vs;
+      const float own = lane < kStep ? scale_reference(vs) : 0.0f;
       const bool was_clean = clean;
       const bool more = i + 1 < steps;
       if (more) {
@@ -299,191 +323,167 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
       }
       __syncwarp();
 
-      // Scores: s[n][e], element e of position fragment n (16 rows: n-th eight positions; 8 rows: one
-      // fragment of all 16).
-      constexpr int kN = ROWS / 8;
-      float s[kN][4];
+      // Scores: s[u][n][e], position 16 u + g + 8 (e / 2), row 8 n + 2 c + e % 2.
+      float s[SUB][NT][4];
 #pragma unroll
-      for (int n = 0; n < kN; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int u = 0; u < SUB; u++)
+#pragma unroll
+        for (int n = 0; n < NT; n++) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
 #pragma unroll
       for (int q = 0; q < L::kStepsK; q++) {
-        uint32_t h[2][2];  // of position 8 n + g: dimensions k_dim, + 1 and + 2, + 3
+        uint2 x[SPLIT][NT];
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-          if constexpr (!FP4) {
-            h[n][0] = half2_of_e4m3(k[n].w[q]);
-            h[n][1] = half2_of_e4m3(k[n].w[q] >> 16);
-          } else {
-            uint32_t w[4];
-            half2_of_e2m1(k[n].w[q / 2], w);
-            const uint32_t f = sh.km[warp][8 * n + g][L::k_dim(0, q) / 32 +
-                                                     (L::kPieceK == 32 ? c : c / 2)] *
-                               0x10001u;
-            h[n][0] = mul_half2(w[q % 2 * 2], f);
-            h[n][1] = mul_half2(w[q % 2 * 2 + 1], f);
-          }
-        }
+        for (int part = 0; part < SPLIT; part++)
 #pragma unroll
-        for (int part = 0; part < SPLIT; part++) {
-          const auto x = sh.q[part][q][lane];
-          if constexpr (ROWS == 16) {
-            mma_f16(s[0], x, h[0][0], h[0][1]);
-            mma_f16(s[1], x, h[1][0], h[1][1]);
-          } else {
-            mma_f16(s[0], make_uint4(h[0][0], h[1][0], h[0][1], h[1][1]), x.x, x.y);
+          for (int n = 0; n < NT; n++) x[part][n] = sh.q[part][n][q][lane];
+#pragma unroll
+        for (int u = 0; u < SUB; u++) {
+          uint32_t h[2][2];  // of position 8 n + g: dimensions k_dim, + 1 and + 2, + 3
+#pragma unroll
+          for (int n = 0; n < 2; n++) {
+            if constexpr (!FP4) {
+              h[n][0] = half2_of_e4m3(k[u][n].w[q]);
+              h[n][1] = half2_of_e4m3(k[u][n].w[q] >> 16);
+            } else {
+              uint32_t w[4];
+              half2_of_e2m1(k[u][n].w[q / 2], w);
+              const uint32_t f = sh.km[warp][16 * u + 8 * n + g][L::k_dim(0, q) / 32 +
+                                                                 (L::kPieceK == 32 ? c : c / 2)] *
+                                 0x10001u;
+              h[n][0] = mul_half2(w[q % 2 * 2], f);
+              h[n][1] = mul_half2(w[q % 2 * 2 + 1], f);
+            }
           }
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int part = 0; part < SPLIT; part++)
+              mma_f16(s[u][n], make_uint4(h[0][0], h[1][0], h[0][1], h[1][1]), x[part][n].x,
+                      x[part][n].y);
         }
       }
       if (more) load_k(i + 1);
 
-      // In units of log2.  Element e of fragment n: row r0 or r1, position at(n, e).
-      auto at = [&](int n, int e) { return ROWS == 16 ? 8 * n + 2 * c + e % 2 : g + 8 * (e / 2); };
-      auto second = [](int e) { return ROWS == 16 ? e >= 2 : e % 2 == 1; };  // of r1
-      float mx0 = m0, mx1 = m1;
-      float sv[kN][2];  // V's scales of the lane's positions
-      {
-        float sk[kN][2];
+      // in units of log2
+      float sv[SUB][2];  // V's scales of the lane's positions
 #pragma unroll
-        for (int n = 0; n < kN; n++) {
-          if (ROWS == 16) {
-            const float2 x = *reinterpret_cast<const float2*>(&sh.ks[warp][8 * n + 2 * c]);
-            const float2 y = *reinterpret_cast<const float2*>(&sh.vs[warp][8 * n + 2 * c]);
-            sk[n][0] = x.x, sk[n][1] = x.y, sv[n][0] = y.x, sv[n][1] = y.y;
-          } else {
-            sk[n][0] = sh.ks[warp][g], sk[n][1] = sh.ks[warp][g + 8];
-            sv[n][0] = sh.vs[warp][g], sv[n][1] = sh.vs[warp][g + 8];
-          }
+      for (int u = 0; u < SUB; u++)
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            s[n][e] *= sk[n][ROWS == 16 ? e % 2 : e / 2] * (second(e) ? rs1 : rs0);
+        for (int h = 0; h < 2; h++) {
+          sv[u][h] = sh.vs[warp][16 * u + 8 * h + g];
+          const float sk = sh.ks[warp][16 * u + 8 * h + g];
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) s[u][n][2 * h + e] *= sk * rs[n][e];
         }
-      }
-      uint32_t hidden = 0;  // bit 4 n + e: not seen
+      float vt[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) vt[n][0] = vt[n][1] = own;
+      uint32_t hidden[SUB];  // bit 4 n + e: not seen
+      bool higher = own > vref_low;
+#pragma unroll
+      for (int u = 0; u < SUB; u++) hidden[u] = 0u;
       if (!was_clean) {
-        const int rows_end = it.rb * ROWS + rows;
+        higher = false;
 #pragma unroll
-        for (int n = 0; n < kN; n++)
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const int p = base0 + i * kAttnTile + at(n, e);
-            const bool there = sh.at[warp][i & 1][at(n, e)] >= 0;
-            if (!(there && (second(e) ? row1 : row0) < rows_end &&
-                  attn_sees(a, seq, second(e) ? tok1 : tok0, p))) {
-              hidden |= 1u << (4 * n + e);
-              s[n][e] = -__builtin_huge_valf();
+          for (int e = 0; e < 2; e++) {
+            vt[n][e] = 0.0f;
+            const int r = 8 * n + 2 * c + e, tok = a.group.quot(it.rb * ROWS + r);
+#pragma unroll
+            for (int u = 0; u < SUB; u++)
+#pragma unroll
+              for (int h = 0; h < 2; h++) {
+                const int at = 16 * u + 8 * h + g;
+                if (r < rows && sh.at[warp][i & 1][at] >= 0 &&
+                    attn_sees(a, seq, tok, base0 + i * kAttnTile + at)) {
+                  vt[n][e] = fmaxf(vt[n][e], scale_reference(sv[u][h]));
+                } else {
+                  hidden[u] |= 1u << (4 * n + 2 * h + e);
+                  s[u][n][2 * h + e] = -__builtin_huge_valf();
+                }
+              }
+            higher = higher || vt[n][e] > vref[n][e];
+          }
+      }
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          mx[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+          for (int u = 1; u < SUB; u++)
+            mx[n][e] = fmaxf(mx[n][e], fmaxf(s[u][n][e], s[u][n][2 + e]));
+          higher = higher || mx[n][e] > m[n][e] + kSlack;
+        }
+      // Seldom after an item's first step: references stay until a maximum is 2^kSlack above.
+      if (__any_sync(0xFFFFFFFFu, higher)) {
+        float low = __builtin_huge_valf();
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float top = fmaxf(mx[n][e], m[n][e]), vtop = fmaxf(vt[n][e], vref[n][e]);
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) {  // the lanes that share a row
+              top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+              vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
+            }
+            if (was_clean)  // lanes' own positions: those of every row
+#pragma unroll
+              for (int d = 1; d <= 2; d <<= 1)
+                vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
+            float f = top == m[n][e] ? 1.0f : attn_exp2(m[n][e] - top);
+            l[n][e] *= f;
+            f *= vref[n][e] * power_reciprocal(vtop);
+#pragma unroll
+            for (int j = 0; j < kTilesO; j++) {
+              o[n][j][e] *= f;
+              o[n][j][2 + e] *= f;
+            }
+            m[n][e] = top;
+            vref[n][e] = vtop;
+            low = fminf(low, vtop);
+          }
+        vref_low = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(low)));
+      }
+      // The weights as the second product's fragments: p[u][n][part], pairs of positions of a row.
+      uint32_t p[SUB][NT][SPLIT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        float use[2], winv[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          use[e] = m[n][e] == -__builtin_huge_valf() ? 0.0f : m[n][e];
+          winv[e] = kWeightUp * power_reciprocal(vref[n][e]);
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; u++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              w[e] = attn_exp2(s[u][n][2 * h + e] - use[e]);
+              l[n][e] += w[e];
+              w[e] *= sv[u][h] * winv[e];
+              if (!was_clean && (hidden[u] >> (4 * n + 2 * h + e) & 1u)) w[e] = 0.0f;  // whatever its scale
+            }
+            const uint32_t first = half2_of(w[0], w[1]);
+            p[u][n][0][h] = transposed(first);
+            if (SPLIT == 2) {
+              const float2 f = floats_of_half2(first);
+              p[u][n][SPLIT - 1][h] = transposed(half2_of(w[0] - f.x, w[1] - f.y));
             }
           }
       }
-#pragma unroll
-      for (int n = 0; n < kN; n++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          if (second(e)) mx1 = fmaxf(mx1, s[n][e]);
-          else mx0 = fmaxf(mx0, s[n][e]);
-        }
-      // the lanes that share a row
-      constexpr int kFirst = ROWS == 16 ? 1 : 4, kLast = ROWS == 16 ? 2 : 16;
-#pragma unroll
-      for (int d = kFirst; d <= kLast; d <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
-      }
-      float vt0, vt1;
-      if (was_clean) {
-        const float own = lane < kStep ? scale_reference(vs_now) : 0.0f;
-        vt0 = vt1 = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(own)));
-      } else {
-        vt0 = vt1 = 0.0f;
-#pragma unroll
-        for (int n = 0; n < kN; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            if (hidden >> (4 * n + e) & 1u) continue;
-            const float x = scale_reference(sv[n][ROWS == 16 ? e % 2 : e / 2]);
-            if (second(e)) vt1 = fmaxf(vt1, x);
-            else vt0 = fmaxf(vt0, x);
-          }
-#pragma unroll
-        for (int d = kFirst; d <= kLast; d <<= 1) {
-          vt0 = fmaxf(vt0, __shfl_xor_sync(0xFFFFFFFFu, vt0, d));
-          vt1 = fmaxf(vt1, __shfl_xor_sync(0xFFFFFFFFu, vt1, d));
-        }
-      }
-      vt0 = fmaxf(vt0, vref0);
-      vt1 = fmaxf(vt1, vref1);
-      const float use0 = mx0 == -__builtin_huge_valf() ? 0.0f : mx0;
-      const float use1 = mx1 == -__builtin_huge_valf() ? 0.0f : mx1;
-      if (__any_sync(0xFFFFFFFFu, mx0 > m0 || mx1 > m1 || vt0 > vref0 || vt1 > vref1)) {
-        float f0 = attn_exp2(m0 - use0), f1 = attn_exp2(m1 - use1);
-        l0 *= f0;
-        l1 *= f1;
-        f0 *= vref0 * power_reciprocal(vt0);
-        f1 *= vref1 * power_reciprocal(vt1);
-#pragma unroll
-        for (int j = 0; j < kTilesO; j++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) o[j][e] *= second(e) ? f1 : f0;
-        m0 = mx0;
-        m1 = mx1;
-        vref0 = vt0;
-        vref1 = vt1;
-      }
-      const float winv0 = kWeightUp * power_reciprocal(vref0);
-      const float winv1 = kWeightUp * power_reciprocal(vref1);
-      float w[kN][4];
-#pragma unroll
-      for (int n = 0; n < kN; n++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          w[n][e] = attn_exp2(s[n][e] - (second(e) ? use1 : use0));
-          if (second(e)) l1 += w[n][e];
-          else l0 += w[n][e];
-          w[n][e] *= sv[n][ROWS == 16 ? e % 2 : e / 2] * (second(e) ? winv1 : winv0);
-          if (!was_clean && (hidden >> (4 * n + e) & 1u)) w[n][e] = 0.0f;  // whatever its scale
-        }
-      // As fragments of the second product: 16 rows its first operand as they are, 8 rows its second,
-      // turned around.  p[part][0 .. 3] or [0 .. 1].
-      uint32_t p[SPLIT][2 * kN];
-#pragma unroll
-      for (int n = 0; n < kN; n++)
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const float x = w[n][2 * h], y = w[n][2 * h + 1];
-          p[0][2 * n + h] = half2_of(x, y);
-          if (SPLIT == 2) {
-            const float2 f = floats_of_half2(p[0][2 * n + h]);
-            p[SPLIT - 1][2 * n + h] = half2_of(x - f.x, y - f.y);
-          }
-        }
-      uint32_t seen[2 * kN];  // ones where a weight may be
-#pragma unroll
-      for (int n = 0; n < 2 * kN; n++)
-        seen[n] = (hidden >> (2 * n) & 1u ? 0u : 0x3C00u) | (hidden >> (2 * n + 1) & 1u ? 0u : 0x3C000000u);
-      if constexpr (ROWS == 8) {
-#pragma unroll
-        for (int n = 0; n < 2; n++) {
-#pragma unroll
-          for (int part = 0; part < SPLIT; part++) p[part][n] = transposed(p[part][n]);
-          if (!was_clean) seen[n] = transposed(seen[n]);
-        }
-      }
 
-      // The second product, for output tiles j and j + 1: x and y pairs of positions (2 c, 2 c + 1; 8
-      // further) of each one's dimension.
-      auto product = [&](int j, uint32_t x0, uint32_t y0, uint32_t x1, uint32_t y1) {
-        auto both = [&](float (&d)[4], float (&d2)[4], const uint32_t (&f)[2 * kN], uint32_t x0, uint32_t y0,
-                        uint32_t x1, uint32_t y1) {
-          if constexpr (ROWS == 16) {
-            const uint4 rows16 = make_uint4(f[0], f[1], f[2 * kN - 2], f[2 * kN - 1]);
-            mma_f16(d, rows16, x0, y0);
-            mma_f16(d2, rows16, x1, y1);
-          } else {
-            mma_f16(d, make_uint4(x0, x1, y0, y1), f[0], f[1]);
-          }
-        };
-        constexpr int kPer = ROWS == 16 ? 1 : 2;  // output tiles a fragment
-        float(&d)[4] = o[j / kPer];
-        float(&d2)[4] = o[(j + 1) / kPer];
+      // The second product, for dimensions' tiles 2 j and 2 j + 1: x and y pairs of positions (2 c,
+      // 2 c + 1; 8 further) of each one's dimension.
+      auto product = [&](int u, int j, uint32_t x0, uint32_t y0, uint32_t x1, uint32_t y1) {
         if (!was_clean) {
           // A NaN of V reaches those who see its position and nobody else: it leaves the
           // product (0 * NaN is a NaN), and is counted.
@@ -493,54 +493,65 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
           };
           const uint32_t a0 = nan_halves(x0), b0 = nan_halves(y0), a1 = nan_halves(x1), b1 = nan_halves(y1);
           if (__any_sync(0xFFFFFFFFu, (a0 | b0 | a1 | b1) != 0)) {
-            float n0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, n1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             constexpr uint32_t one = 0x3C003C00u;
-            both(n0, n1, seen, a0 & one, b0 & one, a1 & one, b1 & one);
-            x0 &= ~a0, y0 &= ~b0, x1 &= ~a1, y1 &= ~b1;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              if (n0[e] > 0.0f) d[e] = __uint_as_float(0x7FC00000u);
-              if (ROWS == 16 && n1[e] > 0.0f) d2[e] = __uint_as_float(0x7FC00000u);
+            for (int n = 0; n < NT; n++) {
+              uint32_t seen[2];  // ones where a weight may be
+#pragma unroll
+              for (int h = 0; h < 2; h++)
+                seen[h] = transposed((hidden[u] >> (4 * n + 2 * h) & 1u ? 0u : 0x3C00u) |
+                                     (hidden[u] >> (4 * n + 2 * h + 1) & 1u ? 0u : 0x3C000000u));
+              float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_f16(count, make_uint4(a0 & one, a1 & one, b0 & one, b1 & one), seen[0], seen[1]);
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                if (count[e] > 0.0f) o[n][j][e] = __uint_as_float(0x7FC00000u);
             }
+            x0 &= ~a0, y0 &= ~b0, x1 &= ~a1, y1 &= ~b1;
           }
         }
 #pragma unroll
-        for (int part = 0; part < SPLIT; part++) both(d, d2, p[part], x0, y0, x1, y1);
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int part = 0; part < SPLIT; part++)
+            mma_f16(o[n][j], make_uint4(x0, x1, y0, y1), p[u][n][part][0], p[u][n][part][1]);
       };
-      if constexpr (!FP4) {
 #pragma unroll
-        for (int q = 0; q < L::kTilesV / 4; q++) {
+      for (int u = 0; u < SUB; u++) {
+        if constexpr (!FP4) {
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint32_t x = __byte_perm(v[0].w[q], v[1].w[q], h ? 0x7362 : 0x5140);
-            const uint32_t y = __byte_perm(v[2].w[q], v[3].w[q], h ? 0x7362 : 0x5140);
-            product(4 * q + 2 * h, half2_of_e4m3(x), half2_of_e4m3(y), half2_of_e4m3(x >> 16),
-                    half2_of_e4m3(y >> 16));
+          for (int q = 0; q < L::kTilesV / 4; q++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const uint32_t x = __byte_perm(v[u][0].w[q], v[u][1].w[q], h ? 0x7362 : 0x5140);
+              const uint32_t y = __byte_perm(v[u][2].w[q], v[u][3].w[q], h ? 0x7362 : 0x5140);
+              product(u, 2 * q + h, half2_of_e4m3(x), half2_of_e4m3(y), half2_of_e4m3(x >> 16),
+                      half2_of_e4m3(y >> 16));
+            }
+        } else {
+          constexpr int per = 32 / L::kPieceV;  // lanes g that share a scale
+          const uint16_t* f = &sh.vm[warp][16 * u][FP4 ? g / per : 0];
+          constexpr int G = FP4 ? L::kGroups : 1;
+          const uint32_t f0 = f[2 * c * G] | static_cast<uint32_t>(f[(2 * c + 1) * G]) << 16;
+          const uint32_t f1 = f[(8 + 2 * c) * G] | static_cast<uint32_t>(f[(9 + 2 * c) * G]) << 16;
+#pragma unroll
+          for (int q = 0; q < L::kTilesV / 8; q++) {
+            auto even = [](uint32_t lo, uint32_t hi) {
+              return (lo & 0x0F0F0F0Fu) | (hi & 0x0F0F0F0Fu) << 4;
+            };
+            auto odd = [](uint32_t lo, uint32_t hi) {
+              return (lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
+            };
+            uint32_t x0[4], y0[4], x1[4], y1[4];
+            half2_of_e2m1(even(v[u][0].w[q], v[u][1].w[q]), x0);
+            half2_of_e2m1(even(v[u][2].w[q], v[u][3].w[q]), y0);
+            half2_of_e2m1(odd(v[u][0].w[q], v[u][1].w[q]), x1);
+            half2_of_e2m1(odd(v[u][2].w[q], v[u][3].w[q]), y1);
+#pragma unroll
+            for (int h = 0; h < 4; h++)
+              product(u, 4 * q + h, mul_half2(x0[h], f0), mul_half2(y0[h], f1), mul_half2(x1[h], f0),
+                      mul_half2(y1[h], f1));
           }
-        }
-      } else {
-        constexpr int per = 32 / L::kPieceV;  // lanes g that share a scale
-        const uint16_t* f = &sh.vm[warp][0][FP4 ? g / per : 0];
-        constexpr int G = FP4 ? L::kGroups : 1;
-        const uint32_t f0 = f[2 * c * G] | static_cast<uint32_t>(f[(2 * c + 1) * G]) << 16;
-        const uint32_t f1 = f[(8 + 2 * c) * G] | static_cast<uint32_t>(f[(9 + 2 * c) * G]) << 16;
-#pragma unroll
-        for (int q = 0; q < L::kTilesV / 8; q++) {
-          auto even = [](uint32_t lo, uint32_t hi) {
-            return (lo & 0x0F0F0F0Fu) | (hi & 0x0F0F0F0Fu) << 4;
-          };
-          auto odd = [](uint32_t lo, uint32_t hi) {
-            return (lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
-          };
-          uint32_t x0[4], y0[4], x1[4], y1[4];
-          half2_of_e2m1(even(v[0].w[q], v[1].w[q]), x0);
-          half2_of_e2m1(even(v[2].w[q], v[3].w[q]), y0);
-          half2_of_e2m1(odd(v[0].w[q], v[1].w[q]), x1);
-          half2_of_e2m1(odd(v[2].w[q], v[3].w[q]), y1);
-#pragma unroll
-          for (int h = 0; h < 4; h++)
-            product(8 * q + 2 * h, mul_half2(x0[h], f0), mul_half2(y0[h], f1), mul_half2(x1[h], f0),
-                    mul_half2(y1[h], f1));
         }
       }
       if (more) load_v(i + 1);
@@ -548,35 +559,33 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
     }
 
     // --- the warps' results joined, in order
-    constexpr int kFirst = ROWS == 16 ? 1 : 4, kLast = ROWS == 16 ? 2 : 16;
 #pragma unroll
-    for (int d = kFirst; d <= kLast; d <<= 1) {
-      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
-      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
-    }
-    if ((ROWS == 16 ? c : g) == 0) {
-      sh.m[warp][r0] = m0;
-      sh.m[warp][r1] = m1;
-      sh.l[warp][r0] = l0;
-      sh.l[warp][r1] = l1;
-    }
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], d);
+        if (g == 0) {
+          sh.m[warp][8 * n + 2 * c + e] = m[n][e];
+          sh.l[warp][8 * n + 2 * c + e] = l[n][e];
+        }
+      }
     __syncthreads();
-    float top0 = sh.m[0][r0], top1 = sh.m[0][r1];
 #pragma unroll
-    for (int w = 1; w < kAttnWarps; w++) {
-      top0 = fmaxf(top0, sh.m[w][r0]);
-      top1 = fmaxf(top1, sh.m[w][r1]);
-    }
-    const float f0 = m0 == -__builtin_huge_valf() ? 0.0f : attn_exp2(m0 - top0);
-    const float f1 = m1 == -__builtin_huge_valf() ? 0.0f : attn_exp2(m1 - top1);
-    const float back0 = vref0 * (1.0f / kWeightUp), back1 = vref1 * (1.0f / kWeightUp);
+    for (int n = 0; n < NT; n++)
 #pragma unroll
-    for (int j = 0; j < kTilesO; j++)
+      for (int e = 0; e < 2; e++) {
+        const int r = 8 * n + 2 * c + e;
+        float top = sh.m[0][r];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const bool two = ROWS == 16 ? e >= 2 : e % 2 == 1;
-        const int d = ROWS == 16 ? L::v_dim(2 * c + e % 2, j) : L::v_dim(g, 2 * j + e / 2);
-        sh.o[warp][two ? r1 : r0][d] = o[j][e] * (two ? back1 : back0) * (two ? f1 : f0);
+        for (int w = 1; w < kAttnWarps; w++) top = fmaxf(top, sh.m[w][r]);
+        const float f = m[n][e] == -__builtin_huge_valf() ? 0.0f : attn_exp2(m[n][e] - top);
+        const float back = vref[n][e] * (1.0f / kWeightUp);
+#pragma unroll
+        for (int j = 0; j < kTilesO; j++)
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+            sh.o[warp][r][L::v_dim(g, 2 * j + h)] = o[n][j][2 * h + e] * back * f;
       }
     if (t < ROWS) {
       float top = sh.m[0][t], sum = 0.0f;
@@ -631,40 +640,46 @@ __global__ void __launch_bounds__(kAttnThreads, attn_blocks<DIM, ROWS>)
     }
     __syncthreads();  // the shared memory is written anew
 
-    unit += steps + kItemCost;
+    unit += steps + kCost;
     if (unit >= end) break;
     next_item<ROWS, kAttnTile>(a, it, seq.queries);
   }
 }
 
-template <typename T, bool FP4, int DIM, int ROWS>
+template <typename T, bool FP4, int DIM, int NT>
 cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
-  constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM, ROWS>);
-  constexpr unsigned shares = kSms * attn_blocks<DIM, ROWS>;
+  constexpr int blocks = attn_blocks<DIM, NT>, ROWS = 8 * NT;
+  constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM, NT, 16 * kSub<FP4, DIM, NT>>);
+  // Shared memory for the blocks that fit, the rest is L1, through which the codes come: 400009
+  // tokens of 48 sequences 188 us, with all of it shared memory 216 us.
+  constexpr int percent = static_cast<int>((blocks * (shared + 1024) * 100 + 228 * 1024 - 1) / (228 * 1024));
+  static_assert(percent <= 100, "blocks an SM");
+  constexpr unsigned shares = kSms * blocks;
   static std::atomic<int> done[64], done_join[64];
-  cudaError_t e = allow_shared(cache_attention_kernel<T, FP4, DIM, ROWS>, shared, done);
-  if (e == cudaSuccess) e = allow_shared(cache_attention_join_kernel<T, ROWS, DIM>, 0, done_join);
+  auto* kernel = cache_attention_kernel<T, FP4, DIM, NT>;
+  auto* join = cache_attention_join_kernel<T, ROWS, DIM>;
+  cudaError_t e = allow_shared(kernel, shared, done, percent);
+  if (e == cudaSuccess) e = allow_shared(join, 0, done_join, percent);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                        attn_joins_bytes(shares));
-  e = launch_pdl(cache_attention_kernel<T, FP4, DIM, ROWS>, dim3(shares), dim3(kAttnThreads), shared,
-                 s, a);
+  e = launch_pdl(kernel, dim3(shares), dim3(kAttnThreads), shared, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attention_join_kernel<T, ROWS, DIM>, dim3(shares, ROWS / kJoinRows),
-                    dim3(DIM / 4, kJoinRows), 0, s, a);
-}
-
-template <typename T, bool FP4, int ROWS>
-cudaError_t attn_dim(int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
-  if (dim == 64) return attn_go<T, FP4, 64, ROWS>(a, ws, s);
-  if (dim == 128) return attn_go<T, FP4, 128, ROWS>(a, ws, s);
-  return attn_go<T, FP4, 256, ROWS>(a, ws, s);
+  return launch_pdl(join, dim3(shares, ROWS / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
 }
 
 template <typename T, bool FP4>
-cudaError_t attn_rows(int64_t average, int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
-  return average <= 8 ? attn_dim<T, FP4, 8>(dim, a, ws, s) : attn_dim<T, FP4, 16>(dim, a, ws, s);
+cudaError_t attn_few(int64_t average, int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
+  if (dim == 64)
+    return average <= 8    ? attn_go<T, FP4, 64, 1>(a, ws, s)
+           : average <= 16 ? attn_go<T, FP4, 64, 2>(a, ws, s)
+                           : attn_go<T, FP4, 64, 3>(a, ws, s);
+  if (dim == 128)
+    return average <= 8    ? attn_go<T, FP4, 128, 1>(a, ws, s)
+           : average <= 16 ? attn_go<T, FP4, 128, 2>(a, ws, s)
+                           : attn_go<T, FP4, 128, 3>(a, ws, s);
+  return average <= 8 ? attn_go<T, FP4, 256, 1>(a, ws, s) : attn_go<T, FP4, 256, 2>(a, ws, s);
 }
 
 AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
@@ -699,12 +714,10 @@ AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
 }  // namespace
 
 int64_t cache_attention_workspace(int64_t head_dim) {
-  const bool wide = head_dim == 256;
-  const int64_t rows8 =
-      attn_bytes(kSms * (wide ? attn_blocks<256, 8> : attn_blocks<128, 8>), 8, head_dim);
-  const int64_t rows16 =
-      attn_bytes(kSms * (wide ? attn_blocks<256, 16> : attn_blocks<128, 16>), 16, head_dim);
-  const int64_t many = attn_rows_bytes(head_dim), few = rows8 > rows16 ? rows8 : rows16;
+  const int64_t few = head_dim == 256
+                          ? attn_bytes(kSms * attn_blocks<256, 2>, 16, head_dim)
+                          : attn_bytes(kSms * attn_blocks<128, 3>, 24, head_dim);
+  const int64_t many = attn_rows_bytes(head_dim);
   return few > many ? few : many;
 }
 
@@ -712,15 +725,15 @@ cudaError_t launch_cache_attention(const KvCacheArgs& c, const CacheAttentionArg
                                    cudaStream_t stream) {
   const AttnArgs a = attn_args(c, p);
   // Query rows an item on average (what each sequence has is known on the device alone).  More than
-  // 16: the kernel whose tile of products has 128.  Up to 8: the form with half the products.
+  // 24: the kernel whose tile of products has 128.
   const int64_t average = (p.tokens * (p.q_heads / c.heads) + p.seqs - 1) / p.seqs;
-  if (is_bf16 && c.head_dim <= 128 && average > 16)
+  if (is_bf16 && c.head_dim <= 128 && average > 24)
     return launch_attn_rows(a, c.fp4, c.head_dim, p.workspace, stream);
   if (is_bf16)
-    return c.fp4 ? attn_rows<__nv_bfloat16, true>(average, c.head_dim, a, p.workspace, stream)
-                 : attn_rows<__nv_bfloat16, false>(average, c.head_dim, a, p.workspace, stream);
-  return c.fp4 ? attn_rows<float, true>(average, c.head_dim, a, p.workspace, stream)
-               : attn_rows<float, false>(average, c.head_dim, a, p.workspace, stream);
+    return c.fp4 ? attn_few<__nv_bfloat16, true>(average, c.head_dim, a, p.workspace, stream)
+                 : attn_few<__nv_bfloat16, false>(average, c.head_dim, a, p.workspace, stream);
+  return c.fp4 ? attn_few<float, true>(average, c.head_dim, a, p.workspace, stream)
+               : attn_few<float, false>(average, c.head_dim, a, p.workspace, stream);
 }
 
 }  // namespace nr
