@@ -34,7 +34,7 @@ constexpr int kSms = 152;
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
-constexpr int kItemCost = 192;  // positions that an item costs besides its own
+constexpr int kItemCost = 3;  // tiles that an item costs besides its own
 constexpr float kSlack = 4.0f;  // a row's reference is behind its maximum by up to 2^4,
 constexpr float kWeightUp = 2048.0f;  // weights are held times 2^11
 
@@ -126,19 +126,18 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
   using L = Layout<FP4, DIM>;
   constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1, SUB = kSub<FP4, DIM, NT>, ROWS = 8 * NT;
   constexpr int kStep = 16 * SUB, kAttnTile = kStep * kAttnWarps;
-  constexpr int kCost = kItemCost / kAttnTile;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   auto& sh = *reinterpret_cast<AttnShared<T, FP4, DIM, NT, kStep>*>(smem_raw);
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp, g = lane / 4, c = lane % 4;
   pdl_enter();  // before any global read: the previous kernel may still run
-  make_plan<ROWS, kAttnTile, kCost>(a, sh.plan);
+  make_plan<ROWS, kAttnTile, kItemCost>(a, sh.plan);
   const int64_t total = sh.plan.at[kAttnThreads];
   const int64_t share = share_size(total, gridDim.x);
   int64_t unit = blockIdx.x * share;
   const int64_t end = min(unit + share, total);
   if (t == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (unit >= end) return;
-  AttnItem it = locate<ROWS, kAttnTile, kCost>(a, sh.plan, unit);
+  AttnItem it = locate<ROWS, kAttnTile, kItemCost>(a, sh.plan, unit);
 
   while (unit < end) {
     const AttnSeq<kAttnTile> seq(a, it.seq);
@@ -483,8 +482,26 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
 
       // The second product, for dimensions' tiles 2 j and 2 j + 1: x and y pairs of positions (2 c,
       // 2 c + 1; 8 further) of each one's dimension.
+      bool nans = false;  // in V, where someone does not see all
+      if (!was_clean) {
+        if constexpr (FP4) {  // of a scale
+#pragma unroll
+          for (int e = 0; e < L::kGroups; e++) nans = nans || (lane < kStep && sh.vm[warp][lane % kStep][FP4 ? e : 0] == 0x7E00);
+        } else {
+          uint32_t full = 0u;
+#pragma unroll
+          for (int u = 0; u < SUB; u++)
+#pragma unroll
+            for (int n = 0; n < 4; n++)
+#pragma unroll
+              for (int q = 0; q < L::kBytesV / 4; q++)
+                full |= (v[u][n].w[q] & 0x7F7F7F7Fu) + 0x01010101u;
+          nans = (full & 0x80808080u) != 0u;
+        }
+        nans = __any_sync(0xFFFFFFFFu, nans);
+      }
       auto product = [&](int u, int j, uint32_t x0, uint32_t y0, uint32_t x1, uint32_t y1) {
-        if (!was_clean) {
+        if (nans) {
           // A NaN of V reaches those who see its position and nobody else: it leaves the
           // product (0 * NaN is a NaN), and is counted.
           auto nan_halves = [](uint32_t h) {
@@ -492,23 +509,21 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
                    ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
           };
           const uint32_t a0 = nan_halves(x0), b0 = nan_halves(y0), a1 = nan_halves(x1), b1 = nan_halves(y1);
-          if (__any_sync(0xFFFFFFFFu, (a0 | b0 | a1 | b1) != 0)) {
-            constexpr uint32_t one = 0x3C003C00u;
+          constexpr uint32_t one = 0x3C003C00u;
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-              uint32_t seen[2];  // ones where a weight may be
+          for (int n = 0; n < NT; n++) {
+            uint32_t seen[2];  // ones where a weight may be
 #pragma unroll
-              for (int h = 0; h < 2; h++)
-                seen[h] = transposed((hidden[u] >> (4 * n + 2 * h) & 1u ? 0u : 0x3C00u) |
-                                     (hidden[u] >> (4 * n + 2 * h + 1) & 1u ? 0u : 0x3C000000u));
-              float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_f16(count, make_uint4(a0 & one, a1 & one, b0 & one, b1 & one), seen[0], seen[1]);
+            for (int h = 0; h < 2; h++)
+              seen[h] = transposed((hidden[u] >> (4 * n + 2 * h) & 1u ? 0u : 0x3C00u) |
+                                   (hidden[u] >> (4 * n + 2 * h + 1) & 1u ? 0u : 0x3C000000u));
+            float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(count, make_uint4(a0 & one, a1 & one, b0 & one, b1 & one), seen[0], seen[1]);
 #pragma unroll
-              for (int e = 0; e < 4; e++)
-                if (count[e] > 0.0f) o[n][j][e] = __uint_as_float(0x7FC00000u);
-            }
-            x0 &= ~a0, y0 &= ~b0, x1 &= ~a1, y1 &= ~b1;
+            for (int e = 0; e < 4; e++)
+              if (count[e] > 0.0f) o[n][j][e] = __uint_as_float(0x7FC00000u);
           }
+          x0 &= ~a0, y0 &= ~b0, x1 &= ~a1, y1 &= ~b1;
         }
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -640,7 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
     }
     __syncthreads();  // the shared memory is written anew
 
-    unit += steps + kCost;
+    unit += steps + kItemCost;
     if (unit >= end) break;
     next_item<ROWS, kAttnTile>(a, it, seq.queries);
   }
