@@ -141,7 +141,8 @@ struct RowsShared {
       o_full[2], meta_full[kMeta], done;
   alignas(16) float ks[kMeta][kPos];
   alignas(16) float vs[kMeta][kPos];
-  alignas(16) float vtop[kMeta][kLoadWarps];           // largest reference of V's scales
+  alignas(16) float vr[kMeta][kPos];          // references of V's scales,
+  alignas(16) float vtop[kMeta][kLoadWarps];  // the largest
   alignas(16) uint16_t there[kMeta][kLoadWarps];       // positions that are in the cache
   alignas(16) unsigned char clean[kMeta][kLoadWarps];  // every position there, seen by every row
   float row_scale[kItems][kRows];
@@ -235,42 +236,16 @@ struct RowsLane {
   }
 };
 
-// One thread's row of a tile of scores: the largest score before the row's own factor, over the
-// positions whose bits are set (ALL: every one).
+// One thread's row of a tile of scores, over the positions whose bits are set (ALL: every one): the
+// weights e^(score - m), summed; times V's scales and `up` as f16 to p_at.  `mx`: the largest score
+// before the row's own factor.
 template <bool ALL>
-__device__ __forceinline__ float rows_largest(unsigned s_at, const float* ks, const uint32_t (&see)[4]) {
-  float mx = kNone;
-  uint32_t x[32];
-#pragma unroll 1
-  for (int j = 0; j < 4; j++) {
-    tmem_load(s_at + 32 * j, x);
-    tmem_loaded(x);
-    const float4* k4 = reinterpret_cast<const float4*>(ks + 32 * j);
-    const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const float4 k = k4[e];
-      float u[4];
-      split(mul2(f2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), f2(k.x, k.y)), u[0], u[1]);
-      split(mul2(f2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), f2(k.z, k.w)), u[2],
-            u[3]);
-      if (!ALL) {
-#pragma unroll
-        for (int h = 0; h < 4; h++)
-          if (!(bits >> (4 * e + h) & 1u)) u[h] = kNone;
-      }
-      mx = fmaxf(mx, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
-    }
-  }
-  return mx;
-}
-
-// Its weights e^(score - m), summed; times V's scales and `up` as f16 over the scores.
-template <bool ALL>
-__device__ __forceinline__ float rows_weigh(unsigned s_at, const float* ks, const float* vs,
-                                            const uint32_t (&see)[4], float rs, float neg, float up) {
+__device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const float* ks,
+                                            const float* vs, const uint32_t (&see)[4], float rs,
+                                            float neg, float up, float& mx) {
   const F2 rs2 = f2(rs, rs), neg2 = f2(neg, neg), up2 = f2(up, up);
   F2 l2 = f2(0.0f, 0.0f);
+  mx = kNone;
   uint32_t x[32];
 #pragma unroll 1
   for (int j = 0; j < 4; j++) {
@@ -285,12 +260,14 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, const float* ks, cons
       const float4 k = k4[e / 2], v = v4[e / 2];
       const F2 kk = e % 2 ? f2(k.z, k.w) : f2(k.x, k.y);
       const F2 vv = e % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
+      const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
+      const F2 score = mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk);
       float u[2];
-      split(fma2(mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk), rs2, neg2), u[0],
-            u[1]);
+      split(score, u[0], u[1]);
+      mx = fmaxf(mx, fmaxf(s0 ? u[0] : kNone, s1 ? u[1] : kNone));
+      split(fma2(score, rs2, neg2), u[0], u[1]);
       u[0] = attn_exp2(u[0]);
       u[1] = attn_exp2(u[1]);
-      const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
       if (!s0) u[0] = 0.0f;
       if (!s1) u[1] = 0.0f;
       const F2 weight = f2(u[0], u[1]);
@@ -300,7 +277,7 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, const float* ks, cons
       if (!s1) u[1] = 0.0f;
       p[e] = half2_of(u[0], u[1]);
     }
-    tmem_store16(s_at + 16 * j, p);
+    tmem_store16(p_at + 16 * j, p);
   }
   float lo, hi;
   split(l2, lo, hi);
@@ -340,7 +317,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   using T = __nv_bfloat16;
   using Sh = RowsShared<FP4, DIM>;
   constexpr int kCodeRow = FP4 ? DIM / 2 : DIM;  // bytes of a head
-  constexpr unsigned kCols = 512;                // S twice 128, O 128
+  constexpr unsigned kCols = 512;                // S twice 128, O 128, the weights twice 64
   extern __shared__ __align__(16) unsigned char smem_raw[];
   // the swizzle goes by address: operands start at multiples of 1024
   auto& sh = *reinterpret_cast<Sh*>(
@@ -442,8 +419,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                   bits &= there;
                 }
                 see[j] = bits;
-                for (int e = 0; e < 32; e++)
-                  if (bits >> e & 1u) vt = fmaxf(vt, scale_reference(vs[32 * j + e]));
+                const float4* ref = reinterpret_cast<const float4*>(&sh.vr[g % kMeta][32 * j]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                  const float4 x = ref[e];
+                  vt = fmaxf(vt, fmaxf(fmaxf(bits >> (4 * e) & 1u ? x.x : 0.0f,
+                                             bits >> (4 * e + 1) & 1u ? x.y : 0.0f),
+                                       fmaxf(bits >> (4 * e + 2) & 1u ? x.z : 0.0f,
+                                             bits >> (4 * e + 3) & 1u ? x.w : 0.0f)));
+                }
               }
             } else {
               const float4 x = *reinterpret_cast<const float4*>(&sh.vtop[g % kMeta][0]);
@@ -453,12 +437,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             vt = fmaxf(vt, vref);
             __syncwarp();
-            // the largest score
-            float mx = clean ? rows_largest<true>(s_at, ks, see) : rows_largest<false>(s_at, ks, see);
-            if (mx > kNone) mx *= rs;
-            // the reference moves, and the row of O with it
-            const bool need = mx > (m == kNone ? kNone : m + kHeadroom) || vt > vref;
-            if (__any_sync(0xFFFFFFFFu, need)) {
+            // With the reference that the row has, and once more where it has to move: at an item's
+            // first tile, seldom after it.
+            float lt, mx;
+#pragma unroll 1
+            for (int turn = 0;; turn++) {
+              const float neg = m == kNone ? 0.0f : -m;
+              const float up = kHeldUp * power_reciprocal(vref);
+              const unsigned p_at = mine + 3 * kPos + b * (kPos / 2);
+              lt = clean ? rows_weigh<true>(s_at, p_at, ks, vs, see, rs, neg, up, mx)
+                         : rows_weigh<false>(s_at, p_at, ks, vs, see, rs, neg, up, mx);
+              if (mx > kNone) mx *= rs;
+              const bool need = mx > (m == kNone ? kNone : m + kHeadroom) || vt > vref;
+              if (turn == 1 || !__any_sync(0xFFFFFFFFu, need)) break;
+              // the row of O moves with it
               float f = 1.0f;
               if (need) {
                 const float to = fmaxf(m, mx);
@@ -485,10 +477,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 tmem_stored();
               }
             }
-            const float neg = m == kNone ? 0.0f : -m;
-            const float up = kHeldUp * power_reciprocal(vref);
-            l += clean ? rows_weigh<true>(s_at, ks, vs, see, rs, neg, up)
-                       : rows_weigh<false>(s_at, ks, vs, see, rs, neg, up);
+            l += lt;
             tmem_stored();
           }
           tc_before();
@@ -585,12 +574,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const unsigned char* vc = a.side[1].codes + from;
         const int base0 = w.it.tile * kPos + lw * kPer;
         auto lookup = [&](int i) {
+          // what the table says, looked at a step later: a comparison here would wait for it
           const int p = base0 + i * kPos + lane;
           if (lane >= kPer || i >= steps || p >= seq.length) return -1;
           const int64_t page = a.page.quot(p);
-          if (page >= a.width) return -1;
-          const int blk = a.table[w.it.seq * a.width + page];
-          return blk >= 0 && blk < a.blocks ? blk : -1;
+          return page < a.width ? a.table[w.it.seq * a.width + page] : -1;
         };
         float ks = 0.0f, vs = 0.0f;
         uint64_t kb = 0, vb = 0;
@@ -601,7 +589,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           int64_t at = -1;
           ks = vs = 0.0f;
           kb = vb = 0;
-          if (blk >= 0) {
+          if (blk >= 0 && blk < a.blocks) {
             const int64_t in = p - static_cast<int64_t>(a.page.quot(p)) * a.page.div;
             at = blk * a.geo.code_block_stride + in * a.geo.code_row;
             const int64_t sc = blk * a.geo.scale_block_stride + in * a.geo.scale_row;
@@ -692,11 +680,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             clean = __all_sync(0xFFFFFFFFu, lane >= kPer || (in && p0 + lane < seq.context));
             const unsigned there = __ballot_sync(0xFFFFFFFFu, in);
-            const float top = __uint_as_float(__reduce_max_sync(
-                0xFFFFFFFFu, lane < kPer ? __float_as_uint(scale_reference(vs)) : 0u));
+            const float ref = lane < kPer ? scale_reference(vs) : 0.0f;
+            const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(ref)));
             if (lane < kPer) {
               sh.ks[g % kMeta][lw * kPer + lane] = ks;
               sh.vs[g % kMeta][lw * kPer + lane] = vs;
+              sh.vr[g % kMeta][lw * kPer + lane] = ref;
             }
             if (lane == 0) {
               sh.there[g % kMeta][lw] = static_cast<uint16_t>(there);
@@ -766,7 +755,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const uint64_t v = operand(smem_addr(sh.v[b]), Sh::kBlockBytes);
 #pragma unroll
           for (int s = 0; s < kPos / 16; s++)
-            mma_ts(tmem + 2 * kPos, tmem + b * kPos + s * 8, v + (s * 2048 >> 4), product_of(DIM, true),
+            mma_ts(tmem + 2 * kPos, tmem + 3 * kPos + b * (kPos / 2) + s * 8, v + (s * 2048 >> 4), product_of(DIM, true),
                    i > 0 || s > 0);
           tc_commit(smem_addr(&sh.v_empty[b]));
           tc_commit(smem_addr(&sh.o_full[b]));
