@@ -89,8 +89,10 @@ def attention(q, parts, table, lens, cu, tree, scale, f32):
                 e_s = (dim / 8 + 16 + (4 if f32 else 0)) * u * mag
                 steps = (2 * n / 16 + 64) * u
                 spread = w @ np.abs(vv)
-                # what a weight below f16's range (2^-39 of the largest, held times 2^14) loses
-                floor = len(w) * 2.0 ** -39 * np.abs(vv).max() * w.max()
+                # What a weight below f16's range loses: its smallest step is 2^-24, so half of it,
+                # 2^-25, of weights that are held times 2^7 (many rows) or 2^11 relative to a
+                # reference that the largest weight is not below: 2^-32 of the largest.
+                floor = len(w) * 2.0 ** -32 * np.abs(vv).max() * w.max()
                 mx = 0.0 if scale_k.dtype == np.float32 else 2.0 ** -36
                 tol[r] = (spread * ((2.0 ** -22 if f32 else 2.0 ** -11)
                                     + 2 * (e_s + 2.0 ** -21 + steps + mx))

@@ -360,3 +360,33 @@ def test_nothing_to_do(nr):
     out = nr.cache_attention(p["q"][:0].cuda(), *parts, i32(2, 3), i32(2), cu_q=i32(3),
                              tree=i32(0, 1))
     assert out.shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("group,queries", [(1, [7, 9]), (3, [3, 2]), (4, [1, 1]), (4, [4, 4]), (5, [1, 5]),
+                                           (8, [3, 3]), (23, [1, 1]), (6, [13, 1, 1])])
+def test_rows_on_both_sides_of_each_variant(nr, dim, fmt, group, queries):
+    """8, 16 and 24 query rows an item, the average and single sequences on either side."""
+    p = problem(group + dim, [50 + 90 * i for i in range(len(queries))], queries, 2, group, dim, 16, fmt,
+                torch.bfloat16, tree=True)
+    compare(nr, p)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rising_scores(nr, dim, dtype):
+    """Scores that rise slowly along the sequence (each step's maximum above the one before it, by less
+    and by more than the references lag), and fall."""
+    for sign in (1, -1):
+        for width in (0.02, 0.3, 4.0):
+            p = problem(dim, [900, 37], [1, 1], 1, 4, dim, 16, "fp8", dtype)
+            codes, scales = p["parts"][0], p["parts"][2]
+            one = cache_ref.quant(np.ones((1, 1, 1, dim), np.float32), "fp8")[0][0, 0, 0]
+            for s, n in enumerate((900, 37)):
+                for pos in range(n):
+                    at = p["table"][s, pos // 16], pos % 16
+                    codes[at] = one
+                    scales[at] = width * (pos if sign > 0 else n - pos) / dim ** 0.5 / 448
+            p["q"] = torch.ones_like(p["q"])
+            compare(nr, p, cu=False)
