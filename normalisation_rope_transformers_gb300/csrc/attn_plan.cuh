@@ -209,23 +209,35 @@ constexpr int kScaleUp = 13;  // MXFP4 values are held times 2^13
 // stays a NaN), times 2^kScaleUp; the largest as f32 without that factor.
 template <int G>
 __device__ __forceinline__ float mx_multipliers(uint64_t bytes, uint16_t (&m)[G]) {
-  uint32_t top = 0;
+  auto byte = [&](int i) { return static_cast<int>(bytes >> (8 * i)) & 255; };
+  int top = 0;
 #pragma unroll
-  for (int i = 0; i < G; i++) {
-    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
-    if (b != 255u) top = max(top, b);
+  for (int i = 0; i < G; i++) top = max(top, byte(i));
+  const bool nan = top == 255;
+  if (nan) {  // seldom
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < G; i++)
+      if (byte(i) != 255) top = max(top, byte(i));
   }
+  // 2^(byte - top + kScaleUp) as f32, then as f16: below its smallest, 2^-24, it becomes 0 (2^-25 is
+  // halfway and 0 the even neighbour)
+  const int base = 127 + kScaleUp - top;
 #pragma unroll
-  for (int i = 0; i < G; i++) {
-    const uint32_t b = static_cast<uint32_t>(bytes >> (8 * i)) & 255u;
-    const int e = static_cast<int>(b) - static_cast<int>(top) + kScaleUp;  // 2^e
-    m[i] = static_cast<uint16_t>(b == 255u ? 0x7E00
-                                 : e >= -14 ? (e + 15) << 10
-                                 : e >= -24 ? 1 << (e + 24)
-                                            : 0);
+  for (int i = 0; i < G; i += 2) {
+    const uint32_t two =
+        half2_of(__uint_as_float(static_cast<uint32_t>(max(byte(i) + base, 0)) << 23),
+                 __uint_as_float(static_cast<uint32_t>(max(byte(i + 1) + base, 0)) << 23));
+    m[i] = static_cast<uint16_t>(two);
+    m[i + 1] = static_cast<uint16_t>(two >> 16);
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < G; i++)
+      if (byte(i) == 255) m[i] = 0x7E00;
   }
   // 2^(top - 127 - kScaleUp); below 2^-126: nothing that f32 scores would see
-  const int e = static_cast<int>(top) - kScaleUp;
+  const int e = top - kScaleUp;
   return e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
 }
 

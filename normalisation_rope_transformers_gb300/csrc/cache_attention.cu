@@ -100,6 +100,13 @@ struct Layout {
   __host__ __device__ static constexpr int v_dim(int g, int j) {
     return j / kPieceV * 8 * kPieceV + kPieceV * g + j % kPieceV;
   }
+  // Where shared memory holds dimension v_dim(g, j) of a row of O: lanes g side by side, rows two
+  // apart eight banks apart, and so that 32 lanes with 4 dimensions each read different banks.
+  static constexpr int kPitchO = DIM / 4 * 5 + 4;
+  __host__ __device__ static constexpr int o_at(int g, int j) { return 8 * j + 8 * (j / 4) + g; }
+  __device__ static int o_first(int d) {  // of dimension d, a multiple of 4; the next three 8 further each
+    return o_at(d % (8 * kPieceV) / kPieceV, d / (8 * kPieceV) * kPieceV + d % kPieceV);
+  }
 };
 
 template <typename T, bool FP4, int DIM, int NT, int STEP>
@@ -107,7 +114,10 @@ struct AttnShared {
   static constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
   using L = Layout<FP4, DIM>;
   static constexpr int ROWS = 8 * NT;
-  uint2 q[SPLIT][NT][L::kStepsK][kWarp];  // fragments
+  union {
+    uint2 q[SPLIT][NT][L::kStepsK][kWarp];  // fragments
+    alignas(16) float o[kAttnWarps][ROWS][L::kPitchO];  // when Q is done with
+  };
   alignas(16) float row_scale[ROWS];
   alignas(16) int64_t at[kAttnWarps][2][STEP];        // code offsets, -1: no such position
   float ks[kAttnWarps][STEP];             // scales of K, of V
@@ -116,7 +126,6 @@ struct AttnShared {
   uint16_t vm[kAttnWarps][STEP][FP4 ? L::kGroups : 1];
   float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];
   float top[ROWS], sum[ROWS];
-  alignas(16) float o[kAttnWarps][ROWS][DIM + 4];
   AttnPlan<kAttnThreads> plan;
 };
 
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
         for (int j = 0; j < kTilesO; j++)
 #pragma unroll
           for (int h = 0; h < 2; h++)
-            sh.o[warp][r][L::v_dim(g, 2 * j + h)] = o[n][j][2 * h + e] * back * f;
+            sh.o[warp][r][L::o_at(g, 2 * j + h)] = o[n][j][2 * h + e] * back * f;
       }
     if (t < ROWS) {
       float top = sh.m[0][t], sum = 0.0f;
@@ -618,11 +627,12 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
                   (2 * static_cast<int64_t>(blockIdx.x) + (from_start ? 1 : 0)) * ROWS * (DIM + 2);
     for (int i = t; i < rows * (DIM / 4); i += kAttnThreads) {
       const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-      float4 x = *reinterpret_cast<const float4*>(&sh.o[0][r][d]);
+      const int at = L::o_first(d);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 1; w < kAttnWarps; w++) {
-        const float4 y = *reinterpret_cast<const float4*>(&sh.o[w][r][d]);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      for (int w = 0; w < kAttnWarps; w++) {
+        const float* y = &sh.o[w][r][at];
+        x.x += y[0], x.y += y[8], x.z += y[16], x.w += y[24];
       }
       const float sum = sh.sum[r];
       if (from_start && to_end) {
@@ -661,14 +671,20 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
   }
 }
 
+// Of an SM's memory what holds `bytes` of shared memory, in percent of the most; the rest is L1, through
+// which the codes come: 400009 tokens of 48 sequences take 154 us with three blocks' room, 188 us with 55
+// percent and four blocks, 216 us with all of it.
+constexpr int room(size_t bytes) {
+  for (size_t kb : {8, 16, 32, 64, 100, 132, 164, 196})
+    if (bytes <= kb * 1024) return static_cast<int>((kb * 100 + 227) / 228);
+  return 100;
+}
+
 template <typename T, bool FP4, int DIM, int NT>
 cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr int blocks = attn_blocks<DIM, NT>, ROWS = 8 * NT;
   constexpr size_t shared = sizeof(AttnShared<T, FP4, DIM, NT, 16 * kSub<FP4, DIM, NT>>);
-  // Shared memory for the blocks that fit, the rest is L1, through which the codes come: 400009
-  // tokens of 48 sequences 188 us, with all of it shared memory 216 us.
-  constexpr int percent = static_cast<int>((blocks * (shared + 1024) * 100 + 228 * 1024 - 1) / (228 * 1024));
-  static_assert(percent <= 100, "blocks an SM");
+  constexpr int percent = room(blocks * (shared + 1024));
   constexpr unsigned shares = kSms * blocks;
   static std::atomic<int> done[64], done_join[64];
   auto* kernel = cache_attention_kernel<T, FP4, DIM, NT>;
