@@ -24,7 +24,7 @@ namespace {
 
 // NT: tiles of eight query rows an item has.  A warp's step is 16 SUB positions: 32 where a lane's
 // codes of them fit in the registers beside O.  (One token, heads of 128 in FP8, 400009 positions in
-// 48 sequences: 16 at a time XXX us, 32 YYY us.)
+// 48 sequences: 16 at a time, four blocks an SM 188 us, 32 at a time, three 159 us.)
 template <bool FP4, int DIM, int NT>
 constexpr int kSub = DIM == 256 || (NT == 3 && DIM == 128 && !FP4) ? 1 : 2;
 // A share for each block that fits at once on 152 SMs (any number is right).
@@ -700,17 +700,41 @@ cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   return launch_pdl(join, dim3(shares, ROWS / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
 }
 
+// How many tiles of eight rows an item has, of at most `most`.  A step costs about 5 + 7 tiles (one
+// token, heads of 128 in FP8, 100009 tokens in 16 sequences: 16 rows take 81 us as two items of one
+// tile, 65 us as one of two; 24 rows 114 us as three of one, 87 us as one of three); a sequence with
+// fewer rows than an item pays for them all.  With as
+// many new tokens in each sequence its rows are known here; otherwise anything up to twice the average is
+// taken to be as likely (4 to 24 rows, 13 on average: one tile 72 us, two 76; in MXFP4 74 and 83).
+int row_tiles(int64_t average, bool even, int most) {
+  int best = 1;
+  int64_t least = 0;
+  for (int nt = 1; nt <= most; nt++) {
+    const int64_t rows = 8 * nt, top = 2 * average - 1, whole = top / rows;
+    const int64_t items = even ? (average + rows - 1) / rows
+                               : rows * whole * (whole + 1) / 2 + top % rows * (whole + 1);
+    if (nt == 1 || items * (5 + 7 * nt) < least) best = nt, least = items * (5 + 7 * nt);
+  }
+  return best;
+}
+
+template <typename T, bool FP4, int DIM, int MOST>
+cudaError_t attn_dim(int64_t average, bool even, const AttnArgs& a, void* ws, cudaStream_t s) {
+  const int tiles = row_tiles(average, even, MOST);
+  if constexpr (MOST >= 3)
+    if (tiles == 3) return attn_go<T, FP4, DIM, 3>(a, ws, s);
+  if constexpr (MOST >= 2)
+    if (tiles == 2) return attn_go<T, FP4, DIM, 2>(a, ws, s);
+  return attn_go<T, FP4, DIM, 1>(a, ws, s);
+}
+
+// Heads of 256: three tiles of O do not fit in the registers, nor do two beside FP8's codes (16 rows of
+// one token, 50009 tokens in 8 sequences: one tile 49 us, two 59; MXFP4 58 and 45).
 template <typename T, bool FP4>
-cudaError_t attn_few(int64_t average, int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
-  if (dim == 64)
-    return average <= 8    ? attn_go<T, FP4, 64, 1>(a, ws, s)
-           : average <= 16 ? attn_go<T, FP4, 64, 2>(a, ws, s)
-                           : attn_go<T, FP4, 64, 3>(a, ws, s);
-  if (dim == 128)
-    return average <= 8    ? attn_go<T, FP4, 128, 1>(a, ws, s)
-           : average <= 16 ? attn_go<T, FP4, 128, 2>(a, ws, s)
-                           : attn_go<T, FP4, 128, 3>(a, ws, s);
-  return average <= 8 ? attn_go<T, FP4, 256, 1>(a, ws, s) : attn_go<T, FP4, 256, 2>(a, ws, s);
+cudaError_t attn_few(int64_t average, bool even, int64_t dim, const AttnArgs& a, void* ws, cudaStream_t s) {
+  if (dim == 64) return attn_dim<T, FP4, 64, 3>(average, even, a, ws, s);
+  if (dim == 128) return attn_dim<T, FP4, 128, 3>(average, even, a, ws, s);
+  return attn_dim<T, FP4, 256, FP4 ? 2 : 1>(average, even, a, ws, s);
 }
 
 AttnArgs attn_args(const KvCacheArgs& c, const CacheAttentionArgs& p) {
@@ -755,16 +779,18 @@ int64_t cache_attention_workspace(int64_t head_dim) {
 cudaError_t launch_cache_attention(const KvCacheArgs& c, const CacheAttentionArgs& p, int is_bf16,
                                    cudaStream_t stream) {
   const AttnArgs a = attn_args(c, p);
-  // Query rows an item on average (what each sequence has is known on the device alone).  More than
-  // 24: the kernel whose tile of products has 128.
+  // Query rows a sequence and head of the cache on average (what each has is known on the device alone).
+  // More than 24: the kernel whose tile of products has 128 (24 rows of one token, heads of 128 in
+  // FP8, 100009 tokens in 16 sequences: 105 us there, 87 here; here every 24 more take as long again).
   const int64_t average = (p.tokens * (p.q_heads / c.heads) + p.seqs - 1) / p.seqs;
+  const bool even = p.tokens % p.seqs == 0;
   if (is_bf16 && c.head_dim <= 128 && average > 24)
     return launch_attn_rows(a, c.fp4, c.head_dim, p.workspace, stream);
   if (is_bf16)
-    return c.fp4 ? attn_few<__nv_bfloat16, true>(average, c.head_dim, a, p.workspace, stream)
-                 : attn_few<__nv_bfloat16, false>(average, c.head_dim, a, p.workspace, stream);
-  return c.fp4 ? attn_few<float, true>(average, c.head_dim, a, p.workspace, stream)
-               : attn_few<float, false>(average, c.head_dim, a, p.workspace, stream);
+    return c.fp4 ? attn_few<__nv_bfloat16, true>(average, even, c.head_dim, a, p.workspace, stream)
+                 : attn_few<__nv_bfloat16, false>(average, even, c.head_dim, a, p.workspace, stream);
+  return c.fp4 ? attn_few<float, true>(average, even, c.head_dim, a, p.workspace, stream)
+               : attn_few<float, false>(average, even, c.head_dim, a, p.workspace, stream);
 }
 
 }  // namespace nr
