@@ -575,7 +575,8 @@ nr_status nr_gelu_and_mul(void* out, const void* x, int64_t rows, int64_t inter,
 /*
  * Device-side failure report.  Kernels that wait on hardware events (the
  * bulk-copy path of nr_qk_norm_rope waits for its copies on shared-memory
- * barriers) bound every wait (about one second of SM clock); a wait that runs
+ * barriers, the tensor-core path of nr_cache_attention for its roles') bound
+ * every wait (about one second of SM clock); a wait that runs
  * out sets a bit in a status word the library keeps on each device, the
  * kernel lets its copies in flight finish and returns, and the outputs of
  * that call are not valid.  nr_device_status works on the device that owns

@@ -10,10 +10,19 @@
 // to the largest V scale met), the one rounding that is not f32's: it is four times finer than the
 // bf16 output's.  With f32 tensors Q and the weights are two f16 parts each (22 bits).
 //
-// Few queries a sequence: bound by HBM, each code read once for up to 16 query rows.  A warp
-// reads 16 positions' codes straight into the registers where mma.sync wants them: which
-// dimensions a lane's vector holds is free as long as Q (and the output's order) agree.  K of the
-// next positions is on its way during softmax and the second product, V during the first.
+// Few queries a sequence: each code read once for 8, 16 or 24 query rows.  A warp reads 16 or 32
+// positions' codes straight into the registers where mma.sync wants them (positions and dimensions
+// are the rows of its first operand, query rows the columns of its second): which dimensions a
+// lane's vector holds is free as long as Q (and the output's order) agree.  K of the next positions is
+// on its way during softmax and the second product, V during the first.  A row's reference follows its
+// maximum only when that is 2^4 above, so most steps reduce nothing across lanes.  Every share of
+// the positions is as long: shares that end inside a sequence leave parts that a second kernel joins.
+//
+// Measured: one token of 48 sequences with 400009 cached tokens, 32 query and 8 cache heads of 128 in
+// FP8: 154 us, 0.81 of the copy rate, bound by what 12 warps an SM have under way (168 registers).
+// Up to 5 tokens of 29 sequences with 150001, 24 and 6 heads, MXFP4: 85 us, 0.21 of it, bound by
+// instructions (53% of the issue slots; widening a code costs as much as FP8's twice as many bytes).
+// One sequence of 1501 tokens: 10.6 us, latency: two launches, a plan, one step, joining.
 #include <type_traits>
 
 #include "attn_plan.cuh"

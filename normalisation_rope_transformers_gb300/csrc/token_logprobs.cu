@@ -21,6 +21,10 @@
 //
 // Gradient: dz = p (-g - h (ln p + H)) + g [j = token], p = e^(z - lse), g and h the
 // gradients of logprob and entropy H: one read and one write of the logits.
+//
+// Measured, bf16: [4093, 151551] with five alternatives 237 us (0.77 of the copy rate; 197 us without:
+// bound by issue, 70% of the slots), [5, 131072] with twenty 14 us (latency: one read, the bound, the
+// list); the gradient at [4096, 131072] 303 us (1.05 of the copy rate), f32 [96, 32003] 4.7 us.
 #include <cooperative_groups.h>
 
 #include "nr_internal.h"
