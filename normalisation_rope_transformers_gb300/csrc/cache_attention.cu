@@ -7,7 +7,7 @@
 // f32.  A token's K scale multiplies its scores, its V scale its weights.  MXFP4 has a scale for
 // 32 elements: relative to the token's largest they are powers of two that f16 holds down to
 // 2^-37 of it; what is smaller counts as zero.  Weights are rounded to f16 (11 bits, relative
-// to the largest V scale met), the one rounding that is not f32's: it is four times finer than the
+// to the largest V scale met), the one rounding that is not f32's: it is eight times finer than the
 // bf16 output's.  With f32 tensors Q and the weights are two f16 parts each (22 bits).
 //
 // Few queries a sequence: each code read once for 8, 16 or 24 query rows.  A warp reads 16 or 32
