@@ -390,3 +390,36 @@ def test_rising_scores(nr, dim, dtype):
                     scales[at] = width * (pos if sign > 0 else n - pos) / dim ** 0.5 / 448
             p["q"] = torch.ones_like(p["q"])
             compare(nr, p, cu=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 4])
+def test_nan_reaches_those_who_see_it_whatever_the_rows(nr, group, dim, fmt, dtype):
+    """6, 12 and 24 query rows an item; two sequences, two heads, the NaN in one of each; one more in
+    front of the drafts, which everyone of its sequence sees."""
+    p = problem(20 + group, [70, 37], [6, 6], 2, group, dim, 16, fmt, dtype, tree=True)
+    p["tree"][6:, 0] = [1, 3, 5, 9, 19, 33]  # tokens 1 and 4 see token 1
+    clean, lse = run(nr, p)
+    block = 32 if fmt == "mxfp4" else 1
+    expect = torch.zeros(clean.shape, dtype=torch.bool, device="cuda")
+
+    def spoil(s, pos, head, d):
+        b, place = p["table"][s, pos // 16], pos % 16
+        if fmt == "fp8":
+            p["parts"][1][b, place, head, d] = 0xFF
+        else:
+            p["parts"][3][b, place, head, d // 32] = 255
+        return slice(d // block * block, d // block * block + block)
+
+    dims = spoil(1, 37 - 6 + 1, 1, 37)
+    for t in (7, 10):
+        expect[t, group:, dims] = True
+    dims = spoil(0, 40, 0, dim - 1)
+    expect[:6, :group, dims] = True
+    dirty, lse2 = run(nr, p)
+    assert torch.equal(lse, lse2)
+    nan = torch.isnan(dirty)
+    assert torch.equal(nan, expect)
+    assert torch.equal(dirty[~nan], clean[~nan])
