@@ -37,8 +37,10 @@ namespace {
 template <bool FP4, int DIM, int NT>
 constexpr int kSub = DIM == 256 || (NT == 3 && DIM == 128 && !FP4) ? 1 : 2;
 // A share for each block that fits at once on 152 SMs (any number is right).
+// (Heads of 64, one token, 300009 positions in 48 sequences: four blocks an SM instead of three 97 -> 96
+// us in FP8, 93 -> 85 in MXFP4; heads of 128 in MXFP4 124 with four, 122 with three.)
 template <int DIM, int NT>
-constexpr int attn_blocks = DIM == 256 || NT > 1 ? 2 : 3;
+constexpr int attn_blocks = DIM == 256 || NT > 1 ? 2 : DIM == 64 ? 4 : 3;
 constexpr int kSms = 152;
 
 constexpr int kAttnThreads = 128;
