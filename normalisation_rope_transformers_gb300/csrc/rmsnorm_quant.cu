@@ -12,10 +12,12 @@
 // once.  HBM bounds many rows, one row's chain of loads and reductions a few.  A row's
 // scale needs no second reduction: 1 / sqrt(...) is common to all of it and
 // cancels in n * (448 / a), so max |v w| is reduced together with the sum of squares.
-// Measured: bf16 [8192, 5120] with the residual, a scale for 128: 47.3 us (0.92 of the copy rate);
-// f32 [2049, 4096], mx: 8.8 us (0.71, one wave of blocks and its ramp); bf16 [8, 5120]: 2.2 us, latency.
+// Measured: bf16 [8192, 5120] with the residual, a scale for 128: 47.0 us (0.93 of the copy rate);
+// f32 [2049, 4096], mx: 8.4 us (0.74, one wave of blocks and its ramp); bf16 [8, 5120]: 2.1 us, latency.
+// (With f32 arithmetic one value at a time instead of pairs: 47.3, 8.8 and 2.2 us.)
 #include <type_traits>
 
+#include "nr_pairs.cuh"
 #include "quant.cuh"
 
 namespace nr {
@@ -99,7 +101,8 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
     bulk_prefetch_l2(x + a.prefetch_rows * a.nvec, static_cast<unsigned>(a.nvec) * 16u);
     if (RES) bulk_prefetch_l2(r + a.prefetch_rows * a.nvec, static_cast<unsigned>(a.nvec) * 16u);
   }
-  float sum = 0.0f, top = 0.0f;
+  F2 squares = f2(0.0f, 0.0f);
+  float top = 0.0f;
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const int i = threadIdx.x + k * blockDim.x;
@@ -110,13 +113,13 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
         float q[N];
         Vec<T>::unpack(rv[RES ? k : 0], q);
 #pragma unroll
-        for (int e = 0; e < N; e++) v[e] += q[e];
+        for (int e = 0; e < N; e += 2) split(add2(f2(v[e], v[e + 1]), f2(q[e], q[e + 1])), v[e], v[e + 1]);
         xv[k] = Vec<T>::pack(v);  // rounded: what is written back is what is normed
         st_stream(r + i, xv[k]);
         Vec<T>::unpack(xv[k], v);
       }
 #pragma unroll
-      for (int e = 0; e < N; e++) sum = fmaf(v[e], v[e], sum);
+      for (int e = 0; e < N; e += 2) squares = fma2(f2(v[e], v[e + 1]), f2(v[e], v[e + 1]), squares);
       if (MODE == kRow) {
         float u[N];
         Vec<T>::unpack(FEW ? wv[FEW ? k : 0] : ld_param(w + i), u);
@@ -125,6 +128,9 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
       }
     }
   }
+  float sum, odd;
+  split(squares, sum, odd);
+  sum += odd;
   block_sum_max(sum, top, scratch);
   float inv;
   {
@@ -189,7 +195,9 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
       Vec<T>::unpack(xv[k], v);
       Vec<T>::unpack(FEW ? wv[FEW ? k : 0] : ld_param(w + i), u);
 #pragma unroll
-      for (int e = 0; e < N; e++) v[e] = v[e] * n_inv * (u[e] + a.w_add);
+      for (int e = 0; e < N; e += 2)
+        split(mul2(mul2(f2(v[e], v[e + 1]), f2(n_inv, n_inv)),
+                   add2(f2(u[e], u[e + 1]), f2(a.w_add, a.w_add))), v[e], v[e + 1]);
     } else {
 #pragma unroll
       for (int e = 0; e < N; e++) v[e] = 0.0f;
@@ -215,7 +223,8 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : kManyThreads)
     }
     if (!in) continue;
 #pragma unroll
-    for (int e = 0; e < N; e++) v[e] *= factor;
+    for (int e = 0; e < N; e += 2)
+      split(mul2(f2(v[e], v[e + 1]), f2(factor, factor)), v[e], v[e + 1]);
     store_codes<T>(a.codes + (row + i) * N, v);
   }
 }
