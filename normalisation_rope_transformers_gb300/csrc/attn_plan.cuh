@@ -260,9 +260,10 @@ __device__ __forceinline__ T narrow(float x) {
 namespace {
 
 // Joins the parts of the items that more than one share worked on: block (i, y) rows
-// kJoinRows y + threadIdx.y of the item that begins in share i, four dimensions a thread.
+// kJoinRows y + threadIdx.y of the item that begins in share i, four dimensions a thread.  (FP4 says
+// whose parts: each kernel's own joining asks for the shared memory that the kernel asks for.)
 constexpr int kJoinRows = 4;
-template <typename T, int R, int DIM>
+template <typename T, int R, int DIM, bool FP4>
 __global__ void __launch_bounds__(DIM / 4 * kJoinRows) cache_attention_join_kernel(const AttnArgs a) {
   pdl_enter();
   const int4 join = a.joins[blockIdx.x];

@@ -699,7 +699,7 @@ cudaError_t attn_go(AttnArgs a, void* workspace, cudaStream_t s) {
   constexpr unsigned shares = kSms * blocks;
   static std::atomic<int> done[64], done_join[64];
   auto* kernel = cache_attention_kernel<T, FP4, DIM, NT>;
-  auto* join = cache_attention_join_kernel<T, ROWS, DIM>;
+  auto* join = cache_attention_join_kernel<T, ROWS, DIM, FP4>;
   cudaError_t e = allow_shared(kernel, shared, done, percent);
   if (e == cudaSuccess) e = allow_shared(join, 0, done_join, percent);
   if (e != cudaSuccess) return e;

@@ -796,7 +796,7 @@ cudaError_t rows_go(AttnArgs a, void* workspace, cudaStream_t s) {
   cudaError_t e = status_word(&status);
   if (e == cudaSuccess) e = allow_shared(cache_attention_rows_kernel<FP4, DIM>, shared, done, percent);
   if (e == cudaSuccess)
-    e = allow_shared(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>, 0, done_join, percent);
+    e = allow_shared(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM, FP4>, 0, done_join, percent);
   if (e != cudaSuccess) return e;
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
@@ -804,7 +804,7 @@ cudaError_t rows_go(AttnArgs a, void* workspace, cudaStream_t s) {
   e = launch_pdl(cache_attention_rows_kernel<FP4, DIM>, dim3(kRowsShares), dim3(kRowsThreads), shared, s,
                  a, status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM>,
+  return launch_pdl(cache_attention_join_kernel<__nv_bfloat16, kRows, DIM, FP4>,
                     dim3(kRowsShares, kRows / kJoinRows), dim3(DIM / 4, kJoinRows), 0, s, a);
 }
 
