@@ -283,6 +283,7 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const 
     }
     tmem_store16(p_at + 16 * j, p);
   }
+  tmem_stored();  // the next stores may go to the same columns, and nothing orders two but this
   float lo, hi;
   split(l2, lo, hi);
   return lo + hi;
@@ -482,7 +483,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               }
             }
             l += lt;
-            tmem_stored();
           }
           tc_before();
           mbar_arrive(smem_addr(&sh.p_full[b]));
