@@ -376,8 +376,12 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
  * or 256; tokens * q_heads < 2^31; scale is finite.
  * workspace    as nr_group_norm, of at least nr_cache_attention_workspace bytes.
  * Sums are formed in a fixed order (the same inputs give the same bits).  Scores, weights and sums
- * are f32; weights are rounded to f16 for the product with V (bf16 tensors), or held in 22 bits
- * (f32 tensors).  MXFP4 elements below 2^-37 of their head row's largest scale count as zero.
+ * are f32.  A weight times its token's V scale (MXFP4: its head row's largest) is rounded for the
+ * product with V to f16's 11 bits (bf16 tensors) or held in 22 (f32 tensors), and is off by up to
+ * 2^-32 of the row's largest such product, or of 2^-104 where that is larger.  Weights below
+ * 2^-118 of the row's largest may count as zero.  FP8 scales may have either sign.  Sums of
+ * weights (up to 2^8 each) times V have to stay in f32's range.  MXFP4 elements below 2^-37 of
+ * their head row's largest scale count as zero.
  * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
  */
 nr_status nr_cache_attention(void* out, float* lse, const void* q, const nr_kv_cache* cache,

@@ -241,15 +241,24 @@ __device__ __forceinline__ float mx_multipliers(uint64_t bytes, uint16_t (&m)[G]
   return e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.0f;
 }
 
-// The power of two at or above a finite scale, between 2^-100 and 2^127; 0 for others.
-__device__ __forceinline__ float scale_reference(float s) {
-  if (!(s > 0.0f && s <= kScaleCeil)) return 0.0f;
-  const uint32_t up = (__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u;
-  return __uint_as_float(min(max(up, 27u << 23), 254u << 23));
+// Weights times V's scales, for the second product's f16.  A row holds e^(score - m) |scale| as that times
+// a power of two, so that the largest it has met (t, the maximum of score + k in units of log2, with
+// |scale| < 2^k) is held in [2^(HOLD - 3/2), 2^(HOLD + 1/2)): a token that nobody attends to does not
+// count, whatever its scale.
+__device__ __forceinline__ float scale_exponent(float s) {  // k; none for a scale that is not finite
+  const uint32_t e = __float_as_uint(s) >> 23 & 255u;
+  return e == 255u ? -__builtin_huge_valf() : static_cast<float>(static_cast<int>(e) - 126);
 }
-// Its reciprocal, of 0: 0.
+// That power of two, 2^(HOLD - round(t - m)).  (Below -104 the products with it would leave f32's range;
+// above 128 there is no scale.)  Behind the addition the low bits are the exponent's.
+template <int HOLD>
+__device__ __forceinline__ float hold_factor(float t, float m) {
+  const float r = fminf(fmaxf(t - m, -104.0f), 128.0f);
+  return __uint_as_float(__float_as_uint((12582912.0f + (127 + HOLD)) - r) << 23);
+}
+// The reciprocal of a power of two between 2^-126 and 2^126.
 __device__ __forceinline__ float power_reciprocal(float p) {
-  return p == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(p));
+  return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
 template <typename T>

@@ -6,9 +6,10 @@
 // Q is brought to f16's range by a power of two, so products of Q and K are exact and summed in
 // f32.  A token's K scale multiplies its scores, its V scale its weights.  MXFP4 has a scale for
 // 32 elements: relative to the token's largest they are powers of two that f16 holds down to
-// 2^-37 of it; what is smaller counts as zero.  Weights are rounded to f16 (11 bits, relative
-// to the largest V scale met), the one rounding that is not f32's: it is eight times finer than the
-// bf16 output's.  With f32 tensors Q and the weights are two f16 parts each (22 bits).
+// 2^-37 of it; what is smaller counts as zero.  Weights times V's scales are rounded to f16 (11 bits), the
+// one rounding that is not f32's: it is eight times finer than the bf16 output's.  A row's largest of them
+// is held at 2^9.5 or more, whatever the weight or the scale alone, so f16's end takes at most 2^-34 of it from
+// another.  With f32 tensors Q and these products are two f16 parts each (22 bits).
 //
 // Few queries a sequence: each code read once for 8, 16 or 24 query rows.  A warp reads 16 or 32
 // positions' codes straight into the registers where mma.sync wants them (positions and dimensions
@@ -47,7 +48,7 @@ constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
 constexpr int kItemCost = 3;  // tiles that an item costs besides its own
 constexpr float kSlack = 4.0f;  // a row's reference is behind its maximum by up to 2^4,
-constexpr float kWeightUp = 2048.0f;  // weights are held times 2^11
+constexpr int kHold = 11;       // and what it holds for f16 behind its largest: 2^11.5 to 2^15.5
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -310,15 +311,15 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
     constexpr int kTilesO = DIM / 16;
     float o[NT][kTilesO][4];
     float m[NT][2], l[NT][2];
-    // A row's weights are held relative to the largest V scale that it has met, as a power of two
-    // (so that a step's result does not depend on it but where weights leave f16's range).
-    float vref[NT][2], vref_low = 0.0f;  // (the smallest of any row)
+    // The same of scores and the exponents of V's scales: what hold_factor takes (a power of two, so
+    // that a step's result does not depend on it but where weights leave f16's range).
+    float vm[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
 #pragma unroll
       for (int j = 0; j < kTilesO; j++) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 2; e++) m[n][e] = -__builtin_huge_valf(), l[n][e] = vref[n][e] = 0.0f;
+      for (int e = 0; e < 2; e++) m[n][e] = vm[n][e] = -__builtin_huge_valf(), l[n][e] = 0.0f;
     }
 
     for (int i = 0; i < steps; i++) {
@@ -333,7 +334,6 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
         for (int e = 0; e < L::kGroups; e++) sh.vm[warp][lane][FP4 ? e : 0] = mul[e];
       }
       if (lane < kStep) sh.ks[warp][lane] = ks, sh.vs[warp][lane] = vs;
-      const float own = lane < kStep ? scale_reference(vs) : 0.0f;
       const bool was_clean = clean;
       const bool more = i + 1 < steps;
       if (more) {
@@ -396,37 +396,35 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
 #pragma unroll
             for (int e = 0; e < 2; e++) s[u][n][2 * h + e] *= sk * rs[n][e];
         }
-      float vt[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; n++) vt[n][0] = vt[n][1] = own;
       uint32_t hidden[SUB];  // bit 4 n + e: not seen
-      bool higher = own > vref_low;
 #pragma unroll
       for (int u = 0; u < SUB; u++) hidden[u] = 0u;
       if (!was_clean) {
-        higher = false;
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            vt[n][e] = 0.0f;
             const int r = 8 * n + 2 * c + e, tok = a.group.quot(it.rb * ROWS + r);
 #pragma unroll
             for (int u = 0; u < SUB; u++)
 #pragma unroll
               for (int h = 0; h < 2; h++) {
                 const int at = 16 * u + 8 * h + g;
-                if (r < rows && sh.at[warp][i & 1][at] >= 0 &&
-                    attn_sees(a, seq, tok, base0 + i * kAttnTile + at)) {
-                  vt[n][e] = fmaxf(vt[n][e], scale_reference(sv[u][h]));
-                } else {
+                if (!(r < rows && sh.at[warp][i & 1][at] >= 0 &&
+                      attn_sees(a, seq, tok, base0 + i * kAttnTile + at))) {
                   hidden[u] |= 1u << (4 * n + 2 * h + e);
                   s[u][n][2 * h + e] = -__builtin_huge_valf();
                 }
               }
-            higher = higher || vt[n][e] > vref[n][e];
           }
       }
+      // The largest exponent of the lane's V scales: with the largest score it is at least what any
+      // position of the lane holds.
+      float big = 0.0f;
+#pragma unroll
+      for (int u = 0; u < SUB; u++) big = fmaxf(big, fmaxf(fabsf(sv[u][0]), fabsf(sv[u][1])));
+      const float most = static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 126);
+      bool higher = false;
       float mx[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; n++)
@@ -436,48 +434,51 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
 #pragma unroll
           for (int u = 1; u < SUB; u++)
             mx[n][e] = fmaxf(mx[n][e], fmaxf(s[u][n][e], s[u][n][2 + e]));
-          higher = higher || mx[n][e] > m[n][e] + kSlack;
+          higher = higher || mx[n][e] > m[n][e] + kSlack || mx[n][e] + most > vm[n][e] + kSlack;
         }
       // Seldom after an item's first step: references stay until a maximum is 2^kSlack above.
       if (__any_sync(0xFFFFFFFFu, higher)) {
-        float low = __builtin_huge_valf();
+        float vk[SUB][2];
+#pragma unroll
+        for (int u = 0; u < SUB; u++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) vk[u][h] = scale_exponent(sv[u][h]);
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            float top = fmaxf(mx[n][e], m[n][e]), vtop = fmaxf(vt[n][e], vref[n][e]);
+            float top = fmaxf(mx[n][e], m[n][e]), vtop = vm[n][e];
+#pragma unroll
+            for (int u = 0; u < SUB; u++)
+#pragma unroll
+              for (int h = 0; h < 2; h++) vtop = fmaxf(vtop, s[u][n][2 * h + e] + vk[u][h]);
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) {  // the lanes that share a row
               top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
               vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
             }
-            if (was_clean)  // lanes' own positions: those of every row
-#pragma unroll
-              for (int d = 1; d <= 2; d <<= 1)
-                vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
             float f = top == m[n][e] ? 1.0f : attn_exp2(m[n][e] - top);
             l[n][e] *= f;
-            f *= vref[n][e] * power_reciprocal(vtop);
+            // (at most 2: what the row has met is below both references)
+            f = f * hold_factor<kHold>(vtop, top) * power_reciprocal(hold_factor<kHold>(vm[n][e], m[n][e]));
 #pragma unroll
             for (int j = 0; j < kTilesO; j++) {
               o[n][j][e] *= f;
               o[n][j][2 + e] *= f;
             }
             m[n][e] = top;
-            vref[n][e] = vtop;
-            low = fminf(low, vtop);
+            vm[n][e] = vtop;
           }
-        vref_low = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(low)));
       }
       // The weights as the second product's fragments: p[u][n][part], pairs of positions of a row.
       uint32_t p[SUB][NT][SPLIT][2];
 #pragma unroll
       for (int n = 0; n < NT; n++) {
-        float use[2], winv[2];
+        float use[2], up[2];
 #pragma unroll
         for (int e = 0; e < 2; e++) {
           use[e] = m[n][e] == -__builtin_huge_valf() ? 0.0f : m[n][e];
-          winv[e] = kWeightUp * power_reciprocal(vref[n][e]);
+          up[e] = hold_factor<kHold>(vm[n][e], m[n][e]);
         }
 #pragma unroll
         for (int u = 0; u < SUB; u++)
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
             for (int e = 0; e < 2; e++) {
               w[e] = attn_exp2(s[u][n][2 * h + e] - use[e]);
               l[n][e] += w[e];
-              w[e] *= sv[u][h] * winv[e];
+              w[e] = w[e] * up[e] * sv[u][h];  // (in this order: a scale times the factor may be infinite)
               if (!was_clean && (hidden[u] >> (4 * n + 2 * h + e) & 1u)) w[e] = 0.0f;  // whatever its scale
             }
             const uint32_t first = half2_of(w[0], w[1]);
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kAttnThreads, (attn_blocks<DIM, NT>))
 #pragma unroll
         for (int w = 1; w < kAttnWarps; w++) top = fmaxf(top, sh.m[w][r]);
         const float f = m[n][e] == -__builtin_huge_valf() ? 0.0f : attn_exp2(m[n][e] - top);
-        const float back = vref[n][e] * (1.0f / kWeightUp);
+        const float back = power_reciprocal(hold_factor<kHold>(vm[n][e], m[n][e]));
 #pragma unroll
         for (int j = 0; j < kTilesO; j++)
 #pragma unroll

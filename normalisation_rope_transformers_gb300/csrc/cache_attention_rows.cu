@@ -1,5 +1,6 @@
 // Attention over the quantised paged cache with many query rows an item: trees and chains of
-// drafted tokens, prompts (sm_103a, tcgen05).  The arithmetic is cache_attention.cu's.
+// drafted tokens, prompts (sm_103a, tcgen05).  The arithmetic is cache_attention.cu's; a row's largest weight
+// times V scale is held at 2^7.5 or more, so f16's end takes at most 2^-32 of it from another.
 //
 // A block owns an SM and up to 128 query rows of one K/V head, and walks its share's positions in
 // tiles of 128.  Eight warps read the codes and write them as f16 into shared memory in
@@ -8,11 +9,12 @@
 //     S = Q K^T    A and B from shared memory, S in tensor memory, two buffers
 //     O += P V     A = P (f16) in tensor memory, beside the S it came from; B = V as it lies
 //                  (the dimension runs fastest); O stays in tensor memory
-// so that Q K^T of the next tile runs under the softmax of this one.  A row's reference m
-// moves only when a score exceeds it by 2^8 (or a larger V scale comes), which weights held
-// times 2^7 leave room for in f16; then the warp multiplies its rows of O.  So a tile's weights are
-// taken with the reference that is there, in one pass that finds the maximum too, and once more where
-// that moves it (a pass of its own for the maximum: 131 us where this takes 121).
+// so that Q K^T of the next tile runs under the softmax of this one.  A row's references (its largest
+// score, and its largest weight times V scale) move only when a tile's weights sum to more than 2^8 or
+// one of them times its V scale leaves f16's range, 2^6.5 above what the largest is held at or more;
+// then the warp multiplies its rows of O.  So a tile's weights are taken with the references that are
+// there, and once more where these have to move (a pass of its own for the maximum in each tile: 131 us
+// where this takes 121).
 //
 // What bounds it: the products take 1076 cycles a tile (D = 128), the operands 160 KB of shared
 // memory a tile (1250 cycles).  The softmax's warps are alone on their schedulers and wait for their own
@@ -35,8 +37,9 @@ constexpr int kPer = kPos / kLoadWarps;  // positions a loading warp
 constexpr int kItemCost = 8;       // tiles that an item costs besides its own
 constexpr int kMeta = 4;           // tiles whose scales are kept
 constexpr int kItems = 8;          // items whose row scales are kept
-constexpr float kHeadroom = 8.0f;  // a score may exceed the reference by 2^8
-constexpr float kHeldUp = 128.0f;  // weights are held times 2^7
+constexpr float kMostSum = 256.0f;  // of a tile's weights, relative to the row's reference
+constexpr int kHold = 9;            // what a row holds for f16 starts between 2^7.5 and 2^9.5,
+constexpr float kMostHeld = 65504.0f;  // and may rise to f16's largest
 constexpr long long kWaitCycles = 1ll << 31;
 constexpr float kNone = -__builtin_huge_valf();
 
@@ -145,8 +148,7 @@ struct RowsShared {
       o_full[2], meta_full[kMeta], done;
   alignas(16) float ks[kMeta][kPos];
   alignas(16) float vs[kMeta][kPos];
-  alignas(16) float vr[kMeta][kPos];          // references of V's scales,
-  alignas(16) float vtop[kMeta][kLoadWarps];  // the largest
+  alignas(16) float vk[kMeta][kPos];  // exponents of V's scales
   alignas(16) uint16_t there[kMeta][kLoadWarps];       // positions that are in the cache
   alignas(16) unsigned char clean[kMeta][kLoadWarps];  // every position there, seen by every row
   float row_scale[kItems][kRows];
@@ -241,15 +243,44 @@ struct RowsLane {
 };
 
 // One thread's row of a tile of scores, over the positions whose bits are set (ALL: every one): the
-// weights e^(score - m), summed; times V's scales and `up` as f16 to p_at.  `mx`: the largest score
-// before the row's own factor.
+// largest score, and the largest sum of a score and the exponent of its V scale.
+template <bool ALL>
+__device__ __forceinline__ void rows_find(unsigned s_at, const float* ks, const float* vk,
+                                          const uint32_t (&see)[4], float rs, float& mx, float& tx) {
+  const F2 rs2 = f2(rs, rs);
+  mx = tx = kNone;
+  uint32_t x[32];
+#pragma unroll 1
+  for (int j = 0; j < 4; j++) {
+    tmem_load(s_at + 32 * j, x);
+    tmem_loaded(x);
+    const float2* k2 = reinterpret_cast<const float2*>(ks + 32 * j);
+    const float2* v2 = reinterpret_cast<const float2*>(vk + 32 * j);
+    const uint32_t bits = j == 0 ? see[0] : j == 1 ? see[1] : j == 2 ? see[2] : see[3];
+#pragma unroll
+    for (int e = 0; e < 16; e++) {
+      const float2 k = k2[e], v = v2[e];
+      const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
+      const F2 score = mul2(mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                 f2(k.x, k.y)), rs2);
+      float u[2];
+      split(score, u[0], u[1]);
+      mx = fmaxf(mx, fmaxf(s0 ? u[0] : kNone, s1 ? u[1] : kNone));
+      split(add2(score, f2(v.x, v.y)), u[0], u[1]);
+      tx = fmaxf(tx, fmaxf(s0 ? u[0] : kNone, s1 ? u[1] : kNone));
+    }
+  }
+}
+
+// The same row's weights e^(score - m), summed; times `up` and V's scales as f16 to p_at.  `most`: the
+// largest magnitude of these.
 template <bool ALL>
 __device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const float* ks,
                                             const float* vs, const uint32_t (&see)[4], float rs,
-                                            float neg, float up, float& mx) {
+                                            float neg, float up, float& most) {
   const F2 rs2 = f2(rs, rs), neg2 = f2(neg, neg), up2 = f2(up, up);
   F2 l2 = f2(0.0f, 0.0f);
-  mx = kNone;
+  most = 0.0f;
   uint32_t x[32];
 #pragma unroll 1
   for (int j = 0; j < 4; j++) {
@@ -267,8 +298,6 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const 
       const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
       const F2 score = mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk);
       float u[2];
-      split(score, u[0], u[1]);
-      mx = fmaxf(mx, fmaxf(s0 ? u[0] : kNone, s1 ? u[1] : kNone));
       split(fma2(score, rs2, neg2), u[0], u[1]);
       u[0] = attn_exp2(u[0]);
       u[1] = attn_exp2(u[1]);
@@ -276,9 +305,10 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const 
       if (!s1) u[1] = 0.0f;
       const F2 weight = f2(u[0], u[1]);
       l2 = add2(l2, weight);
-      split(mul2(mul2(weight, vv), up2), u[0], u[1]);
+      split(mul2(mul2(weight, up2), vv), u[0], u[1]);  // (a scale times `up` may be infinite)
       if (!s0) u[0] = 0.0f;  // whatever its scale
       if (!s1) u[1] = 0.0f;
+      most = fmaxf(most, fmaxf(fabsf(u[0]), fabsf(u[1])));
       p[e] = half2_of(u[0], u[1]);
     }
     tmem_store16(p_at + 16 * j, p);
@@ -380,7 +410,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const bool busy = warp * kWarp < rows;
         const int row = w.it.rb * kRows + r;
         const int tok = a.group.quot(row);
-        float m = kNone, l = 0.0f, vref = 0.0f, rs = 0.0f;
+        float m = kNone, vm = kNone, l = 0.0f, rs = 0.0f;  // (vm: as hold_factor's t)
         for (int i = 0; i < steps; i++) {
           const int64_t g = tile + i;
           const int b = g & 1;
@@ -398,7 +428,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             const bool clean = *reinterpret_cast<const volatile uint64_t*>(sh.clean[g % kMeta]) ==
                                0x0101010101010101ull;
             uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-            float vt = 0.0f;
             if (!clean) {
               const int p0 = (w.it.tile + i) * kPos;
 #pragma unroll
@@ -424,63 +453,56 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                   bits &= there;
                 }
                 see[j] = bits;
-                const float4* ref = reinterpret_cast<const float4*>(&sh.vr[g % kMeta][32 * j]);
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                  const float4 x = ref[e];
-                  vt = fmaxf(vt, fmaxf(fmaxf(bits >> (4 * e) & 1u ? x.x : 0.0f,
-                                             bits >> (4 * e + 1) & 1u ? x.y : 0.0f),
-                                       fmaxf(bits >> (4 * e + 2) & 1u ? x.z : 0.0f,
-                                             bits >> (4 * e + 3) & 1u ? x.w : 0.0f)));
-                }
               }
-            } else {
-              const float4 x = *reinterpret_cast<const float4*>(&sh.vtop[g % kMeta][0]);
-              const float4 y = *reinterpret_cast<const float4*>(&sh.vtop[g % kMeta][4]);
-              vt = fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)),
-                         fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
             }
-            vt = fmaxf(vt, vref);
             __syncwarp();
-            // With the reference that the row has, and once more where it has to move: at an item's
-            // first tile, seldom after it.
-            float lt, mx;
+            // With the references that the row has, and once more where they have to move: at an item's
+            // first tile, where there are none, at once; seldom after it.
+            float lt;
+            bool need = i == 0;
 #pragma unroll 1
-            for (int turn = 0;; turn++) {
-              const float neg = m == kNone ? 0.0f : -m;
-              const float up = kHeldUp * power_reciprocal(vref);
-              const unsigned p_at = mine + 3 * kPos + b * (kPos / 2);
-              lt = clean ? rows_weigh<true>(s_at, p_at, ks, vs, see, rs, neg, up, mx)
-                         : rows_weigh<false>(s_at, p_at, ks, vs, see, rs, neg, up, mx);
-              if (mx > kNone) mx *= rs;
-              const bool need = mx > (m == kNone ? kNone : m + kHeadroom) || vt > vref;
-              if (turn == 1 || !__any_sync(0xFFFFFFFFu, need)) break;
-              // the row of O moves with it
-              float f = 1.0f;
-              if (need) {
-                const float to = fmaxf(m, mx);
-                const float fl = m == kNone ? 0.0f : attn_exp2(m - to);
-                l *= fl;
-                f = fl * (vref * power_reciprocal(vt));
-                m = to;
-                vref = vt;
-              }
-              __syncwarp();
-              if (i > 0) {
-                wait(smem_addr(&sh.o_full[b ^ 1]), ((g - 1) >> 1) & 1);
-                __syncwarp();
-                tc_after();
-                uint32_t x[32];
-#pragma unroll 1
-                for (int j = 0; j < DIM / 32; j++) {
-                  tmem_load(mine + 2 * kPos + 32 * j, x);
-                  tmem_loaded(x);
-#pragma unroll
-                  for (int e = 0; e < 32; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                  tmem_store32(mine + 2 * kPos + 32 * j, x);
+            for (int turn = i == 0 ? 1 : 0;; turn++) {
+              if (turn == 1) {
+                float mx, tx, f = 1.0f;
+                if (clean)
+                  rows_find<true>(s_at, ks, sh.vk[g % kMeta], see, rs, mx, tx);
+                else
+                  rows_find<false>(s_at, ks, sh.vk[g % kMeta], see, rs, mx, tx);
+                if (need) {
+                  const float to = fmaxf(m, mx), vto = fmaxf(vm, tx);
+                  const float fl = m == kNone ? 0.0f : attn_exp2(m - to);
+                  l *= fl;
+                  f = fl * hold_factor<kHold>(vto, to) * power_reciprocal(hold_factor<kHold>(vm, m));
+                  m = to;
+                  vm = vto;
                 }
-                tmem_stored();
+                __syncwarp();
+                if (i > 0) {  // the row of O moves with them
+                  wait(smem_addr(&sh.o_full[b ^ 1]), ((g - 1) >> 1) & 1);
+                  __syncwarp();
+                  tc_after();
+                  uint32_t x[32];
+#pragma unroll 1
+                  for (int j = 0; j < DIM / 32; j++) {
+                    tmem_load(mine + 2 * kPos + 32 * j, x);
+                    tmem_loaded(x);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                    tmem_store32(mine + 2 * kPos + 32 * j, x);
+                  }
+                  tmem_stored();
+                }
               }
+              const float neg = m == kNone ? 0.0f : -m;
+              const float up = hold_factor<kHold>(vm, m);
+              const unsigned p_at = mine + 3 * kPos + b * (kPos / 2);
+              float most;
+              lt = clean ? rows_weigh<true>(s_at, p_at, ks, vs, see, rs, neg, up, most)
+                         : rows_weigh<false>(s_at, p_at, ks, vs, see, rs, neg, up, most);
+              // (a sum above 2^8 has a weight above 2: the reference moves)
+              need = lt > kMostSum || most > kMostHeld ||
+                     (m == kNone && (see[0] | see[1] | see[2] | see[3]) != 0u);
+              if (turn == 1 || !__any_sync(0xFFFFFFFFu, need)) break;
             }
             l += lt;
           }
@@ -495,7 +517,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (busy) {
           const int lo = *static_cast<volatile int*>(&sh.nan_lo[item % kItems]);
           const int hi = *static_cast<volatile int*>(&sh.nan_hi[item % kItems]);
-          const float back = vref * (1.0f / kHeldUp);
+          const float back = power_reciprocal(hold_factor<kHold>(vm, m));
           const bool whole = from_start && to_end;
           const float scale = whole ? (l != 0.0f ? __fdiv_rn(back, l) : 0.0f) : back;
           const int64_t head = static_cast<int64_t>(seq.first + tok) * a.heads * a.group.div +
@@ -684,16 +706,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             clean = __all_sync(0xFFFFFFFFu, lane >= kPer || (in && p0 + lane < seq.context));
             const unsigned there = __ballot_sync(0xFFFFFFFFu, in);
-            const float ref = lane < kPer ? scale_reference(vs) : 0.0f;
-            const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(ref)));
             if (lane < kPer) {
               sh.ks[g % kMeta][lw * kPer + lane] = ks;
               sh.vs[g % kMeta][lw * kPer + lane] = vs;
-              sh.vr[g % kMeta][lw * kPer + lane] = ref;
+              sh.vk[g % kMeta][lw * kPer + lane] = scale_exponent(vs);
             }
             if (lane == 0) {
               sh.there[g % kMeta][lw] = static_cast<uint16_t>(there);
-              sh.vtop[g % kMeta][lw] = top;
               sh.clean[g % kMeta][lw] = clean ? 1 : 0;
             }
             __syncwarp();
