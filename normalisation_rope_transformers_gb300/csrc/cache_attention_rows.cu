@@ -261,8 +261,8 @@ __device__ __forceinline__ void rows_find(unsigned s_at, const float* ks, const 
     for (int e = 0; e < 16; e++) {
       const float2 k = k2[e], v = v2[e];
       const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
-      const F2 score = mul2(mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                 f2(k.x, k.y)), rs2);
+      const F2 score = mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                            mul2(f2(k.x, k.y), rs2));
       float u[2];
       split(score, u[0], u[1]);
       mx = fmaxf(mx, fmaxf(s0 ? u[0] : kNone, s1 ? u[1] : kNone));
@@ -296,9 +296,9 @@ __device__ __forceinline__ float rows_weigh(unsigned s_at, unsigned p_at, const 
       const F2 kk = e % 2 ? f2(k.z, k.w) : f2(k.x, k.y);
       const F2 vv = e % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
       const bool s0 = ALL || (bits >> (2 * e) & 1u), s1 = ALL || (bits >> (2 * e + 1) & 1u);
-      const F2 score = mul2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), kk);
-      float u[2];
-      split(fma2(score, rs2, neg2), u[0], u[1]);
+      float u[2];  // (the products with Q first times K's scale could leave f32's range)
+      split(fma2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), mul2(kk, rs2), neg2), u[0],
+            u[1]);
       u[0] = attn_exp2(u[0]);
       u[1] = attn_exp2(u[1]);
       if (!s0) u[0] = 0.0f;
