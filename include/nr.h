@@ -469,7 +469,7 @@ nr_status nr_group_norm_workspace(int64_t samples, int64_t space, int64_t channe
  *                        aligned to an element (rows need no 16 bytes).
  * tokens                 [rows] int64 (8-byte aligned).
  * vocab in [1, 2^31), stride >= vocab, top in [0, min(32, vocab)].
- * inv_temperature        finite, > 0.
+ * inv_temperature        in [2^-90, 2^127].
  * Errors: as nr_rmsnorm.
  */
 nr_status nr_token_logprobs(float* logprob, float* entropy, float* lse, float* top_logprob,

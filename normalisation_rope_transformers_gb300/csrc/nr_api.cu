@@ -963,8 +963,9 @@ nr_status check_logits(const char* fn, int64_t rows, int64_t vocab, int64_t stri
   const int64_t per_row = vocab / 4096 + 1;
   if (rows > INT32_MAX / (per_row > 8 ? per_row : 8))
     return fail(NR_ERR_SHAPE, "%s: too many rows for one launch", fn);
-  if (!(isfinite(inv_t) && inv_t > 0.0f))
-    return fail(NR_ERR_VALUE, "%s: inv_temperature must be finite and > 0", fn);
+  // log2(e) times it is finite, and a logit 1e30 below another's has no probability
+  if (!(inv_t >= 0x1p-90f && inv_t <= 0x1p127f))
+    return fail(NR_ERR_VALUE, "%s: inv_temperature must be in [2^-90, 2^127]", fn);
   return NR_OK;
 }
 
