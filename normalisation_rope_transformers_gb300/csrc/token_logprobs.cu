@@ -567,8 +567,10 @@ struct GradRow {
     const F2 lp = fma2(x, inv_t, neg_lse);
     float u[2];
     split(lp, u[0], u[1]);
-    u[0] = fmaxf(u[0], -1e30f);  // a masked logit: p = 0, and 0 * -inf would be a NaN
-    u[1] = fmaxf(u[1], -1e30f);
+    // p = 0 far above this; a masked logit's 0 * -inf would be a NaN, and 0 times what leaves f32's
+    // range with a large gradient of the entropy too
+    u[0] = fmaxf(u[0], -1e3f);
+    u[1] = fmaxf(u[1], -1e3f);
     const F2 p = f2(exp2_fast(u[0] * kLog2e), exp2_fast(u[1] * kLog2e));
     return mul2(p, fma2(b, f2(u[0], u[1]), a));
   }
