@@ -860,8 +860,8 @@ def token_logprobs(logits, tokens, top=0, temperature=1.0):
     """Log softmax of logits [rows, vocab] (rows may be strided) / temperature at tokens
     [rows] int64 (outside the vocabulary: padding, 0), the entropy of each row, its log sum
     of exponentials, and the `top` largest alternatives (at most 32; equal logits by the
-    lower index).  temperature is in [2^-127, 2^90].  Returns a TokenLogprobs.  No autograd graph is recorded: the gradient
-    is token_logprobs_backward."""
+    lower index).  temperature is in [2^-127, 2^90].  Returns a TokenLogprobs.  No autograd
+    graph is recorded: the gradient is token_logprobs_backward."""
     top, inv_t = int(top), _inv_temperature(temperature)
     key, known = _known("logprobs", (top, inv_t), (logits, tokens))
     if known is None:
