@@ -788,15 +788,18 @@ int64_t cache_attention_workspace(int64_t head_dim) {
   return few > many ? few : many;
 }
 
+// Query rows a sequence and head of the cache, on average, that the kernel for few rows takes where there
+// is one for many: three tiles.  (24 rows of one token, heads of 128 in FP8, 100009 tokens in 16 sequences:
+// 87 us here, 105 there; here every 24 more take as long again.)
+constexpr int64_t kFewRows = 24;
+
 cudaError_t launch_cache_attention(const KvCacheArgs& c, const CacheAttentionArgs& p, int is_bf16,
                                    cudaStream_t stream) {
   const AttnArgs a = attn_args(c, p);
-  // Query rows a sequence and head of the cache on average (what each has is known on the device alone).
-  // More than 24: the kernel whose tile of products has 128 (24 rows of one token, heads of 128 in
-  // FP8, 100009 tokens in 16 sequences: 105 us there, 87 here; here every 24 more take as long again).
+  // (what each sequence has is known on the device alone)
   const int64_t average = (p.tokens * (p.q_heads / c.heads) + p.seqs - 1) / p.seqs;
   const bool even = p.tokens % p.seqs == 0;
-  if (is_bf16 && c.head_dim <= 128 && average > 24)
+  if (is_bf16 && c.head_dim <= 128 && average > kFewRows)
     return launch_attn_rows(a, c.fp4, c.head_dim, p.workspace, stream);
   if (is_bf16)
     return c.fp4 ? attn_few<__nv_bfloat16, true>(average, even, c.head_dim, a, p.workspace, stream)
