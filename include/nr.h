@@ -373,15 +373,17 @@ nr_status nr_kv_cache_read(void* k_out, void* v_out, const nr_kv_cache* cache,
  * tree         [tokens, tree_words] int32; NULL with tree_words = 0.  Words past a sequence's T
  *              tokens are ignored; new tokens past the words are not seen.
  * All tables are device memory.  q_heads is a multiple of the cache's heads; head_dim is 64, 128
- * or 256; tokens * q_heads < 2^31; scale is finite.
+ * or 256; tokens * q_heads < 2^31; |scale| is at most 2^127, and finite times any element of q.
  * workspace    as nr_group_norm, of at least nr_cache_attention_workspace bytes.
  * Sums are formed in a fixed order (the same inputs give the same bits).  Scores, weights and sums
- * are f32.  A weight times its token's V scale (MXFP4: its head row's largest) is rounded for the
- * product with V to f16's 11 bits (bf16 tensors) or held in 22 (f32 tensors), and is off by up to
- * 2^-32 of the row's largest such product, or of 2^-104 where that is larger.  Weights below
- * 2^-118 of the row's largest may count as zero.  FP8 scales may have either sign.  Sums of
- * weights (up to 2^8 each) times V have to stay in f32's range.  MXFP4 elements below 2^-37 of
- * their head row's largest scale count as zero.
+ * are f32.  q goes into the scores with all its bits (bf16 tensors; elements down to 2^-31 of their
+ * head row's largest) or 22 (f32 tensors; down to 2^-17).  A weight times its token's V scale
+ * (MXFP4: its head row's largest) is rounded for the product with V to f16's 11 bits (bf16
+ * tensors) or held in 22 (f32 tensors), and is off by up to 2^-32 of the row's largest such
+ * product, or of 2^-104 where that is larger.  Weights below 2^-118 of the row's largest may count
+ * as zero.  FP8 scales may have either sign.  Sums of weights (up to 2^8 each) times V have to
+ * stay in f32's range.  MXFP4 elements below 2^-37 of their head row's largest scale count as
+ * zero, and so do head rows with no scale above 2^-114.
  * Errors: as nr_rmsnorm; a workspace that is too small is NR_ERR_SHAPE.
  */
 nr_status nr_cache_attention(void* out, float* lse, const void* q, const nr_kv_cache* cache,

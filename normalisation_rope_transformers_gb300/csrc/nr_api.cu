@@ -1087,7 +1087,8 @@ nr_status nr_cache_attention(void* out, float* lse, const void* q, const nr_kv_c
   if (!cu_q && tokens != seqs)
     return fail(NR_ERR_SHAPE, "%s: without cu_q there is one query a sequence (%lld, %lld)", fn,
                 (long long)tokens, (long long)seqs);
-  if (!isfinite(scale)) return fail(NR_ERR_VALUE, "%s: scale must be finite", fn);
+  if (!(fabsf(scale) <= 0x1p127f))  // times log2(e) it is finite
+    return fail(NR_ERR_VALUE, "%s: scale must be finite, at most 2^127", fn);
   if (empty) return ok();
   if ((tree != nullptr) != (tree_words > 0))
     return fail(NR_ERR_NULL, "%s: tree is given exactly when tree_words > 0", fn);
