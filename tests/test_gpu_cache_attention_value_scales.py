@@ -13,8 +13,8 @@ pytestmark = pytest.mark.gpu
 bf = torch.bfloat16
 
 
-def close(got, p, scale):
-    """Compare with 64 bits.  Roundings, u = 2^-24 f32's half step: a score is a sum of dim products in
+def close(got, p, scale, heads_at=slice(None)):
+    """Compare with 64 bits (some query heads of each token).  Roundings, u = 2^-24 f32's half step: a score is a sum of dim products in
     dim / 16 steps, two units each, and is multiplied by two factors, so e_p = (dim / 8 + 16) u mag_p with
     mag_p = scale sum |q k_p| (f32 tensors: Q in 22 bits, four units more); its weight has that relative
     error and 2^-21 of the exponential, and is rounded for the product (2^-11, or 2^-22 in two
@@ -35,7 +35,7 @@ def close(got, p, scale):
         at = table[i, at // page], at % page
         for t in range(cu[i + 1] - cu[i]):
             see = ref.sees(n, cu[i + 1] - cu[i], t, None if tree is None else tree[cu[i] + t])
-            for h in range(q.shape[1]):
+            for h in range(q.shape[1])[heads_at]:
                 kk, vv, ss = (x[at][see, h // group] for x in (k, v, np.abs(s)))
                 qq = q[cu[i] + t, h]
                 score = scale * (kk @ qq)
@@ -136,3 +136,22 @@ def test_scales_near_the_ends_of_the_range(nr, exponent, dtype, rows):
     p["parts"][1] = rng.choice(np.array(codes, np.uint8), p["parts"][1].shape)
     p["parts"][3] = (2.0 ** exponent * rng.uniform(1, 2, p["parts"][3].shape)).astype(np.float32)
     close(run(nr, p), p, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("scores,values,dim", [
+    (300, 0, 64), (-300, 0, 128), (300, 60, 128), (300, -60, 64), (-40, 100, 64), (0, 100, 128),
+    (0, -100, 64), (40, -100, 128)])
+def test_references_that_move_from_tile_to_tile(nr, scores, values, dim):
+    """Sequences so long that a block walks many tiles of each: scores that move by `scores` along them
+    and V's scales by 2^values, with normal values on top of both."""
+    lens, queries, group = [5000, 4100, 3000], [14, 20, 13], 2
+    p = problem(dim, lens, queries, 8, group, dim, 64, "fp8", bf)
+    rng = np.random.default_rng(7)
+    for i, n in enumerate(lens):
+        pos = np.arange(n)
+        at = p["table"][i, pos // 64], pos % 64
+        k = rng.standard_normal((n, 8, dim)) + (pos / n * scores / dim ** 0.5)[:, None, None]
+        p["parts"][0][at], p["parts"][2][at] = cache_ref.quant(k.astype(np.float32), "fp8")
+        p["parts"][3][at] *= (2.0 ** np.round((pos / n - 0.5) * values)).astype(np.float32)[:, None]
+    p["q"] = torch.ones_like(p["q"]) + 0.1 * p["q"]  # the scores' drift is that of their sum
+    close(run(nr, p), p, dim ** -0.5, slice(None, None, 5))
