@@ -617,9 +617,10 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     each).  A query sees every earlier token, itself, and of its sequence's other new
     tokens those in front of it, or with `tree` [tokens, words] int32 those whose bit is set
     (bit j % 32 of word j / 32 for the j-th new token; a token's own bit included).  `scale`
-    is 1 / sqrt(head_dim) if not given.  A query that sees nothing gets zeros.  Returns out
-    [tokens, q_heads, head_dim], or (out, lse) with the float32 [tokens, q_heads] log sums of
-    exponentials."""
+    is 1 / sqrt(head_dim) if not given.  A query that sees nothing gets zeros.  Rows of no
+    sequence (outside [cu_q[0], cu_q[seqs]), or all if there are no sequences) are left as they
+    were: what a fresh out and lse hold there is not defined.  Returns out [tokens, q_heads,
+    head_dim], or (out, lse) with the float32 [tokens, q_heads] log sums of exponentials."""
     if scale is not None:
         scale = float(scale)
     return_lse = bool(return_lse)

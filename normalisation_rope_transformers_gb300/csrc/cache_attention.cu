@@ -20,10 +20,10 @@
 // the positions is as long: shares that end inside a sequence leave parts that a second kernel joins.
 //
 // Measured: one token of 48 sequences with 400009 cached tokens, 32 query and 8 cache heads of 128 in
-// FP8: 154 us, 0.81 of the copy rate, bound by what 12 warps an SM have under way (168 registers).
-// Up to 5 tokens of 29 sequences with 150001, 24 and 6 heads, MXFP4: 85 us, 0.21 of it, bound by
-// instructions (53% of the issue slots; widening a code costs as much as FP8's twice as many bytes).
-// One sequence of 1501 tokens: 10.6 us, latency: two launches, a plan, one step, joining.
+// FP8: 152 us, 0.82 of the copy rate, bound by what 12 warps an SM have under way (168 registers).
+// Up to 5 tokens of 29 sequences with 150001, 24 and 6 heads, MXFP4: 89 us, 0.20 of it, bound by
+// instructions (52% of the issue slots; widening a code costs as much as FP8's twice as many bytes).
+// One sequence of 1501 tokens: 10.7 us, latency: two launches, a plan, one step, joining.
 #include <type_traits>
 
 #include "attn_plan.cuh"
@@ -38,7 +38,7 @@ namespace {
 template <bool FP4, int DIM, int NT>
 constexpr int kSub = DIM == 256 || (NT == 3 && DIM == 128 && !FP4) ? 1 : 2;
 // A share for each block that fits at once on 152 SMs (any number is right).
-// (Heads of 64, one token, 300009 positions in 48 sequences: four blocks an SM instead of three 97 -> 96
+// (32 query and 8 cache heads of 64, one token, 300009 positions in 48 sequences: four blocks an SM instead of three 97 -> 96
 // us in FP8, 93 -> 85 in MXFP4; heads of 128 in MXFP4 124 with four, 122 with three.)
 template <int DIM, int NT>
 constexpr int attn_blocks = DIM == 256 || NT > 1 ? 2 : DIM == 64 ? 4 : 3;

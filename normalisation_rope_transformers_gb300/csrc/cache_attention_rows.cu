@@ -13,13 +13,13 @@
 // score, and its largest weight times V scale) move only when a tile's weights sum to more than 2^8 or
 // one of them times its V scale leaves f16's range, 2^6.5 above what the largest is held at or more;
 // then the warp multiplies its rows of O.  So a tile's weights are taken with the references that are
-// there, and once more where these have to move (a pass of its own for the maximum in each tile: 131 us
-// where this takes 121).
+// there, and once more where these have to move (a pass of its own for the maximum in each tile took 131 us
+// where one pass took 121).
 //
 // What bounds it: the products take 1076 cycles a tile (D = 128), the operands 160 KB of shared
 // memory a tile (1250 cycles).  The softmax's warps are alone on their schedulers and wait for their own
 // results most of the time: that is what a tile takes now, about twice the products.  Trees of up to 61
-// tokens of 6 sequences with 60013 cached tokens, 32 query and 8 cache heads of 128 in FP8: 121 us, 475
+// tokens of 6 sequences with 60013 cached tokens, 32 query and 8 cache heads of 128 in FP8: 124 us, 467
 // TFLOP/s (mma.sync, 16 rows an item: 790 us).
 #include "attn_plan.cuh"
 #include "nr_internal.h"
