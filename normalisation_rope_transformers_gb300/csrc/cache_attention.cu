@@ -38,8 +38,8 @@ namespace {
 template <bool FP4, int DIM, int NT>
 constexpr int kSub = DIM == 256 || (NT == 3 && DIM == 128 && !FP4) ? 1 : 2;
 // A share for each block that fits at once on 152 SMs (any number is right).
-// (32 query and 8 cache heads of 64, one token, 300009 positions in 48 sequences: four blocks an SM instead of three 97 -> 96
-// us in FP8, 93 -> 85 in MXFP4; heads of 128 in MXFP4 124 with four, 122 with three.)
+// (32 query and 8 cache heads of 64, one token, 300009 positions in 48 sequences: four blocks an SM instead
+// of three 97 -> 96 us in FP8, 93 -> 85 in MXFP4; heads of 128 in MXFP4 124 with four, 122 with three.)
 template <int DIM, int NT>
 constexpr int attn_blocks = DIM == 256 || NT > 1 ? 2 : DIM == 64 ? 4 : 3;
 constexpr int kSms = 152;
@@ -48,7 +48,7 @@ constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = kAttnThreads / kWarp;
 constexpr int kItemCost = 3;  // tiles that an item costs besides its own
 constexpr float kSlack = 4.0f;  // a row's reference is behind its maximum by up to 2^4,
-constexpr int kHold = 11;       // and what it holds for f16 behind its largest: 2^11.5 to 2^15.5
+constexpr int kHold = 11;       // and what it holds for f16 starts between 2^9.5 and 2^11.5, up to 2^15.5
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
